@@ -25,6 +25,11 @@ FQ_OUTER_NONE, FQ_OUTER_TENSOR, FQ_OUTER_BLOCK128 = 0, 1, 2
 FQ_ROUND_RNE, FQ_ROUND_SR = 0, 1
 FQ_AXIS_ROW, FQ_AXIS_COL = 0, 1
 FQ_OSCI_BIN_CENTRE, FQ_OSCI_GRID_VALUE = 0, 1
+FQ_F8_NONE, FQ_F8_MX, FQ_F8_ROW = 0, 1, 2
+FQ_TYPE_BF16, FQ_TYPE_F32 = 0, 1
+FQ_STATE_F32, FQ_STATE_F8 = 0, 1
+FQ_MOE_MAX_K, FQ_MOE_MAX_ALIGN = 64, 1024
+STATE_BLOCK = 128                 # elements under one scale of an 8-bit AdamW state
 
 # every symbol include/fq.h declares
 EXPORTED = (
@@ -35,7 +40,9 @@ EXPORTED = (
     "fq_qlinear_workspace_size", "fq_qlinear_fwd", "fq_hadamard",
     "fq_qlinear_bwd_workspace_size", "fq_qlinear_bwd", "fq_status_string",
     "fq_last_error", "fq_version", "fq_fake_quant_noalloc", "fq_qlinear_fwd_retain",
-    "fq_qlinear_bwd_retain",
+    "fq_qlinear_bwd_retain", "fq_rmsnorm_fwd", "fq_rmsnorm_bwd_workspace_size",
+    "fq_rmsnorm_bwd", "fq_moe_rows", "fq_moe_sort_workspace_size", "fq_moe_sort",
+    "fq_moe_dispatch", "fq_moe_combine", "fq_moe_combine_bwd", "fq_adamw_step",
 )
 
 
@@ -54,6 +61,37 @@ class FqDesc(ctypes.Structure):
         return (f"FqDesc(block_size={self.block_size}, scale_type={self.scale_type}, "
                 f"outer={self.outer}, rounding={self.rounding}, axis={self.axis}, "
                 f"seed={self.seed})")
+
+
+class FqAdamWTensor(ctypes.Structure):
+    _fields_ = [
+        ("w", ctypes.c_void_p),
+        ("w_bf16", ctypes.c_void_p),
+        ("g", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("g_type", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("lr_mult", ctypes.c_float),
+        ("weight_decay", ctypes.c_float),
+    ]
+
+
+class FqAdamWHyper(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("step", ctypes.c_int64),
+        ("seed", ctypes.c_uint64),
+        ("grad_scale", ctypes.c_void_p),
+        ("state_type", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
 
 
 class FqError(RuntimeError):
@@ -129,6 +167,29 @@ def lib() -> ctypes.CDLL:
         L.fq_qlinear_bwd_retain.argtypes = [dp, dp, dp, vp, vp, vp, i64, i64, i64, vp, vp, vp, vp,
                                             vp, sz, vp]
         L.fq_qlinear_bwd_retain.restype = ctypes.c_int
+        L.fq_rmsnorm_fwd.argtypes = [vp, vp, i32, vp, i32, f32, i64, i64, i32, vp, vp, vp, vp, vp,
+                                     vp]
+        L.fq_rmsnorm_fwd.restype = ctypes.c_int
+        L.fq_rmsnorm_bwd_workspace_size.argtypes = [i64, i64]
+        L.fq_rmsnorm_bwd_workspace_size.restype = sz
+        L.fq_rmsnorm_bwd.argtypes = [vp, vp, i32, vp, i32, vp, vp, i64, i64, vp, vp, vp, vp, sz,
+                                     vp]
+        L.fq_rmsnorm_bwd.restype = ctypes.c_int
+        L.fq_moe_rows.argtypes = [i64, i64, i64, i64]
+        L.fq_moe_rows.restype = i64
+        L.fq_moe_sort_workspace_size.argtypes = [i64, i64, i64]
+        L.fq_moe_sort_workspace_size.restype = sz
+        L.fq_moe_sort.argtypes = [vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, sz, vp]
+        L.fq_moe_sort.restype = ctypes.c_int
+        L.fq_moe_dispatch.argtypes = [vp, i32, vp, i64, i64, i64, i64, vp, vp, vp, vp]
+        L.fq_moe_dispatch.restype = ctypes.c_int
+        L.fq_moe_combine.argtypes = [vp, vp, i64, i64, i64, i64, vp, vp, vp]
+        L.fq_moe_combine.restype = ctypes.c_int
+        L.fq_moe_combine_bwd.argtypes = [vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp]
+        L.fq_moe_combine_bwd.restype = ctypes.c_int
+        L.fq_adamw_step.argtypes = [ctypes.POINTER(FqAdamWHyper), ctypes.POINTER(FqAdamWTensor),
+                                    i64, vp]
+        L.fq_adamw_step.restype = ctypes.c_int
         L.fq_status_string.argtypes = [ctypes.c_int]
         L.fq_status_string.restype = ctypes.c_char_p
         L.fq_last_error.argtypes = []
@@ -591,6 +652,287 @@ def fq_qlinear_bwd_retain(desc_x: FqDesc, desc_w: FqDesc, desc_g: FqDesc, x, w, 
                                        _bf16(dx, M, K, "dx"), _bf16(dw, K, N, "dw"),
                                        _ptr(ws, None, "ws", elem=1), ws.numel(), _stream(stream)))
     return dx, dw
+
+
+# ---------------------------------------------------------------------------
+# around the linears: norm, expert sorting, optimizer
+# ---------------------------------------------------------------------------
+
+def _type_of(t, name: str) -> int:
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return FQ_TYPE_BF16
+    if t.dtype == torch.float32:
+        return FQ_TYPE_F32
+    raise ValueError(f"{name} must be bfloat16 or float32, not {t.dtype}")
+
+
+def _typed(t, dtype, n: int, name: str):
+    """Pointer of an optional operand of exactly this dtype, `n` elements at least."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    return _ptr(t, n * t.element_size(), name)
+
+
+def _scales8(scales, f8: int, rows: int, cols: int):
+    """Pointer of the scales of 8-bit rows."""
+    if scales is None or f8 == FQ_F8_NONE:
+        return _ptr(scales, None, "scales")
+    if f8 == FQ_F8_MX:
+        return _ptr(scales, rows * (cols // 32), "scales", elem=1)
+    return _typed(scales, _torch().float32, rows, "scales")
+
+
+def fq_rmsnorm_fwd(x, gamma, eps: float, res=None, f8: int = FQ_F8_NONE, h=None, y=None,
+                   codes=None, scales=None, rstd=None, stream=None):
+    """Residual addition and root-mean-square norm of x BF16 [rows, cols].
+
+    With a residual `res` (BF16 or FP32, the stream) h = x + res in its type;
+    h may be res itself.  f8=FQ_F8_NONE writes y (BF16); otherwise codes (E4M3,
+    uint8) and scales, and y only if given (the values they stand for).  rstd
+    (FP32 [rows], for the backward) is written if given.  Returns (h, y) without
+    f8 and (h, codes, scales) with it; h is None without a residual."""
+    torch = _torch()
+    rows, cols = x.shape
+    stream_type = FQ_TYPE_BF16
+    if res is not None:
+        stream_type = _type_of(res, "res")
+        if h is None:
+            h = torch.empty_like(res)
+    if f8 == FQ_F8_NONE:
+        if y is None:
+            y = torch.empty_like(x)
+    elif codes is None or scales is None:
+        if codes is None:
+            codes = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        if scales is None:
+            scales = (torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
+                      if f8 == FQ_F8_MX else
+                      torch.empty(rows, dtype=torch.float32, device=x.device))
+    n = rows * cols
+    _check(lib().fq_rmsnorm_fwd(
+        _typed(x, torch.bfloat16, n, "x"),
+        None if res is None else _ptr(res, n * res.element_size(), "res"), stream_type,
+        _ptr(gamma, cols * gamma.element_size(), "gamma"), _type_of(gamma, "gamma"), eps, rows,
+        cols, f8, None if h is None else _typed(h, (x if res is None else res).dtype, n, "h"),
+        _typed(y, torch.bfloat16, n, "y"), _ptr(codes, n, "codes", elem=1),
+        _scales8(scales, f8, rows, cols), _typed(rstd, torch.float32, rows, "rstd"),
+        _stream(stream)))
+    return (h, y) if f8 == FQ_F8_NONE else (h, codes, scales)
+
+
+def rmsnorm_bwd_workspace(rows: int, cols: int, device):
+    torch = _torch()
+    n = lib().fq_rmsnorm_bwd_workspace_size(rows, cols)
+    return torch.empty((n,), dtype=torch.uint8, device=device)
+
+
+def fq_rmsnorm_bwd(dy, h, gamma, rstd, dres=None, dh=None, dx=None, dgamma=None, ws=None,
+                   need_dgamma: bool = True, stream=None):
+    """(dh, dgamma) of the norm of h (the forward's h, or its x without a
+    residual) for the gradient dy of its output; dres is added to dh (and may
+    be dh).  dx, if given, receives dh in BF16 beside an FP32 stream.
+    need_dgamma=False leaves dgamma out (None)."""
+    torch = _torch()
+    rows, cols = dy.shape
+    n = rows * cols
+    if dh is None:
+        dh = torch.empty_like(h)
+    if not need_dgamma:
+        dgamma, ws, nbytes = None, None, 0
+    else:
+        if dgamma is None:
+            dgamma = torch.empty(cols, dtype=torch.float32, device=dy.device)
+        if ws is None:
+            ws = rmsnorm_bwd_workspace(rows, cols, dy.device)
+        nbytes = ws.numel() * ws.element_size()
+    _check(lib().fq_rmsnorm_bwd(
+        _typed(dy, torch.bfloat16, n, "dy"), _ptr(h, n * h.element_size(), "h"),
+        _type_of(h, "h"), _ptr(gamma, cols * gamma.element_size(), "gamma"),
+        _type_of(gamma, "gamma"), _typed(rstd, torch.float32, rows, "rstd"),
+        _typed(dres, h.dtype, n, "dres"), rows, cols, _typed(dh, h.dtype, n, "dh"),
+        _typed(dx, torch.bfloat16, n, "dx"), _typed(dgamma, torch.float32, cols, "dgamma"),
+        _ptr(ws, None, "ws"), nbytes, _stream(stream)))
+    return dh, dgamma
+
+
+@dataclass
+class MoeSorted:
+    """Where the assignments are in the sorted order: int32 offsets [experts + 1],
+    pos [tokens, k] and src [rows]."""
+    offsets: "object"
+    pos: "object"
+    src: "object"
+
+
+def moe_rows(tokens: int, k: int, experts: int, align: int = 1) -> int:
+    """Rows of the sorted order's buffers (what its segments take at most)."""
+    n = lib().fq_moe_rows(tokens, k, experts, align)
+    if n == 0:
+        _check(FQ_ERR_SHAPE)
+    return n
+
+
+def moe_sort_workspace(tokens: int, k: int, experts: int, device):
+    torch = _torch()
+    n = lib().fq_moe_sort_workspace_size(tokens, k, experts)
+    return torch.empty((n,), dtype=torch.uint8, device=device)
+
+
+def fq_moe_sort(experts_of, experts: int, align: int = 1, out: MoeSorted | None = None, ws=None,
+                stream=None) -> MoeSorted:
+    """Sort the assignments experts_of (int32 [tokens, k]) by expert, each
+    expert's segment padded to a multiple of `align` rows."""
+    torch = _torch()
+    tokens, k = experts_of.shape
+    if out is None:
+        dev = experts_of.device
+        out = MoeSorted(torch.empty(experts + 1, dtype=torch.int32, device=dev),
+                        torch.empty((tokens, k), dtype=torch.int32, device=dev),
+                        torch.empty(moe_rows(tokens, k, experts, align), dtype=torch.int32,
+                                    device=dev))
+    if ws is None:
+        ws = moe_sort_workspace(tokens, k, experts, experts_of.device)
+    nbytes = ws.numel() * ws.element_size()
+    i32, rows = torch.int32, out.src.numel()
+    _check(lib().fq_moe_sort(
+        _typed(experts_of, i32, tokens * k, "experts_of"), tokens, k, experts, align, rows,
+        _typed(out.offsets, i32, experts + 1, "offsets"), _typed(out.pos, i32, tokens * k, "pos"),
+        _typed(out.src, i32, rows, "src"), _ptr(ws, None, "ws") if nbytes else None, nbytes,
+        _stream(stream)))
+    return out
+
+
+def _sorted_ptrs(q: MoeSorted):
+    torch = _torch()
+    tokens, k = q.pos.shape
+    return (tokens, k, q.src.numel(), _typed(q.pos, torch.int32, tokens * k, "pos"),
+            _typed(q.src, torch.int32, 0, "src"))
+
+
+def fq_moe_dispatch(x, q: MoeSorted, f8: int = FQ_F8_NONE, scales=None, y=None, stream=None):
+    """Rows of the tokens in the sorted order (BF16 [rows, cols], 0 in padding):
+    x BF16 [tokens, cols], or the codes of 8-bit rows with their scales."""
+    torch = _torch()
+    tokens, k, rows, pos, src = _sorted_ptrs(q)
+    if x.shape[0] != tokens:
+        raise ValueError(f"x has {x.shape[0]} rows, {tokens} tokens were sorted")
+    cols = x.shape[1]
+    if y is None:
+        y = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device)
+    xp = (_typed(x, torch.bfloat16, tokens * cols, "x") if f8 == FQ_F8_NONE
+          else _ptr(x, tokens * cols, "x", elem=1))
+    _check(lib().fq_moe_dispatch(xp, f8, _scales8(scales, f8, tokens, cols), tokens, k, cols, rows,
+                                 pos, src, _typed(y, torch.bfloat16, rows * cols, "y"),
+                                 _stream(stream)))
+    return y
+
+
+def fq_moe_combine(y, q: MoeSorted, weights=None, out=None, stream=None):
+    """out[t] = sum_j weights[t, j] * y[row of (t, j)] (weights None: ones, the
+    backward of fq_moe_dispatch)."""
+    torch = _torch()
+    tokens, k, rows, pos, _ = _sorted_ptrs(q)
+    cols = y.shape[1]
+    if out is None:
+        out = torch.empty((tokens, cols), dtype=torch.bfloat16, device=y.device)
+    _check(lib().fq_moe_combine(_typed(y, torch.bfloat16, rows * cols, "y"),
+                                _typed(weights, torch.float32, tokens * k, "weights"), tokens, k,
+                                cols, rows, pos,
+                                _typed(out, torch.bfloat16, tokens * cols, "out"),
+                                _stream(stream)))
+    return out
+
+
+def fq_moe_combine_bwd(dout, y, q: MoeSorted, weights, dy=None, dweights=None, stream=None):
+    """(dy [rows, cols] BF16, dweights [tokens, k] FP32) of fq_moe_combine."""
+    torch = _torch()
+    tokens, k, rows, pos, src = _sorted_ptrs(q)
+    cols = dout.shape[1]
+    if dy is None:
+        dy = torch.empty((rows, cols), dtype=torch.bfloat16, device=dout.device)
+    if dweights is None:
+        dweights = torch.empty((tokens, k), dtype=torch.float32, device=dout.device)
+    _check(lib().fq_moe_combine_bwd(
+        _typed(dout, torch.bfloat16, tokens * cols, "dout"),
+        _typed(y, torch.bfloat16, rows * cols, "y"),
+        _typed(weights, torch.float32, tokens * k, "weights"), tokens, k, cols, rows, pos, src,
+        _typed(dy, torch.bfloat16, rows * cols, "dy"),
+        _typed(dweights, torch.float32, tokens * k, "dweights"), _stream(stream)))
+    return dy, dweights
+
+
+@dataclass
+class AdamWTensor:
+    """One tensor of an AdamW step: FP32 master w, gradient g (BF16 or FP32),
+    moments m and v (FP32, or uint8 codes with m_scale and v_scale), and the
+    BF16 copy of w that the linears read (may be None)."""
+    w: "object"
+    g: "object"
+    m: "object"
+    v: "object"
+    w_bf16: "object" = None
+    m_scale: "object" = None
+    v_scale: "object" = None
+    weight_decay: float = 0.0
+    lr_mult: float = 1.0
+
+
+def adamw_state(n: int, device, f8: bool = False) -> dict:
+    """Moments of n elements before the first step (keywords of AdamWTensor)."""
+    torch = _torch()
+    dtype = torch.uint8 if f8 else torch.float32
+    st = {k: torch.zeros(n, dtype=dtype, device=device) for k in ("m", "v")}
+    if f8:
+        for k in ("m_scale", "v_scale"):
+            st[k] = torch.zeros(-(-n // STATE_BLOCK), dtype=torch.float32, device=device)
+    return st
+
+
+class AdamWPlan:
+    """The tensors of an optimizer as the library takes them, checked once.  It
+    holds the tensors it was made from; their contents may change between
+    steps, the tensors may not."""
+
+    def __init__(self, tensors):
+        torch = _torch()
+        self.tensors = list(tensors)
+        self.array = (FqAdamWTensor * len(self.tensors))()
+        self.f8 = bool(self.tensors) and self.tensors[0].m.dtype != torch.float32
+        self.hyper = FqAdamWHyper(state_type=FQ_STATE_F8 if self.f8 else FQ_STATE_F32)
+        for i, (s, t) in enumerate(zip(self.array, self.tensors)):
+            n, name = t.w.numel(), f"tensor {i}: "
+            s.n = n
+            s.w = _typed(t.w, torch.float32, n, name + "w")
+            s.w_bf16 = _typed(t.w_bf16, torch.bfloat16, n, name + "w_bf16")
+            s.g = _ptr(t.g, n * t.g.element_size(), name + "g")
+            s.g_type = _type_of(t.g, name + "g")
+            if self.f8:
+                blocks = -(-n // STATE_BLOCK)
+                s.m, s.v = _ptr(t.m, n, name + "m", elem=1), _ptr(t.v, n, name + "v", elem=1)
+                s.m_scale = _typed(t.m_scale, torch.float32, blocks, name + "m_scale")
+                s.v_scale = _typed(t.v_scale, torch.float32, blocks, name + "v_scale")
+            else:
+                s.m = _typed(t.m, torch.float32, n, name + "m")
+                s.v = _typed(t.v, torch.float32, n, name + "v")
+            s.lr_mult, s.weight_decay = t.lr_mult, t.weight_decay
+
+
+def adamw_plan(tensors) -> AdamWPlan:
+    return AdamWPlan(tensors)
+
+
+def fq_adamw_step(plan: AdamWPlan, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999,
+                  eps: float = 1e-8, grad_scale=None, seed: int = 0, stream=None):
+    """One AdamW step (in place) over a plan's tensors.  step counts from 1;
+    grad_scale is an FP32 device scalar the gradients are multiplied by; seed
+    keys the stochastic rounding of 8-bit moments."""
+    h = plan.hyper
+    h.lr, h.beta1, h.beta2, h.eps, h.step, h.seed = lr, beta1, beta2, eps, step, seed
+    h.grad_scale = _typed(grad_scale, _torch().float32, 1, "grad_scale")
+    _check(lib().fq_adamw_step(ctypes.byref(h), plan.array, len(plan.tensors), _stream(stream)))
 
 
 def version() -> str:

@@ -21,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfq.so")
 
-SOURCES = ["fq_api.cpp", "fq_kernels.hip", "fq_gemm.hip", "fq_hadamard.hip", "fq_outcontrol.hip"]
+SOURCES = ["fq_api.cpp", "fq_kernels.hip", "fq_gemm.hip", "fq_hadamard.hip", "fq_outcontrol.hip",
+           "fq_norm.hip", "fq_moe.hip", "fq_adamw.hip"]
 ARCH = "gfx950"
 
 COMMON = [
@@ -59,7 +60,7 @@ def _compile(src: str, verbose: bool) -> str:
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
     # --no-undefined: a symbol missing from the sources fails here, not at load time
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,--no-undefined", *objs,

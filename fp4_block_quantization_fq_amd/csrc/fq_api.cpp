@@ -6,6 +6,7 @@
 // reported as FQ_ERR_DEVICE.  No exception crosses the boundary.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -1057,6 +1058,377 @@ fq_status fq_fake_quant_retain(const fq_desc *desc, const void *x_bf16, int64_t 
                             scales, outer, nullptr, retain, chan_scale, (uint32_t *)ws,
                             (hipStream_t)stream, false);
 }
+
+}  // extern "C"
+
+// ---- row operators around the quantized linears ------------------------------
+namespace {
+
+fq_status check_type(int32_t type, const char *name)
+{
+    if (type != FQ_TYPE_BF16 && type != FQ_TYPE_F32)
+        return fail(FQ_ERR_DESC, "%s=%d is not FQ_TYPE_BF16/F32", name, type);
+    return FQ_OK;
+}
+
+fq_status check_f8(int32_t f8)
+{
+    if (f8 != FQ_F8_NONE && f8 != FQ_F8_MX && f8 != FQ_F8_ROW)
+        return fail(FQ_ERR_DESC, "f8=%d is not FQ_F8_NONE/MX/ROW", f8);
+    return FQ_OK;
+}
+
+fq_status check_norm_shape(int64_t rows, int64_t cols)
+{
+    if (rows < 1 || cols < 1)
+        return fail(FQ_ERR_SHAPE, "rows=%lld cols=%lld must be >= 1", (long long)rows,
+                    (long long)cols);
+    if (cols > fqimpl::kNormMaxCols)
+        return fail(FQ_ERR_SHAPE, "cols=%lld must be at most %lld", (long long)cols,
+                    (long long)fqimpl::kNormMaxCols);
+    if (rows > kMaxDim || rows * cols > kMaxElems)
+        return fail(FQ_ERR_SHAPE, "rows=%lld must be below 2^31 and rows*cols at most 2^34",
+                    (long long)rows);
+    return FQ_OK;
+}
+
+// T, k, E of the expert sort
+fq_status check_moe(int64_t T, int64_t k, int64_t E)
+{
+    if (T < 1 || k < 1 || E < 1)
+        return fail(FQ_ERR_SHAPE, "tokens=%lld k=%lld experts=%lld must be >= 1", (long long)T,
+                    (long long)k, (long long)E);
+    if (k > FQ_MOE_MAX_K || E > fqimpl::kMoeMaxExperts)
+        return fail(FQ_ERR_SHAPE, "k=%lld must be at most %d, experts=%lld at most %d",
+                    (long long)k, FQ_MOE_MAX_K, (long long)E, fqimpl::kMoeMaxExperts);
+    if (T > (int64_t(1) << 30) / k)
+        return fail(FQ_ERR_SHAPE, "tokens*k=%lld*%lld must be at most 2^30", (long long)T,
+                    (long long)k);
+    return FQ_OK;
+}
+
+fq_status check_moe_rows(int64_t T, int64_t k, int64_t H, int64_t rows, int64_t unit)
+{
+    FQ_TRY(check_moe(T, k, 1));
+    if (H < unit || H % unit != 0)
+        return fail(FQ_ERR_SHAPE, "cols=%lld must be a positive multiple of %lld", (long long)H,
+                    (long long)unit);
+    if (rows < 1 || rows > kMaxDim)
+        return fail(FQ_ERR_SHAPE, "rows=%lld must be >= 1 and below 2^31", (long long)rows);
+    if (H > kMaxElems / (rows > T ? rows : T))
+        return fail(FQ_ERR_SHAPE, "cols=%lld: rows*cols and tokens*cols must be at most 2^34",
+                    (long long)H);
+    return FQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fq_status fq_rmsnorm_fwd(const void *x_bf16, const void *res, int32_t stream_type,
+                         const void *gamma, int32_t gamma_type, float eps, int64_t rows,
+                         int64_t cols, int32_t f8, void *h, void *y_bf16, void *codes,
+                         void *scales, float *rstd, void *stream)
+{
+    FQ_TRY(check_type(stream_type, "stream_type"));
+    FQ_TRY(check_type(gamma_type, "gamma_type"));
+    FQ_TRY(check_f8(f8));
+    if (!(eps >= 0.0f)) return fail(FQ_ERR_DESC, "eps must be >= 0");
+    FQ_TRY(check_norm_shape(rows, cols));
+    if (f8 != FQ_F8_NONE && cols % 32 != 0)
+        return fail(FQ_ERR_SHAPE, "cols=%lld must be a multiple of 32 for an 8-bit output",
+                    (long long)cols);
+    FQ_TRY(check_ptr(x_bf16, "x", true));
+    FQ_TRY(check_ptr(gamma, "gamma", true));
+    FQ_TRY(check_ptr(res, "res", false));
+    FQ_TRY(check_ptr(h, "h", res != nullptr));
+    if (!res && h) return fail(FQ_ERR_DESC, "h is written only with a residual");
+    FQ_TRY(check_ptr(y_bf16, "y", f8 == FQ_F8_NONE));
+    FQ_TRY(check_ptr(codes, "codes", f8 != FQ_F8_NONE && !y_bf16));
+    if (f8 == FQ_F8_NONE && (codes || scales))
+        return fail(FQ_ERR_DESC, "codes and scales are written only for an 8-bit output");
+    FQ_TRY(check_ptr(scales, "scales", codes != nullptr));
+    FQ_TRY(check_ptr(rstd, "rstd", false, 4));
+    fqimpl::NormFwdArgs a;
+    a.x = x_bf16;
+    a.res = res;
+    a.stream_f32 = stream_type == FQ_TYPE_F32;
+    a.gamma = gamma;
+    a.gamma_f32 = gamma_type == FQ_TYPE_F32;
+    a.eps = eps;
+    a.rows = rows;
+    a.cols = cols;
+    a.f8 = f8;
+    a.h = h;
+    a.y = y_bf16;
+    a.codes = codes;
+    a.scales = scales;
+    a.rstd = rstd;
+    return device_status(fqimpl::launch_rmsnorm_fwd(a, (hipStream_t)stream), "norm launch");
+}
+
+size_t fq_rmsnorm_bwd_workspace_size(int64_t rows, int64_t cols)
+{
+    if (check_norm_shape(rows, cols) != FQ_OK) return 0;
+    return (size_t)fqimpl::rmsnorm_bwd_groups(rows, cols) * cols * sizeof(float);
+}
+
+fq_status fq_rmsnorm_bwd(const void *dy_bf16, const void *h, int32_t stream_type,
+                         const void *gamma, int32_t gamma_type, const float *rstd,
+                         const void *dres, int64_t rows, int64_t cols, void *dh, void *dx_bf16,
+                         float *dgamma, void *ws, size_t ws_bytes, void *stream)
+{
+    FQ_TRY(check_type(stream_type, "stream_type"));
+    FQ_TRY(check_type(gamma_type, "gamma_type"));
+    FQ_TRY(check_norm_shape(rows, cols));
+    FQ_TRY(check_ptr(dy_bf16, "dy", true));
+    FQ_TRY(check_ptr(h, "h", true));
+    FQ_TRY(check_ptr(gamma, "gamma", true));
+    FQ_TRY(check_ptr(rstd, "rstd", true, 4));
+    FQ_TRY(check_ptr(dres, "dres", false));
+    FQ_TRY(check_ptr(dh, "dh", true));
+    FQ_TRY(check_ptr(dx_bf16, "dx", false));
+    FQ_TRY(check_ptr(dgamma, "dgamma", false, 4));
+    if (dgamma) {
+        FQ_TRY(check_ptr(ws, "ws", true));
+        const size_t need = fq_rmsnorm_bwd_workspace_size(rows, cols);
+        if (ws_bytes < need)
+            return fail(FQ_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, need);
+    }
+    fqimpl::NormBwdArgs a;
+    a.dy = dy_bf16;
+    a.h = h;
+    a.stream_f32 = stream_type == FQ_TYPE_F32;
+    a.gamma = gamma;
+    a.gamma_f32 = gamma_type == FQ_TYPE_F32;
+    a.rstd = rstd;
+    a.dres = dres;
+    a.rows = rows;
+    a.cols = cols;
+    a.dh = dh;
+    a.dx = dx_bf16;
+    a.partials = (float *)ws;
+    a.groups = 0;
+    return device_status(fqimpl::launch_rmsnorm_bwd(a, dgamma, (hipStream_t)stream),
+                         "norm backward launch");
+}
+
+int64_t fq_moe_rows(int64_t tokens, int64_t k, int64_t experts, int64_t align)
+{
+    if (check_moe(tokens, k, experts) != FQ_OK) return 0;
+    if (align < 1 || align > FQ_MOE_MAX_ALIGN) {
+        fail(FQ_ERR_SHAPE, "align=%lld must be in [1, %d]", (long long)align, FQ_MOE_MAX_ALIGN);
+        return 0;
+    }
+    const int64_t n = tokens * k, used = experts < n ? experts : n;
+    return (n + used * (align - 1)) / align * align;
+}
+
+size_t fq_moe_sort_workspace_size(int64_t tokens, int64_t k, int64_t experts)
+{
+    if (check_moe(tokens, k, experts) != FQ_OK) return 0;
+    const int64_t n = tokens * k, chunk = fqimpl::moe_sort_chunk(n);
+    const int64_t chunks = (n + chunk - 1) / chunk;
+    return chunks > 1 ? (size_t)chunks * experts * sizeof(uint32_t) : 0;
+}
+
+fq_status fq_moe_sort(const int32_t *experts_of, int64_t tokens, int64_t k, int64_t experts,
+                      int64_t align, int64_t rows, int32_t *offsets, int32_t *pos, int32_t *src,
+                      void *ws, size_t ws_bytes, void *stream)
+{
+    const int64_t want = fq_moe_rows(tokens, k, experts, align);
+    if (!want) return FQ_ERR_SHAPE;
+    if (rows < want || rows > kMaxDim)
+        return fail(FQ_ERR_SHAPE, "rows=%lld must be at least fq_moe_rows = %lld and below 2^31",
+                    (long long)rows, (long long)want);
+    FQ_TRY(check_ptr(experts_of, "experts_of", true, 4));
+    FQ_TRY(check_ptr(offsets, "offsets", true, 4));
+    FQ_TRY(check_ptr(pos, "pos", true, 4));
+    FQ_TRY(check_ptr(src, "src", true, 4));
+    const size_t need = fq_moe_sort_workspace_size(tokens, k, experts);
+    if (need) {
+        FQ_TRY(check_ptr(ws, "ws", true));
+        if (ws_bytes < need)
+            return fail(FQ_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, need);
+    }
+    fqimpl::MoeSortArgs a;
+    a.ids = experts_of;
+    a.n = tokens * k;
+    a.E = (uint32_t)experts;
+    a.align = (uint32_t)align;
+    a.rows = rows;
+    a.offsets = offsets;
+    a.pos = pos;
+    a.src = src;
+    a.ws = (uint32_t *)ws;
+    a.chunk = 0;
+    return device_status(fqimpl::launch_moe_sort(a, (hipStream_t)stream), "expert sort launch");
+}
+
+fq_status fq_moe_dispatch(const void *x, int32_t f8, const void *scales, int64_t tokens,
+                          int64_t k, int64_t cols, int64_t rows, const int32_t *pos,
+                          const int32_t *src, void *y_bf16, void *stream)
+{
+    FQ_TRY(check_f8(f8));
+    FQ_TRY(check_moe_rows(tokens, k, cols, rows, f8 == FQ_F8_NONE ? 8 : 32));
+    FQ_TRY(check_ptr(x, "x", true));
+    if (f8 == FQ_F8_NONE && scales)
+        return fail(FQ_ERR_DESC, "scales are read only with 8-bit rows");
+    FQ_TRY(check_ptr(scales, "scales", f8 != FQ_F8_NONE));
+    FQ_TRY(check_ptr(pos, "pos", true, 4));
+    FQ_TRY(check_ptr(src, "src", true, 4));
+    FQ_TRY(check_ptr(y_bf16, "y", true));
+    fqimpl::MoeRowsArgs a = {};
+    a.T = tokens;
+    a.k = k;
+    a.H = cols;
+    a.rows = rows;
+    a.pos = pos;
+    a.src = src;
+    a.x = x;
+    a.scales = scales;
+    a.rows_out = y_bf16;
+    return device_status(fqimpl::launch_moe_dispatch(f8, a, (hipStream_t)stream),
+                         "dispatch launch");
+}
+
+fq_status fq_moe_combine(const void *y_bf16, const float *weights, int64_t tokens, int64_t k,
+                         int64_t cols, int64_t rows, const int32_t *pos, void *out_bf16,
+                         void *stream)
+{
+    FQ_TRY(check_moe_rows(tokens, k, cols, rows, 8));
+    FQ_TRY(check_ptr(y_bf16, "y", true));
+    FQ_TRY(check_ptr(weights, "weights", false, 4));
+    FQ_TRY(check_ptr(pos, "pos", true, 4));
+    FQ_TRY(check_ptr(out_bf16, "out", true));
+    fqimpl::MoeRowsArgs a = {};
+    a.T = tokens;
+    a.k = k;
+    a.H = cols;
+    a.rows = rows;
+    a.pos = pos;
+    a.weights = weights;
+    a.y = y_bf16;
+    a.out = out_bf16;
+    return device_status(fqimpl::launch_moe_combine(a, (hipStream_t)stream), "combine launch");
+}
+
+fq_status fq_moe_combine_bwd(const void *dout_bf16, const void *y_bf16, const float *weights,
+                             int64_t tokens, int64_t k, int64_t cols, int64_t rows,
+                             const int32_t *pos, const int32_t *src, void *dy_bf16,
+                             float *dweights, void *stream)
+{
+    FQ_TRY(check_moe_rows(tokens, k, cols, rows, 8));
+    FQ_TRY(check_ptr(dout_bf16, "dout", true));
+    FQ_TRY(check_ptr(y_bf16, "y", true));
+    FQ_TRY(check_ptr(weights, "weights", true, 4));
+    FQ_TRY(check_ptr(pos, "pos", true, 4));
+    FQ_TRY(check_ptr(src, "src", true, 4));
+    FQ_TRY(check_ptr(dy_bf16, "dy", true));
+    FQ_TRY(check_ptr(dweights, "dweights", true, 4));
+    fqimpl::MoeRowsArgs a = {};
+    a.T = tokens;
+    a.k = k;
+    a.H = cols;
+    a.rows = rows;
+    a.pos = pos;
+    a.src = src;
+    a.weights = weights;
+    a.y = y_bf16;
+    a.dout = dout_bf16;
+    a.rows_out = dy_bf16;
+    a.dweights = dweights;
+    return device_status(fqimpl::launch_moe_combine_bwd(a, (hipStream_t)stream),
+                         "combine backward launch");
+}
+
+fq_status fq_adamw_step(const fq_adamw_hyper *hyper, const fq_adamw_tensor *tensors,
+                        int64_t count, void *stream)
+{
+    if (!hyper) return fail(FQ_ERR_NULL, "hyper is NULL");
+    const fq_adamw_hyper &h = *hyper;
+    if (h.reserved != 0) return fail(FQ_ERR_DESC, "hyper->reserved must be 0");
+    if (h.state_type != FQ_STATE_F32 && h.state_type != FQ_STATE_F8)
+        return fail(FQ_ERR_DESC, "hyper->state_type=%d is not FQ_STATE_F32/F8", h.state_type);
+    if (!(h.beta1 >= 0 && h.beta1 < 1 && h.beta2 >= 0 && h.beta2 < 1))
+        return fail(FQ_ERR_DESC, "beta1 and beta2 must be in [0, 1)");
+    if (!(h.eps >= 0) || !std::isfinite(h.lr) || !std::isfinite(h.eps))
+        return fail(FQ_ERR_DESC, "lr must be finite and eps finite and >= 0");
+    if (h.step < 1 || h.step > 0xFFFFFFFFll)
+        return fail(FQ_ERR_DESC, "step=%lld must be in [1, 2^32)", (long long)h.step);
+    FQ_TRY(check_ptr(h.grad_scale, "hyper->grad_scale", false, 4));
+    if (count < 0 || count > kMaxDim)
+        return fail(FQ_ERR_SHAPE, "count=%lld must be >= 0 and below 2^31", (long long)count);
+    if (count && !tensors) return fail(FQ_ERR_NULL, "tensors is NULL");
+    const bool f8 = h.state_type == FQ_STATE_F8;
+    for (int64_t i = 0; i < count; ++i) {
+        const fq_adamw_tensor &t = tensors[i];
+        if (t.reserved != 0)
+            return fail(FQ_ERR_DESC, "tensors[%lld].reserved must be 0", (long long)i);
+        if (t.g_type != FQ_TYPE_BF16 && t.g_type != FQ_TYPE_F32)
+            return fail(FQ_ERR_DESC, "tensors[%lld].g_type=%d is not FQ_TYPE_BF16/F32",
+                        (long long)i, t.g_type);
+        if (t.n < 0 || t.n > kMaxElems)
+            return fail(FQ_ERR_SHAPE, "tensors[%lld].n=%lld must be in [0, 2^34]", (long long)i,
+                        (long long)t.n);
+        if (!std::isfinite(t.lr_mult) || !std::isfinite(t.weight_decay))
+            return fail(FQ_ERR_DESC, "tensors[%lld]: lr_mult and weight_decay must be finite",
+                        (long long)i);
+        if (t.n == 0) continue;
+        const void *need[] = {t.w, t.g, t.m, t.v};
+        for (const void *p : need) {
+            if (!p) return fail(FQ_ERR_NULL, "tensors[%lld]: w, g, m or v is NULL", (long long)i);
+            if (!aligned(p, 16))
+                return fail(FQ_ERR_ALIGN, "tensors[%lld]: w, g, m or v is not 16-byte aligned",
+                            (long long)i);
+        }
+        if (!aligned(t.w_bf16, 16))
+            return fail(FQ_ERR_ALIGN, "tensors[%lld].w_bf16 is not 16-byte aligned", (long long)i);
+        if (f8 && (!t.m_scale || !t.v_scale))
+            return fail(FQ_ERR_NULL, "tensors[%lld]: m_scale or v_scale is NULL", (long long)i);
+        if (f8 && !(aligned(t.m_scale, 4) && aligned(t.v_scale, 4)))
+            return fail(FQ_ERR_ALIGN, "tensors[%lld]: m_scale or v_scale is not 4-byte aligned",
+                        (long long)i);
+    }
+    fqimpl::AdamWArgs a;
+    a.lr = (float)h.lr;
+    a.beta1 = (float)h.beta1;
+    a.one_beta1 = (float)(1.0 - h.beta1);
+    a.beta2 = (float)h.beta2;
+    a.one_beta2 = (float)(1.0 - h.beta2);
+    a.eps = (float)h.eps;
+    a.inv_bc1 = (float)(1.0 / (1.0 - std::pow(h.beta1, (double)h.step)));
+    a.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(h.beta2, (double)h.step)));
+    a.grad_scale = h.grad_scale;
+    a.step = (uint32_t)h.step;
+    a.seed_lo = (uint32_t)h.seed;
+    a.seed_hi = (uint32_t)(h.seed >> 32);
+    a.count = 0;
+    uint32_t grid = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const fq_adamw_tensor &t = tensors[i];
+        if (t.n) {
+            const uint32_t wgs = fqimpl::adamw_workgroups(t.n);
+            // a launch's grid stays well below 2^31 workgroups
+            if (a.count == fqimpl::kAdamWTensors || (a.count && grid + (uint64_t)wgs > (1u << 30))) {
+                FQ_TRY(device_status(fqimpl::launch_adamw(a, f8, grid, (hipStream_t)stream),
+                                     "AdamW launch"));
+                a.count = grid = 0;
+            }
+            a.first[a.count] = grid;
+            a.index[a.count] = (uint32_t)i;
+            a.t[a.count++] = {t.w, t.w_bf16, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n,
+                              t.lr_mult, t.weight_decay, t.g_type == FQ_TYPE_F32};
+            grid += wgs;
+        }
+    }
+    if (!a.count) return ok();
+    return device_status(fqimpl::launch_adamw(a, f8, grid, (hipStream_t)stream), "AdamW launch");
+}
+
+}  // extern "C"
+
+extern "C" {
 
 const char *fq_status_string(fq_status s)
 {

@@ -126,4 +126,100 @@ struct RetainArgs {
 };
 hipError_t launch_quant_retain(const RetainArgs &a, hipStream_t stream);
 
+// ---- row operators around the quantized linears ------------------------------
+enum { F8_NONE = 0, F8_MX = 1, F8_ROW = 2 };       // FQ_F8_* of fq.h
+
+// fq_norm.hip
+constexpr int64_t kNormMaxCols = 32768;
+struct NormFwdArgs {
+    const void *x;           // BF16 [rows, cols]
+    const void *res;         // the stream, BF16 or FP32 [rows, cols], or null
+    int stream_f32;
+    const void *gamma;       // BF16 or FP32 [cols]
+    int gamma_f32;
+    float eps;
+    int64_t rows, cols;
+    int f8;                  // F8_*
+    void *h;                 // x + res in the stream's type (may be res), with res only
+    void *y;                 // BF16 or null
+    void *codes;             // E4M3 or null
+    void *scales;            // E8M0 [rows, cols / 32] or FP32 [rows], or null
+    float *rstd;             // FP32 [rows] or null
+};
+hipError_t launch_rmsnorm_fwd(const NormFwdArgs &a, hipStream_t stream);
+struct NormBwdArgs {
+    const void *dy;          // BF16
+    const void *h;           // the normalized values, BF16 or FP32
+    int stream_f32;
+    const void *gamma;
+    int gamma_f32;
+    const float *rstd;
+    const void *dres;        // gradient of h from elsewhere, in h's type, or null
+    int64_t rows, cols;
+    void *dh;                // in h's type (may be dres)
+    void *dx;                // BF16 copy of dh, or null
+    float *partials;         // groups * cols column sums
+    int64_t groups;
+};
+// groups of column sums the backward leaves (its workspace holds as many rows)
+int64_t rmsnorm_bwd_groups(int64_t rows, int64_t cols);
+hipError_t launch_rmsnorm_bwd(NormBwdArgs a, float *dgamma, hipStream_t stream);
+
+// fq_moe.hip
+constexpr int kMoeMaxExperts = 1024;
+constexpr int64_t kMoeMaxChunks = 256;      // workgroups of the sort
+struct MoeSortArgs {
+    const int32_t *ids;      // [n] expert of each assignment
+    int64_t n;
+    uint32_t E, align;
+    int64_t rows;            // of the sorted order, padding included
+    int32_t *offsets;        // [E + 1]
+    int32_t *pos;            // [n]
+    int32_t *src;            // [rows]
+    uint32_t *ws;            // counts of every chunk and expert
+    uint32_t chunk;
+};
+uint32_t moe_sort_chunk(int64_t n);         // assignments of a workgroup
+hipError_t launch_moe_sort(MoeSortArgs a, hipStream_t stream);
+struct MoeRowsArgs {
+    int64_t T, k, H, rows;
+    const int32_t *pos;      // [T, k]
+    const int32_t *src;      // [rows]
+    const float *weights;    // [T, k] or null
+    const void *x;           // dispatch: BF16 or E4M3 [T, H]
+    const void *scales;      // dispatch: E8M0 [T, H / 32] or FP32 [T]
+    const void *y;           // BF16 [rows, H]
+    const void *dout;        // BF16 [T, H]
+    void *rows_out;          // dispatch's y, combine_bwd's dy: BF16 [rows, H]
+    void *out;               // combine's BF16 [T, H]
+    float *dweights;         // [T, k]
+};
+hipError_t launch_moe_dispatch(int f8, const MoeRowsArgs &a, hipStream_t stream);
+hipError_t launch_moe_combine(const MoeRowsArgs &a, hipStream_t stream);
+hipError_t launch_moe_combine_bwd(const MoeRowsArgs &a, hipStream_t stream);
+
+// fq_adamw.hip
+constexpr uint32_t kAdamWTensors = 32;      // of one launch (the table is 2.4 KB of arguments)
+struct AdamWTensor {
+    float *w;
+    void *w_bf16;            // or null
+    const void *g;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    int64_t n;
+    float lr_mult, weight_decay;
+    int g_f32;
+};
+struct AdamWArgs {
+    uint32_t count;          // tensors of this launch, all with n > 0
+    float lr, beta1, one_beta1, beta2, one_beta2, eps, inv_bc1, inv_sqrt_bc2;
+    const float *grad_scale; // device scalar or null
+    uint32_t step, seed_lo, seed_hi;
+    uint32_t first[kAdamWTensors];          // first workgroup of each tensor
+    uint32_t index[kAdamWTensors];          // number of each tensor in the whole list
+    AdamWTensor t[kAdamWTensors];
+};
+uint32_t adamw_workgroups(int64_t n);       // workgroups that n elements take
+hipError_t launch_adamw(const AdamWArgs &a, bool f8, uint32_t grid, hipStream_t stream);
+
 }  // namespace fqimpl

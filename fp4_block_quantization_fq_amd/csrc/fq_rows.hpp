@@ -1,0 +1,210 @@
+// fq_rows.hpp -- device-side building blocks of the row operators around the
+// quantized linears (norm, expert sorting, optimizer): eight-element chunks
+// of BF16 or FP32 rows at any alignment, sums and maxima across a wave, and
+// the 8-bit float encodings.
+//
+// 8-bit formats (OCP OFP8 v1.0): E4M3 (4 exponent bits, bias 7, largest 448,
+// NaN 0x7F) and E5M2 (5 exponent bits, bias 15, largest 57344, NaN 0x7F used
+// here).  gfx950's converters decode both exactly.
+#pragma once
+
+#include "fq_device.hpp"
+
+namespace fqdev {
+
+typedef uint32_t u32w4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32w2 __attribute__((ext_vector_type(2)));
+typedef u32w4 u32w4_any __attribute__((aligned(2)));   // unaligned global access
+typedef u32w4 u32w4_any4 __attribute__((aligned(4)));
+
+// ---- eight consecutive elements of a row ------------------------------------
+// `n` of them exist (8, or fewer in the last chunk of a row whose length is
+// no multiple of 8); missing ones read as 0 and are not written.  ANY: the
+// row may start at any element; gfx950 serves the 16-byte access at element
+// alignment, so only the last chunk goes element by element.
+template <bool ANY>
+__device__ __forceinline__ void load8(const uint16_t *__restrict__ p, int n, float (&v)[8])
+{
+    u32w4 w;
+    if (ANY) {
+        if (n < 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < n ? as_f((uint32_t)p[i] << 16) : 0.0f;
+            return;
+        }
+        w = *reinterpret_cast<const u32w4_any *>(p);
+    } else {
+        w = *reinterpret_cast<const u32w4 *>(p);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = as_f(lo_bits(w[i]));
+        v[2 * i + 1] = as_f(hi_bits(w[i]));
+    }
+}
+template <bool ANY>
+__device__ __forceinline__ void load8(const float *__restrict__ p, int n, float (&v)[8])
+{
+    u32w4 a, b;
+    if (ANY) {
+        if (n < 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
+            return;
+        }
+        a = reinterpret_cast<const u32w4_any4 *>(p)[0];
+        b = reinterpret_cast<const u32w4_any4 *>(p)[1];
+    } else {
+        a = reinterpret_cast<const u32w4 *>(p)[0];
+        b = reinterpret_cast<const u32w4 *>(p)[1];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = as_f(a[i]);
+        v[4 + i] = as_f(b[i]);
+    }
+}
+// BF16: each value rounded once, to nearest even.
+template <bool ANY>
+__device__ __forceinline__ void store8(uint16_t *__restrict__ p, int n, const float (&v)[8])
+{
+    u32w4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = bf16_pair_rne(v[2 * i], v[2 * i + 1]);
+    if (ANY) {
+        if (n < 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) p[i] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+            return;
+        }
+        *reinterpret_cast<u32w4_any *>(p) = w;
+    } else {
+        *reinterpret_cast<u32w4 *>(p) = w;
+    }
+}
+template <bool ANY>
+__device__ __forceinline__ void store8(float *__restrict__ p, int n, const float (&v)[8])
+{
+    if (ANY && n < 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = v[i];
+        return;
+    }
+    const u32w4 a = {as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3])};
+    const u32w4 b = {as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7])};
+    if (ANY) {
+        reinterpret_cast<u32w4_any4 *>(p)[0] = a;
+        reinterpret_cast<u32w4_any4 *>(p)[1] = b;
+    } else {
+        reinterpret_cast<u32w4 *>(p)[0] = a;
+        reinterpret_cast<u32w4 *>(p)[1] = b;
+    }
+}
+
+// ---- across the wave ----------------------------------------------------------
+// DPP inside a 16-lane row (quad permutes, then the row's halves and the row
+// mirrored, each pairing lanes that hold equal partial results), two lane
+// exchanges across the four rows.  Every lane gets the same value.
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v += dpp_f<0xB1>(v);
+    v += dpp_f<0x4E>(v);
+    v += dpp_f<0x141>(v);
+    v += dpp_f<0x140>(v);
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    return v;
+}
+// maximum over the 16 lanes of a DPP row (values >= 0, or their bits)
+__device__ __forceinline__ uint32_t dpp_max_16lanes(uint32_t v)
+{
+    v = dpp_max_8lanes(v);
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    v = dpp_max_16lanes(v);
+    v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+    return max(v, (uint32_t)__shfl_xor((int)v, 32));
+}
+
+// bits of the largest magnitude of eight values; a NaN's bits exceed
+// infinity's, which exceed every finite value's
+__device__ __forceinline__ uint32_t absmax8(const float (&v)[8])
+{
+    uint32_t m = as_u(v[0]) & 0x7FFFFFFFu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max(m, as_u(v[i]) & 0x7FFFFFFFu);
+    return m;
+}
+
+// ---- E4M3 with a scale ---------------------------------------------------------
+// E8M0 code of the smallest power of two 2^e with amax <= 448 * 2^e = 1.75 *
+// 2^(e + 8) (amax as FP32 bits, finite): one more than the exponent's own
+// where the significand exceeds 1.75.  Codes 0 .. 247.
+__device__ __forceinline__ uint32_t mx8_scale_code(uint32_t amax_bits)
+{
+    const int e = (int)(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return (uint32_t)max(e, 0);
+}
+// eight values (|v| <= 448) -> eight E4M3 codes, nearest even
+__device__ __forceinline__ u32w2 e4m3_encode8(const float (&v)[8])
+{
+    int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], a, true);
+    int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], b, true);
+    return (u32w2){(uint32_t)a, (uint32_t)b};
+}
+__device__ __forceinline__ void e4m3_decode8(u32w2 c, float (&v)[8])
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[h], false);
+        const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[h], true);
+        v[4 * h] = lo[0];
+        v[4 * h + 1] = lo[1];
+        v[4 * h + 2] = hi[0];
+        v[4 * h + 3] = hi[1];
+    }
+}
+__device__ __forceinline__ void e5m2_decode8(u32w2 c, float (&v)[8])
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_bf8((int)c[h], false);
+        const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_bf8((int)c[h], true);
+        v[4 * h] = lo[0];
+        v[4 * h + 1] = lo[1];
+        v[4 * h + 2] = hi[0];
+        v[4 * h + 3] = hi[1];
+    }
+}
+
+// Stochastic rounding of 0 <= a <= the format's largest value to an 8-bit
+// float with MANT mantissa bits, smallest normal value 2^LOWEST: with T =
+// floor(2^16 * (a - g_k) / (g_{k+1} - g_k)) for neighbouring values g_k <= a <
+// g_{k+1}, up exactly when r16 < T.  On the FP32 bits T is the top 16 of the
+// dropped mantissa bits, and adding 0xFFFF - r16 to it carries into the kept
+// bits exactly when T > r16; below 2^LOWEST the same carry on the value in
+// fixed point, in units of the subnormal step.
+template <int MANT, int LOWEST>
+__device__ __forceinline__ uint32_t float8_sr(float a, uint32_t r16)
+{
+    constexpr int kDrop = 23 - MANT;
+    const uint32_t add = 0xFFFFu - r16;
+    const uint32_t normal = ((as_u(a) + (add << (kDrop - 16))) >> kDrop) -
+                            ((uint32_t)(127 + LOWEST - 1) << MANT);
+    const float per_step = as_f((uint32_t)(127 - LOWEST + MANT + 16) << 23);   // 2^16 a / step
+    const uint32_t sub = ((uint32_t)(a * per_step) + add) >> 16;
+    return a < as_f((uint32_t)(127 + LOWEST) << 23) ? sub : normal;
+}
+
+}  // namespace fqdev

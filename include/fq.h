@@ -414,6 +414,160 @@ fq_status fq_qlinear_bwd_retain(const fq_desc *desc_x, const fq_desc *desc_w,
                                 const void *retain, const float *chan_scale, void *dx_bf16,
                                 void *dw_bf16, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- Around the linears of a training step ------------------------------------
+ * Operators that a quantization-aware training step runs beside its quantized
+ * products: the norm in front of a linear, the sorting of tokens by expert
+ * around the experts' linears, and the optimizer behind them.  Unlike the
+ * quantizers they accept infinities and NaN, as described at each.
+ *
+ * 8-bit rows (FQ_F8_*), elements E4M3 (OCP OFP8 v1.0), scales rounded up so
+ * that no value saturates (so the straight-through gradient passes everywhere):
+ *   FQ_F8_MX   per 32 consecutive elements the smallest power of two 2^e with
+ *              amax <= 448 * 2^e, as E8M0 code clamp(e, -127, 127) + 127 (OCP
+ *              MX v1.0's MXFP8 layout): scales uint8 [rows, cols / 32].
+ *   FQ_F8_ROW  per row s = max(RN(amax / 448), 2^-126): scales FP32 [rows];
+ *              the scaled value is RN(x * RN(1 / s)) clamped to +-448.
+ * Codes are nearest even.  A block (row) whose amax is infinite or NaN gets
+ * scale code 255 (scale NaN) and codes 0x7F, and stands for NaN.  cols must be
+ * a multiple of 32. */
+enum { FQ_F8_NONE = 0, FQ_F8_MX = 1, FQ_F8_ROW = 2 };
+enum { FQ_TYPE_BF16 = 0, FQ_TYPE_F32 = 1 };
+
+/* Residual addition and root-mean-square norm:
+ *   h = x + res   rounded once to the stream's type (nearest even);
+ *   r = 1 / sqrt(mean(h^2) + eps) over each row, FP32;
+ *   n = (h * r) * gamma, FP32;   y = BF16_RNE(n).
+ * The norm is that of the stored h, the value the backward reads.  Without a
+ * residual (res NULL, then h NULL too) h is x and stream_type is not used.
+ * With f8 != FQ_F8_NONE n goes to 8 bits instead (above): codes [rows, cols]
+ * and scales, and y, if given, holds the values they stand for (for
+ * FQ_F8_ROW rounded to BF16).
+ * x BF16 [rows, cols]; res and h of stream_type (FQ_TYPE_*), h may be res;
+ * gamma [cols] of gamma_type; rstd FP32 [rows] receives r (may be NULL).  y is
+ * required without f8; with it at least one of y and codes, and scales with
+ * codes.  rows >= 1, 1 <= cols <= 32768 (any, a multiple of 32 with f8), rows *
+ * cols <= 2^34.  All pointers 16-byte aligned, rstd 4-byte.  A NaN in
+ * a row makes all of its n NaN; an infinity makes r 0, so n is NaN there and 0
+ * elsewhere in the row. */
+fq_status fq_rmsnorm_fwd(const void *x_bf16, const void *res, int32_t stream_type,
+                         const void *gamma, int32_t gamma_type, float eps, int64_t rows,
+                         int64_t cols, int32_t f8, void *h, void *y_bf16, void *codes,
+                         void *scales, float *rstd, void *stream);
+
+/* Bytes of workspace of fq_rmsnorm_bwd (column sums of groups of rows); 0 for
+ * a shape outside its limits. */
+size_t fq_rmsnorm_bwd_workspace_size(int64_t rows, int64_t cols);
+
+/* Backward of fq_rmsnorm_fwd.  With xh = h * r and g = dy * gamma:
+ *   dh = r * (g - xh * mean(g * xh)) + dres,   dgamma = sum over rows of dy * xh.
+ * h of stream_type is the forward's h (x in BF16 where it had no residual),
+ * rstd the forward's r.  dres (same type, may be NULL) is the gradient that
+ * reaches h from elsewhere; dh (same type, may be dres) is the gradient of
+ * both x and res; dx, if given, receives it rounded to BF16 (the gradient of x
+ * beside an FP32 stream).  dgamma FP32 [cols] may be NULL, then no workspace
+ * is needed.  FP32 sums in a fixed order: equal calls give equal bits.  The
+ * rounding to 8 bits is passed straight through. */
+fq_status fq_rmsnorm_bwd(const void *dy_bf16, const void *h, int32_t stream_type,
+                         const void *gamma, int32_t gamma_type, const float *rstd,
+                         const void *dres, int64_t rows, int64_t cols, void *dh, void *dx_bf16,
+                         float *dgamma, void *ws, size_t ws_bytes, void *stream);
+
+/* Tokens sorted by expert.  experts_of [tokens, k] int32 names the experts of
+ * every token; assignment a = t * k + j.  Expert e's assignments, in ascending
+ * order, take rows offsets[e], offsets[e] + 1, ... of the sorted order; each
+ * segment is padded to a multiple of `align` rows (fq_qlinear_bwd takes
+ * multiples of 64 or 128).  An id outside [0, experts) is no expert: such an
+ * assignment has no row.
+ *   offsets [experts + 1] int32: segment starts, then the number of rows used;
+ *   pos [tokens, k] int32: row of each assignment, -1 without one;
+ *   src [rows] int32: assignment of each row, -1 for padding and unused rows.
+ * rows, the length of the sorted order's buffers, is at least fq_moe_rows
+ * (what the segments take at most, whatever the ids; 0 for arguments outside
+ * the limits).  1 <= k <= 64, 1 <= experts <= 1024, tokens * k <= 2^30, 1 <=
+ * align <= 1024.  ws: fq_moe_sort_workspace_size bytes (0: may be NULL). */
+enum { FQ_MOE_MAX_K = 64, FQ_MOE_MAX_ALIGN = 1024 };
+int64_t fq_moe_rows(int64_t tokens, int64_t k, int64_t experts, int64_t align);
+size_t fq_moe_sort_workspace_size(int64_t tokens, int64_t k, int64_t experts);
+fq_status fq_moe_sort(const int32_t *experts_of, int64_t tokens, int64_t k, int64_t experts,
+                      int64_t align, int64_t rows, int32_t *offsets, int32_t *pos, int32_t *src,
+                      void *ws, size_t ws_bytes, void *stream);
+
+/* Rows of the tokens in the sorted order: y[pos[t, j]] = x[t], +0 in rows
+ * without an assignment.  y BF16 [rows, cols]; x BF16 [tokens, cols], or with
+ * f8 the codes and scales of fq_rmsnorm_fwd, decoded on the way (rounded to
+ * BF16).  cols a multiple of 8 (32 with f8).  pos and src as fq_moe_sort wrote
+ * them; entries outside [0, rows) or [0, tokens * k) count as -1.  Its
+ * backward is fq_moe_combine without weights. */
+fq_status fq_moe_dispatch(const void *x, int32_t f8, const void *scales, int64_t tokens,
+                          int64_t k, int64_t cols, int64_t rows, const int32_t *pos,
+                          const int32_t *src, void *y_bf16, void *stream);
+
+/* Back to the tokens: out[t] = BF16_RNE(sum over j of weights[t, j] *
+ * y[pos[t, j]]), summed in FP32 in the order of j over the assignments that
+ * have a row (+0 for a token with none); weights FP32 [tokens, k], NULL for
+ * ones. */
+fq_status fq_moe_combine(const void *y_bf16, const float *weights, int64_t tokens, int64_t k,
+                         int64_t cols, int64_t rows, const int32_t *pos, void *out_bf16,
+                         void *stream);
+
+/* Backward of fq_moe_combine: dy[pos[t, j]] = BF16_RNE(weights[t, j] *
+ * dout[t]), +0 in rows without an assignment; dweights[t, j] = <dout[t],
+ * y[pos[t, j]]> in FP32, 0 without a row. */
+fq_status fq_moe_combine_bwd(const void *dout_bf16, const void *y_bf16, const float *weights,
+                             int64_t tokens, int64_t k, int64_t cols, int64_t rows,
+                             const int32_t *pos, const int32_t *src, void *dy_bf16,
+                             float *dweights, void *stream);
+
+/* One AdamW step over `count` tensors:
+ *   g' = g * grad_scale;  m = beta1 m + (1 - beta1) g';
+ *   v = beta2 v + (1 - beta2) g'^2;  l = lr * lr_mult;
+ *   w = w (1 - l * weight_decay)
+ *       - l / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps);
+ *   w_bf16 = BF16_RNE(w),
+ * in FP32.  w is the FP32 master weight (as for fq_osci_track), w_bf16 (may be
+ * NULL) the copy that the linears read, g BF16 or FP32.
+ * state_type FQ_STATE_F32: m, v FP32 [n].  FQ_STATE_F8: m E4M3 and v E5M2
+ * codes [n], m_scale and v_scale FP32 [ceil(n / 128)], a scale per 128
+ * consecutive elements: s = max(RN(amax / 448), 2^-126) for m (57344 for v)
+ * with amax over the block's finite values, a = min(|x| RN(1 / s), largest),
+ * rounded stochastically: up to the next value exactly when r16 <
+ * floor(2^16 * fraction of the way to it), with r16 the low (m) or high (v)
+ * half of word n mod 4 of Philox4x32-10 with key seed and counter (low and
+ * high word of n / 4, number of the tensor in the list, step), n the element.
+ * A positive v gets at least code 1; infinities and NaN get code 0x7F, NaN.
+ * Rounding to nearest would keep an 8-bit v where it is for ever, because
+ * 1 - beta2 is far below half a step of the format.  All-zero codes and scales
+ * are the state before the first step.
+ * step counts from 1.  grad_scale: device scalar (a clipping factor), NULL for
+ * 1.  lr and step are read by the call: a captured call keeps them.  w, w_bf16,
+ * g, m, v 16-byte aligned, scales 4-byte; n <= 2^34, n = 0 is skipped;
+ * `tensors` is read during the call only.  No workspace. */
+enum { FQ_STATE_F32 = 0, FQ_STATE_F8 = 1 };
+typedef struct {
+    float *w;
+    void *w_bf16;
+    const void *g;
+    void *m;
+    void *v;
+    float *m_scale;
+    float *v_scale;
+    int64_t n;
+    int32_t g_type;
+    int32_t reserved;      /* must be 0 */
+    float lr_mult;
+    float weight_decay;
+} fq_adamw_tensor;
+typedef struct {
+    double lr, beta1, beta2, eps;
+    int64_t step;
+    uint64_t seed;
+    const float *grad_scale;
+    int32_t state_type;
+    int32_t reserved;      /* must be 0 */
+} fq_adamw_hyper;
+fq_status fq_adamw_step(const fq_adamw_hyper *hyper, const fq_adamw_tensor *tensors,
+                        int64_t count, void *stream);
+
 /* Static description of a status code. */
 const char *fq_status_string(fq_status s);
 

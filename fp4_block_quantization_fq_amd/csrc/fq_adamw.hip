@@ -43,6 +43,12 @@ __device__ __forceinline__ uint32_t finite_max8(const float (&v)[8])
     return m;
 }
 
+// scale of a state block from the bits of its largest magnitude
+__device__ __forceinline__ float state_scale(uint32_t top, float per_largest)
+{
+    return __builtin_fmaxf(as_f(top) * per_largest, 0x1p-126f);
+}
+
 __device__ __forceinline__ u32w2 load_codes(const uint8_t *__restrict__ p, int n)
 {
     if (n == 8) return *(const u32w2 *)p;
@@ -141,30 +147,53 @@ __global__ __launch_bounds__(kThreads) void k_adamw(fqimpl::AdamWArgs a)
         const u32x4 o = philox4x32_10((uint32_t)q, (uint32_t)(q >> 32), a.index[lo], a.step,
                                       a.seed_lo, a.seed_hi);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[4 * h + e] = o.v[e];
+        for (int e = 0; e < 4; ++e) r[4 * h + e] = ~o.v[e];
     }
     // lanes past the end hold zeros
-    const float mtop = as_f(dpp_max_16lanes(finite_max8(m)));
-    const float vtop = as_f(dpp_max_16lanes(finite_max8(v)));
-    const float ms = __builtin_fmaxf(mtop / 448.0f, 0x1p-126f);
-    const float vs = __builtin_fmaxf(vtop / 57344.0f, 0x1p-126f);
+    uint32_t mt = absmax8(m), vt = absmax8(v);
+    const bool finite = max(mt, vt) < 0x7F800000u;
+    if (!finite) {
+        mt = finite_max8(m);
+        vt = finite_max8(v);
+    }
+    const float ms = state_scale(dpp_max_16lanes(mt), 1.0f / 448.0f);
+    const float vs = state_scale(dpp_max_16lanes(vt), 1.0f / 57344.0f);
     const float mi = 1.0f / ms, vi = 1.0f / vs;
-    u32w2 mc = {0, 0}, vc = {0, 0};
+    // The converter adds its random operand, shifted down to the dropped bits,
+    // and truncates: with 0xFFFF - r16 in the top 16 bits and zeros below, the
+    // kept bits grow exactly when r16 < floor(2^16 * fraction).
+    uint32_t mc[2] = {0, 0}, vc[2] = {0, 0};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t mu = as_u(m[e]), vu = as_u(v[e]);
-        uint32_t x = float8_sr<3, -6>(__builtin_fminf(__builtin_fabsf(m[e]) * mi, 448.0f), r[e] & 0xFFFFu);
-        if ((mu & 0x7FFFFFFFu) >= 0x7F800000u) x = 0x7Fu;
-        x |= (mu >> 31) << 7;
-        mc[e / 4] |= x << (8 * (e % 4));
-        uint32_t y = float8_sr<2, -14>(__builtin_fminf(v[e] * vi, 57344.0f), r[e] >> 16);
-        if (v[e] > 0.0f) y = max(y, 1u);
-        if (vu >= 0x7F800000u) y = 0x7Fu;
-        vc[e / 4] |= y << (8 * (e % 4));
+    for (int h = 0; h < 2; ++h) {
+        const int e = 4 * h;
+        const auto ma = [&](int k) { return __builtin_amdgcn_fmed3f(m[e + k] * mi, -448.0f, 448.0f); };
+        // a positive v is at least the smallest code's value, 2^-16
+        const auto va = [&](int k) {
+            return __builtin_amdgcn_fmed3f(v[e + k] * vi, v[e + k] > 0.0f ? 0x1p-16f : 0.0f, 57344.0f);
+        };
+        mc[h] = __builtin_amdgcn_cvt_sr_fp8_f32(ma(0), r[e] << 16, mc[h], 0);
+        mc[h] = __builtin_amdgcn_cvt_sr_fp8_f32(ma(1), r[e + 1] << 16, mc[h], 1);
+        mc[h] = __builtin_amdgcn_cvt_sr_fp8_f32(ma(2), r[e + 2] << 16, mc[h], 2);
+        mc[h] = __builtin_amdgcn_cvt_sr_fp8_f32(ma(3), r[e + 3] << 16, mc[h], 3);
+        vc[h] = __builtin_amdgcn_cvt_sr_bf8_f32(va(0), r[e] & 0xFFFF0000u, vc[h], 0);
+        vc[h] = __builtin_amdgcn_cvt_sr_bf8_f32(va(1), r[e + 1] & 0xFFFF0000u, vc[h], 1);
+        vc[h] = __builtin_amdgcn_cvt_sr_bf8_f32(va(2), r[e + 2] & 0xFFFF0000u, vc[h], 2);
+        vc[h] = __builtin_amdgcn_cvt_sr_bf8_f32(va(3), r[e + 3] & 0xFFFF0000u, vc[h], 3);
+    }
+    if (!finite) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int shift = 8 * (e % 4);
+            const uint32_t mu = as_u(m[e]);
+            if ((mu & 0x7FFFFFFFu) >= 0x7F800000u)
+                mc[e / 4] = (mc[e / 4] & ~(0xFFu << shift)) | ((0x7Fu | (mu >> 31) << 7) << shift);
+            if ((as_u(v[e]) & 0x7FFFFFFFu) >= 0x7F800000u)
+                vc[e / 4] = (vc[e / 4] & ~(0xFFu << shift)) | (0x7Fu << shift);
+        }
     }
     if (n <= 0) return;
-    store_codes((uint8_t *)t.m + at, nn, mc);
-    store_codes((uint8_t *)t.v + at, nn, vc);
+    store_codes((uint8_t *)t.m + at, nn, (u32w2){mc[0], mc[1]});
+    store_codes((uint8_t *)t.v + at, nn, (u32w2){vc[0], vc[1]});
     if ((threadIdx.x & 15) == 0) {
         t.m_scale[at >> 7] = ms;
         t.v_scale[at >> 7] = vs;

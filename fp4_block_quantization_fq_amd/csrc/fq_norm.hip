@@ -127,7 +127,7 @@ __global__ __launch_bounds__(threads_of<WPR>()) void k_rmsnorm_fwd(fqimpl::NormF
 #pragma unroll
         for (int i = 0; i < NCH; ++i) top = max(top, absmax8(h[i]));
         top = row_max<WPR>(top, red, 1);
-        scale = __builtin_fmaxf(as_f(top) / 448.0f, 0x1p-126f);
+        scale = __builtin_fmaxf(as_f(top) * (1.0f / 448.0f), 0x1p-126f);
         inv = 1.0f / scale;
         if (top >= 0x7F800000u) scale = as_f(0x7FC00000u);
         if (a.scales && live && l == 0) ((float *)a.scales)[row] = scale;

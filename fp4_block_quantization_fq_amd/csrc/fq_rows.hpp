@@ -188,23 +188,4 @@ __device__ __forceinline__ void e5m2_decode8(u32w2 c, float (&v)[8])
     }
 }
 
-// Stochastic rounding of 0 <= a <= the format's largest value to an 8-bit
-// float with MANT mantissa bits, smallest normal value 2^LOWEST: with T =
-// floor(2^16 * (a - g_k) / (g_{k+1} - g_k)) for neighbouring values g_k <= a <
-// g_{k+1}, up exactly when r16 < T.  On the FP32 bits T is the top 16 of the
-// dropped mantissa bits, and adding 0xFFFF - r16 to it carries into the kept
-// bits exactly when T > r16; below 2^LOWEST the same carry on the value in
-// fixed point, in units of the subnormal step.
-template <int MANT, int LOWEST>
-__device__ __forceinline__ uint32_t float8_sr(float a, uint32_t r16)
-{
-    constexpr int kDrop = 23 - MANT;
-    const uint32_t add = 0xFFFFu - r16;
-    const uint32_t normal = ((as_u(a) + (add << (kDrop - 16))) >> kDrop) -
-                            ((uint32_t)(127 + LOWEST - 1) << MANT);
-    const float per_step = as_f((uint32_t)(127 - LOWEST + MANT + 16) << 23);   // 2^16 a / step
-    const uint32_t sub = ((uint32_t)(a * per_step) + add) >> 16;
-    return a < as_f((uint32_t)(127 + LOWEST) << 23) ? sub : normal;
-}
-
 }  // namespace fqdev

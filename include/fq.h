@@ -425,8 +425,8 @@ fq_status fq_qlinear_bwd_retain(const fq_desc *desc_x, const fq_desc *desc_w,
  *   FQ_F8_MX   per 32 consecutive elements the smallest power of two 2^e with
  *              amax <= 448 * 2^e, as E8M0 code clamp(e, -127, 127) + 127 (OCP
  *              MX v1.0's MXFP8 layout): scales uint8 [rows, cols / 32].
- *   FQ_F8_ROW  per row s = max(RN(amax / 448), 2^-126): scales FP32 [rows];
- *              the scaled value is RN(x * RN(1 / s)) clamped to +-448.
+ *   FQ_F8_ROW  per row s = max(RN(amax * RN(1 / 448)), 2^-126): scales FP32
+ *              [rows]; the scaled value is RN(x * RN(1 / s)) clamped to +-448.
  * Codes are nearest even.  A block (row) whose amax is infinite or NaN gets
  * scale code 255 (scale NaN) and codes 0x7F, and stands for NaN.  cols must be
  * a multiple of 32. */
@@ -528,7 +528,7 @@ fq_status fq_moe_combine_bwd(const void *dout_bf16, const void *y_bf16, const fl
  * NULL) the copy that the linears read, g BF16 or FP32.
  * state_type FQ_STATE_F32: m, v FP32 [n].  FQ_STATE_F8: m E4M3 and v E5M2
  * codes [n], m_scale and v_scale FP32 [ceil(n / 128)], a scale per 128
- * consecutive elements: s = max(RN(amax / 448), 2^-126) for m (57344 for v)
+ * consecutive elements: s = max(RN(amax * RN(1 / 448)), 2^-126) for m (57344 for v)
  * with amax over the block's finite values, a = min(|x| RN(1 / s), largest),
  * rounded stochastically: up to the next value exactly when r16 <
  * floor(2^16 * fraction of the way to it), with r16 the low (m) or high (v)

@@ -176,7 +176,7 @@ def quantize_state(x: np.ndarray, r16: np.ndarray, largest: float, table: np.nda
         xb = x[s]
         ok = np.isfinite(xb)
         amax = np.abs(xb[ok]).max() if ok.any() else np.float32(0)
-        scale = max(np.float32(amax / np.float32(largest)), np.float32(TINY))
+        scale = max(np.float32(amax * np.float32(1 / largest)), np.float32(TINY))
         inv = np.float32(1) / scale
         a = np.minimum(np.abs(np.where(ok, xb, 0)) * inv, np.float32(largest)).astype(np.float32)
         c = float8_sr(a.astype(np.float64), r16[s], table)

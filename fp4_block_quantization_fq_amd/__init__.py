@@ -1,7 +1,8 @@
 """Blockwise FP4 (MXFP4 / NVFP4) fake quantization on AMD MI355X (gfx950).
 
-Thin ctypes binding over libfq.so (C ABI in include/fq.h).  Every function
-here only marshals arguments: shapes, device pointers and the current HIP
+Thin binding over libfq.so (C ABI in include/fq.h): ctypes, and for the row
+operators, whose calls can be shorter than that takes, a small extension
+(csrc/fq_binding.cpp).  Every function here only marshals arguments: shapes, device pointers and the current HIP
 stream go to the library, and all arithmetic runs in its HIP kernels.  PyTorch
 supplies device memory and streams.  There is no fallback: if libfq.so is
 missing or a call fails, an exception is raised.
@@ -14,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -277,6 +279,25 @@ def _stream(stream=None):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+_binding_module = None
+
+
+def _binding():
+    """The compiled argument marshalling of the row operators."""
+    global _binding_module
+    if _binding_module is None:
+        lib()                              # loaded first: the extension links to it
+        from . import _fq_binding
+        _binding_module = _fq_binding
+    return _binding_module
+
+
+def _allocating(stream):
+    """Outputs and workspaces that a call makes for itself belong to the stream
+    it runs on, so their memory is not handed out again while it still works."""
+    return nullcontext() if stream is None else _torch().cuda.stream(stream)
 
 
 @dataclass
@@ -676,15 +697,6 @@ def _typed(t, dtype, n: int, name: str):
     return _ptr(t, n * t.element_size(), name)
 
 
-def _scales8(scales, f8: int, rows: int, cols: int):
-    """Pointer of the scales of 8-bit rows."""
-    if scales is None or f8 == FQ_F8_NONE:
-        return _ptr(scales, None, "scales")
-    if f8 == FQ_F8_MX:
-        return _ptr(scales, rows * (cols // 32), "scales", elem=1)
-    return _typed(scales, _torch().float32, rows, "scales")
-
-
 def fq_rmsnorm_fwd(x, gamma, eps: float, res=None, f8: int = FQ_F8_NONE, h=None, y=None,
                    codes=None, scales=None, rstd=None, stream=None):
     """Residual addition and root-mean-square norm of x BF16 [rows, cols].
@@ -694,32 +706,26 @@ def fq_rmsnorm_fwd(x, gamma, eps: float, res=None, f8: int = FQ_F8_NONE, h=None,
     uint8) and scales, and y only if given (the values they stand for).  rstd
     (FP32 [rows], for the backward) is written if given.  Returns (h, y) without
     f8 and (h, codes, scales) with it; h is None without a residual."""
-    torch = _torch()
-    rows, cols = x.shape
-    stream_type = FQ_TYPE_BF16
-    if res is not None:
-        stream_type = _type_of(res, "res")
-        if h is None:
-            h = torch.empty_like(res)
-    if f8 == FQ_F8_NONE:
-        if y is None:
-            y = torch.empty_like(x)
-    elif codes is None or scales is None:
-        if codes is None:
-            codes = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
-        if scales is None:
-            scales = (torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
-                      if f8 == FQ_F8_MX else
-                      torch.empty(rows, dtype=torch.float32, device=x.device))
-    n = rows * cols
-    _check(lib().fq_rmsnorm_fwd(
-        _typed(x, torch.bfloat16, n, "x"),
-        None if res is None else _ptr(res, n * res.element_size(), "res"), stream_type,
-        _ptr(gamma, cols * gamma.element_size(), "gamma"), _type_of(gamma, "gamma"), eps, rows,
-        cols, f8, None if h is None else _typed(h, (x if res is None else res).dtype, n, "h"),
-        _typed(y, torch.bfloat16, n, "y"), _ptr(codes, n, "codes", elem=1),
-        _scales8(scales, f8, rows, cols), _typed(rstd, torch.float32, rows, "rstd"),
-        _stream(stream)))
+    if res is not None and h is None or (y is None if f8 == FQ_F8_NONE
+                                         else codes is None or scales is None):
+        torch = _torch()
+        rows, cols = x.shape
+        with _allocating(stream):
+            if res is not None and h is None:
+                h = torch.empty_like(res)
+            if f8 == FQ_F8_NONE:
+                y = torch.empty_like(x) if y is None else y
+            else:
+                if codes is None:
+                    codes = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+                if scales is None:
+                    scales = (torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
+                              if f8 == FQ_F8_MX else
+                              torch.empty(rows, dtype=torch.float32, device=x.device))
+    st = (_binding_module or _binding()).rmsnorm_fwd(x, gamma, eps, res, f8, h, y, codes, scales,
+                                                     rstd, stream)
+    if st:
+        _check(st)
     return (h, y) if f8 == FQ_F8_NONE else (h, codes, scales)
 
 
@@ -735,26 +741,22 @@ def fq_rmsnorm_bwd(dy, h, gamma, rstd, dres=None, dh=None, dx=None, dgamma=None,
     residual) for the gradient dy of its output; dres is added to dh (and may
     be dh).  dx, if given, receives dh in BF16 beside an FP32 stream.
     need_dgamma=False leaves dgamma out (None)."""
-    torch = _torch()
-    rows, cols = dy.shape
-    n = rows * cols
-    if dh is None:
-        dh = torch.empty_like(h)
     if not need_dgamma:
-        dgamma, ws, nbytes = None, None, 0
-    else:
-        if dgamma is None:
-            dgamma = torch.empty(cols, dtype=torch.float32, device=dy.device)
-        if ws is None:
-            ws = rmsnorm_bwd_workspace(rows, cols, dy.device)
-        nbytes = ws.numel() * ws.element_size()
-    _check(lib().fq_rmsnorm_bwd(
-        _typed(dy, torch.bfloat16, n, "dy"), _ptr(h, n * h.element_size(), "h"),
-        _type_of(h, "h"), _ptr(gamma, cols * gamma.element_size(), "gamma"),
-        _type_of(gamma, "gamma"), _typed(rstd, torch.float32, rows, "rstd"),
-        _typed(dres, h.dtype, n, "dres"), rows, cols, _typed(dh, h.dtype, n, "dh"),
-        _typed(dx, torch.bfloat16, n, "dx"), _typed(dgamma, torch.float32, cols, "dgamma"),
-        _ptr(ws, None, "ws"), nbytes, _stream(stream)))
+        dgamma = ws = None
+    if dh is None or (need_dgamma and (dgamma is None or ws is None)):
+        torch = _torch()
+        rows, cols = dy.shape
+        with _allocating(stream):
+            if dh is None:
+                dh = torch.empty_like(h)
+            if need_dgamma and dgamma is None:
+                dgamma = torch.empty(cols, dtype=torch.float32, device=dy.device)
+            if need_dgamma and ws is None:
+                ws = rmsnorm_bwd_workspace(rows, cols, dy.device)
+    st = (_binding_module or _binding()).rmsnorm_bwd(dy, h, gamma, rstd, dres, dh, dx, dgamma, ws,
+                                                     stream)
+    if st:
+        _check(st)
     return dh, dgamma
 
 
@@ -785,82 +787,67 @@ def fq_moe_sort(experts_of, experts: int, align: int = 1, out: MoeSorted | None 
                 stream=None) -> MoeSorted:
     """Sort the assignments experts_of (int32 [tokens, k]) by expert, each
     expert's segment padded to a multiple of `align` rows."""
-    torch = _torch()
-    tokens, k = experts_of.shape
-    if out is None:
+    if out is None or ws is None:
+        torch = _torch()
+        tokens, k = experts_of.shape
         dev = experts_of.device
-        out = MoeSorted(torch.empty(experts + 1, dtype=torch.int32, device=dev),
-                        torch.empty((tokens, k), dtype=torch.int32, device=dev),
-                        torch.empty(moe_rows(tokens, k, experts, align), dtype=torch.int32,
-                                    device=dev))
-    if ws is None:
-        ws = moe_sort_workspace(tokens, k, experts, experts_of.device)
-    nbytes = ws.numel() * ws.element_size()
-    i32, rows = torch.int32, out.src.numel()
-    _check(lib().fq_moe_sort(
-        _typed(experts_of, i32, tokens * k, "experts_of"), tokens, k, experts, align, rows,
-        _typed(out.offsets, i32, experts + 1, "offsets"), _typed(out.pos, i32, tokens * k, "pos"),
-        _typed(out.src, i32, rows, "src"), _ptr(ws, None, "ws") if nbytes else None, nbytes,
-        _stream(stream)))
+        with _allocating(stream):
+            if out is None:
+                out = MoeSorted(
+                    torch.empty(experts + 1, dtype=torch.int32, device=dev),
+                    torch.empty((tokens, k), dtype=torch.int32, device=dev),
+                    torch.empty(moe_rows(tokens, k, experts, align), dtype=torch.int32,
+                                device=dev))
+            if ws is None:
+                ws = moe_sort_workspace(tokens, k, experts, dev)
+    st = (_binding_module or _binding()).moe_sort(experts_of, experts, align, out.offsets, out.pos,
+                                                  out.src, ws, stream)
+    if st:
+        _check(st)
     return out
-
-
-def _sorted_ptrs(q: MoeSorted):
-    torch = _torch()
-    tokens, k = q.pos.shape
-    return (tokens, k, q.src.numel(), _typed(q.pos, torch.int32, tokens * k, "pos"),
-            _typed(q.src, torch.int32, 0, "src"))
 
 
 def fq_moe_dispatch(x, q: MoeSorted, f8: int = FQ_F8_NONE, scales=None, y=None, stream=None):
     """Rows of the tokens in the sorted order (BF16 [rows, cols], 0 in padding):
     x BF16 [tokens, cols], or the codes of 8-bit rows with their scales."""
-    torch = _torch()
-    tokens, k, rows, pos, src = _sorted_ptrs(q)
-    if x.shape[0] != tokens:
-        raise ValueError(f"x has {x.shape[0]} rows, {tokens} tokens were sorted")
-    cols = x.shape[1]
     if y is None:
-        y = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device)
-    xp = (_typed(x, torch.bfloat16, tokens * cols, "x") if f8 == FQ_F8_NONE
-          else _ptr(x, tokens * cols, "x", elem=1))
-    _check(lib().fq_moe_dispatch(xp, f8, _scales8(scales, f8, tokens, cols), tokens, k, cols, rows,
-                                 pos, src, _typed(y, torch.bfloat16, rows * cols, "y"),
-                                 _stream(stream)))
+        with _allocating(stream):
+            y = _torch().empty((q.src.numel(), x.shape[1]), dtype=_torch().bfloat16,
+                               device=x.device)
+    st = (_binding_module or _binding()).moe_dispatch(x, f8, scales, q.pos, q.src, y, stream)
+    if st:
+        _check(st)
     return y
 
 
 def fq_moe_combine(y, q: MoeSorted, weights=None, out=None, stream=None):
     """out[t] = sum_j weights[t, j] * y[row of (t, j)] (weights None: ones, the
     backward of fq_moe_dispatch)."""
-    torch = _torch()
-    tokens, k, rows, pos, _ = _sorted_ptrs(q)
-    cols = y.shape[1]
     if out is None:
-        out = torch.empty((tokens, cols), dtype=torch.bfloat16, device=y.device)
-    _check(lib().fq_moe_combine(_typed(y, torch.bfloat16, rows * cols, "y"),
-                                _typed(weights, torch.float32, tokens * k, "weights"), tokens, k,
-                                cols, rows, pos,
-                                _typed(out, torch.bfloat16, tokens * cols, "out"),
-                                _stream(stream)))
+        with _allocating(stream):
+            out = _torch().empty((q.pos.shape[0], y.shape[1]), dtype=_torch().bfloat16,
+                                 device=y.device)
+    st = (_binding_module or _binding()).moe_combine(y, weights, q.pos, q.src, out, stream)
+    if st:
+        _check(st)
     return out
 
 
 def fq_moe_combine_bwd(dout, y, q: MoeSorted, weights, dy=None, dweights=None, stream=None):
     """(dy [rows, cols] BF16, dweights [tokens, k] FP32) of fq_moe_combine."""
-    torch = _torch()
-    tokens, k, rows, pos, src = _sorted_ptrs(q)
-    cols = dout.shape[1]
-    if dy is None:
-        dy = torch.empty((rows, cols), dtype=torch.bfloat16, device=dout.device)
-    if dweights is None:
-        dweights = torch.empty((tokens, k), dtype=torch.float32, device=dout.device)
-    _check(lib().fq_moe_combine_bwd(
-        _typed(dout, torch.bfloat16, tokens * cols, "dout"),
-        _typed(y, torch.bfloat16, rows * cols, "y"),
-        _typed(weights, torch.float32, tokens * k, "weights"), tokens, k, cols, rows, pos, src,
-        _typed(dy, torch.bfloat16, rows * cols, "dy"),
-        _typed(dweights, torch.float32, tokens * k, "dweights"), _stream(stream)))
+    if dy is None or dweights is None:
+        torch = _torch()
+        with _allocating(stream):
+            if dy is None:
+                dy = torch.empty((q.src.numel(), dout.shape[1]), dtype=torch.bfloat16,
+                                 device=dout.device)
+            if dweights is None:
+                dweights = torch.empty(tuple(q.pos.shape), dtype=torch.float32,
+                                       device=dout.device)
+    st = (_binding_module or _binding()).moe_combine_bwd(dout, y, weights, q.pos, q.src, dy,
+                                                         dweights, stream)
+    if st:
+        _check(st)
     return dy, dweights
 
 
@@ -901,7 +888,7 @@ class AdamWPlan:
         self.tensors = list(tensors)
         self.array = (FqAdamWTensor * len(self.tensors))()
         self.f8 = bool(self.tensors) and self.tensors[0].m.dtype != torch.float32
-        self.hyper = FqAdamWHyper(state_type=FQ_STATE_F8 if self.f8 else FQ_STATE_F32)
+        self.table = ctypes.addressof(self.array)
         for i, (s, t) in enumerate(zip(self.array, self.tensors)):
             n, name = t.w.numel(), f"tensor {i}: "
             s.n = n
@@ -929,10 +916,11 @@ def fq_adamw_step(plan: AdamWPlan, lr: float, step: int, beta1: float = 0.9, bet
     """One AdamW step (in place) over a plan's tensors.  step counts from 1;
     grad_scale is an FP32 device scalar the gradients are multiplied by; seed
     keys the stochastic rounding of 8-bit moments."""
-    h = plan.hyper
-    h.lr, h.beta1, h.beta2, h.eps, h.step, h.seed = lr, beta1, beta2, eps, step, seed
-    h.grad_scale = _typed(grad_scale, _torch().float32, 1, "grad_scale")
-    _check(lib().fq_adamw_step(ctypes.byref(h), plan.array, len(plan.tensors), _stream(stream)))
+    st = (_binding_module or _binding()).adamw_step(
+        plan.table, len(plan.array), FQ_STATE_F8 if plan.f8 else FQ_STATE_F32, lr, beta1, beta2,
+        eps, step, seed, grad_scale, stream)
+    if st:
+        _check(st)
 
 
 def version() -> str:

@@ -9,13 +9,18 @@
 //
 // Both passes are bound by memory: one read of every input and one write of
 // every output, a row staying in registers between the statistic and its use.
-//  * WPR waves share a row, each lane holding NCH chunks of 8 consecutive
-//    elements (16-byte BF16 accesses); chunk i of lane l of the row's lanes is
-//    i * 64 * WPR + l, so every access of a wave covers 1 KB.
+//  * LANES lanes share a row (8 for a row of 64 elements, up to a workgroup of
+//    1024), each holding NCH chunks of 8 consecutive elements (16-byte BF16
+//    accesses); chunk i of lane l is i * LANES + l, so neighbouring lanes read
+//    neighbouring chunks.  One chunk a lane up to 8192 columns: many short
+//    waves keep the loads of some rows in flight while others wait for their
+//    sum (16384x4096 with 8-bit output: 512 lanes 100 us, 256 lanes of two
+//    chunks 107, 64 of eight 113; backward 8192x2880: 37.1, 39.5 and 41.2).
 //  * An MX block of 32 is four neighbouring lanes (two DPP steps).
-//  * dgamma: each group of WPR waves walks over rows and keeps its column sums
-//    in registers; they go to the workspace once, and a second kernel adds the
-//    groups in a fixed order (no atomics, the same bits on every call).
+//  * dgamma: each group of lanes walks over rows and keeps its column sums in
+//    registers; the groups of a workgroup are added through LDS, the
+//    workgroups' sums go to the workspace, and a second kernel adds those, all
+//    in a fixed order (no atomics, the same bits on every call).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -26,39 +31,52 @@ using namespace fqdev;
 
 namespace {
 
-// Sum / maximum over the WPR waves of a row.  `slot` alternates per use so
-// that one barrier between writing and reading is enough.
-template <int WPR>
-__device__ __forceinline__ float row_sum(float v, float (*red)[16], int slot)
+// Threads of a workgroup, or one row's lanes.  The backward's are more, because
+// each workgroup leaves a row of column sums (32768x1024: 512 workgroups
+// of 512 threads 47.5 us, of 256 52.0).
+constexpr int kFwdThreads = 256, kBwdThreads = 512;
+template <int LANES, int LEAST>
+constexpr int threads_of() { return LANES <= LEAST ? LEAST : LANES; }
+
+// Which of the workgroup's rows this lane works on: the same one for a whole
+// wave where a row has at least one, so that addresses are a scalar base and a
+// 32-bit offset.
+template <int LANES>
+__device__ __forceinline__ int group_of()
 {
-    v = wave_sum(v);
-    if (WPR == 1) return v;
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) red[slot][wave] = v;
-    __syncthreads();
-    const int first = wave / WPR * WPR;
-    v = red[slot][first];
-#pragma unroll
-    for (int w = 1; w < WPR; ++w) v += red[slot][first + w];
-    return v;
-}
-template <int WPR>
-__device__ __forceinline__ uint32_t row_max(uint32_t v, float (*red)[16], int slot)
-{
-    v = wave_max(v);
-    if (WPR == 1) return v;
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) red[slot][wave] = as_f(v);
-    __syncthreads();
-    const int first = wave / WPR * WPR;
-    v = as_u(red[slot][first]);
-#pragma unroll
-    for (int w = 1; w < WPR; ++w) v = max(v, as_u(red[slot][first + w]));
-    return v;
+    const int g = threadIdx.x / LANES;
+    return LANES >= 64 ? __builtin_amdgcn_readfirstlane(g) : g;
 }
 
-template <int WPR>
-constexpr int threads_of() { return WPR <= 4 ? 256 : WPR * 64; }
+// Sum / maximum over the lanes of a row.  Where a row has several waves, `slot`
+// is another one than the previous reduction's, so that one barrier between
+// writing and reading is enough.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v, float (*red)[16], int slot)
+{
+    if (LANES <= 64) return lanes_sum<LANES>(v);
+    v = wave_sum(v);
+    const int wave = threadIdx.x >> 6, first = group_of<LANES>() * (LANES / 64);
+    if ((threadIdx.x & 63) == 0) red[slot][wave] = v;
+    __syncthreads();
+    v = red[slot][first];
+#pragma unroll
+    for (int w = 1; w < LANES / 64; ++w) v += red[slot][first + w];
+    return v;
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, float (*red)[16], int slot)
+{
+    if (LANES <= 64) return lanes_max<LANES>(v);
+    v = lanes_max<64>(v);
+    const int wave = threadIdx.x >> 6, first = group_of<LANES>() * (LANES / 64);
+    if ((threadIdx.x & 63) == 0) red[slot][wave] = as_f(v);
+    __syncthreads();
+    v = as_u(red[slot][first]);
+#pragma unroll
+    for (int w = 1; w < LANES / 64; ++w) v = max(v, as_u(red[slot][first + w]));
+    return v;
+}
 
 // gamma of eight columns in either type
 template <bool ANY>
@@ -73,226 +91,307 @@ template <int STREAM> struct StreamType { typedef uint16_t type; };
 template <> struct StreamType<2> { typedef float type; };
 
 // STREAM: 0 no residual (h = x), 1 BF16 residual, 2 FP32 residual.
-template <int WPR, int NCH, int STREAM, int F8, bool ANY>
-__global__ __launch_bounds__(threads_of<WPR>()) void k_rmsnorm_fwd(fqimpl::NormFwdArgs a)
+template <int LANES, int NCH, int STREAM, int F8, bool ANY, bool NT>
+__global__ __launch_bounds__((threads_of<LANES, kFwdThreads>())) void k_rmsnorm_fwd(fqimpl::NormFwdArgs a)
 {
     typedef typename StreamType<STREAM>::type T;
-    constexpr int kGroups = threads_of<WPR>() / 64 / WPR;      // rows per workgroup
-    __shared__ float red[2][16];
-    const int wave = threadIdx.x >> 6, l = (wave % WPR) * 64 + (threadIdx.x & 63);
-    const int64_t row = (int64_t)blockIdx.x * kGroups + wave / WPR;
-    const bool live = row < a.rows;
-    const int64_t base = (live ? row : 0) * a.cols;
-    float h[NCH][8];
-    float ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-        const int c = (i * WPR * 64 + l) * 8;
-        const int n = live ? min(8, (int)a.cols - c) : 0;
-        if (n <= 0) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
-            continue;
-        }
-        load8<ANY>((const uint16_t *)a.x + base + c, n, h[i]);
-        if (STREAM) {
-            float r[8];
-            load8<ANY>((const T *)a.res + base + c, n, r);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                h[i][e] = h[i][e] + r[e];
-                // the norm sees the stream's stored value, as the backward will
-                if (STREAM == 1) h[i][e] = (float)(__bf16)h[i][e];
-            }
-            store8<ANY>((T *)a.h + base + c, n, h[i]);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss += h[i][e] * h[i][e];
-    }
-    const float rstd = 1.0f / __builtin_sqrtf(row_sum<WPR>(ss, red, 0) / (float)a.cols + a.eps);
-    if (a.rstd && live && l == 0) a.rstd[row] = rstd;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-        const int c = (i * WPR * 64 + l) * 8;
-        const int n = live ? min(8, (int)a.cols - c) : 0;
-        if (n <= 0) continue;
-        float g[8];
-        load_gamma<ANY>(a.gamma, a.gamma_f32, c, n, g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] = (h[i][e] * rstd) * g[e];
-    }
-    uint32_t top = 0;
-    float scale = 0.0f, inv = 0.0f;
-    if (F8 == fqimpl::F8_ROW) {
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) top = max(top, absmax8(h[i]));
-        top = row_max<WPR>(top, red, 1);
-        scale = __builtin_fmaxf(as_f(top) * (1.0f / 448.0f), 0x1p-126f);
-        inv = 1.0f / scale;
-        if (top >= 0x7F800000u) scale = as_f(0x7FC00000u);
-        if (a.scales && live && l == 0) ((float *)a.scales)[row] = scale;
-    }
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-        const int c = (i * WPR * 64 + l) * 8;
-        const int n = live ? min(8, (int)a.cols - c) : 0;
-        if (n <= 0) continue;
-        if (F8 != fqimpl::F8_NONE) {
-            if (F8 == fqimpl::F8_MX) {
-                top = dpp_max_xor2(dpp_max_xor1(absmax8(h[i])));
-                const uint32_t code = mx8_scale_code(top);
-                scale = e8m0_value(code);
-                inv = e8m0_recip(code);
-                if (top >= 0x7F800000u) scale = as_f(0x7FC00000u);
-                if (a.scales && (l & 3) == 0)
-                    ((uint8_t *)a.scales)[(base + c) >> 5] = (uint8_t)(top >= 0x7F800000u ? 255u : code);
-            }
-            float q[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                q[e] = F8 == fqimpl::F8_MX ? h[i][e] * inv
-                                           : __builtin_fminf(__builtin_fmaxf(h[i][e] * inv, -448.0f), 448.0f);
-            u32w2 codes = e4m3_encode8(q);
-            if (top >= 0x7F800000u) codes = (u32w2){0x7F7F7F7Fu, 0x7F7F7F7Fu};
-            if (a.codes) *(u32w2 *)((uint8_t *)a.codes + base + c) = codes;
-            if (a.y) {
-                e4m3_decode8(codes, q);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) h[i][e] = q[e] * scale;
-            }
-        }
-        if (a.y) store8<ANY>((uint16_t *)a.y + base + c, n, h[i]);
-    }
-}
-
-// One group of WPR waves walks over rows group, group + groups, ...; T is the
-// stream's type (h, dres, dh).
-template <int WPR, int NCH, typename T, bool ANY>
-__global__ __launch_bounds__(threads_of<WPR>()) void k_rmsnorm_bwd(fqimpl::NormBwdArgs a)
-{
-    constexpr int kGroups = threads_of<WPR>() / 64 / WPR;
-    __shared__ float red[2][16];
-    const int wave = threadIdx.x >> 6, l = (wave % WPR) * 64 + (threadIdx.x & 63);
-    const int64_t group = (int64_t)blockIdx.x * kGroups + wave / WPR;
-    const int64_t groups = (int64_t)gridDim.x * kGroups;
-    const float inv_cols = 1.0f / (float)a.cols;
-    float gamma[NCH][8], acc[NCH][8];
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-        const int c = (i * WPR * 64 + l) * 8;
-        const int n = min(8, (int)a.cols - c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) gamma[i][e] = acc[i][e] = 0.0f;
-        if (n > 0) load_gamma<ANY>(a.gamma, a.gamma_f32, c, n, gamma[i]);
-    }
+    constexpr int kGroups = threads_of<LANES, kFwdThreads>() / LANES;      // rows per workgroup
+    __shared__ float red[4][16];
+    const uint32_t l = threadIdx.x % LANES;
+    const int group = group_of<LANES>();
     int slot = 0;
-    // every wave of a workgroup makes the same number of turns (row_sum's barrier)
-    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.rows; r0 += groups) {
-        const int64_t row = r0 + wave / WPR;
+    // every lane of a workgroup makes the same number of turns (the barriers)
+    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.rows; r0 += (int64_t)gridDim.x * kGroups) {
+        const int64_t row = r0 + group;
         const bool live = row < a.rows;
         const int64_t base = (live ? row : 0) * a.cols;
-        const float r = live ? a.rstd[row] : 0.0f;
-        float xh[NCH][8], g[NCH][8];
-        float dot = 0.0f;
+        float h[NCH][8];
+        float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            const int c = (i * WPR * 64 + l) * 8;
-            const int n = live ? min(8, (int)a.cols - c) : 0;
+            const uint32_t c = (i * LANES + l) * 8;
+            const int n = live ? min(8, (int)a.cols - (int)c) : 0;
             if (n <= 0) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) xh[i][e] = g[i][e] = 0.0f;
+                for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
                 continue;
             }
-            load8<ANY>((const T *)a.h + base + c, n, xh[i]);
-            load8<ANY>((const uint16_t *)a.dy + base + c, n, g[i]);
+            load8<ANY, NT>((const uint16_t *)a.x + base + c, n, h[i]);
+            if (STREAM) {
+                float r[8];
+                load8<ANY, NT>((const T *)a.res + base + c, n, r);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                xh[i][e] = xh[i][e] * r;
-                acc[i][e] += g[i][e] * xh[i][e];
-                g[i][e] = g[i][e] * gamma[i][e];
-                dot += g[i][e] * xh[i][e];
+                for (int e = 0; e < 8; ++e) {
+                    h[i][e] = h[i][e] + r[e];
+                    // the norm sees the stream's stored value, as the backward will
+                    if (STREAM == 1) h[i][e] = (float)(__bf16)h[i][e];
+                }
+                store8<ANY, NT>((T *)a.h + base + c, n, h[i]);
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss += h[i][e] * h[i][e];
         }
-        dot = row_sum<WPR>(dot, red, slot) * inv_cols;
+        const float rstd = 1.0f / __builtin_sqrtf(row_sum<LANES>(ss, red, slot) / (float)a.cols + a.eps);
+        if (a.rstd && live && l == 0) a.rstd[row] = rstd;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const uint32_t c = (i * LANES + l) * 8;
+            const int n = live ? min(8, (int)a.cols - (int)c) : 0;
+            if (n <= 0) continue;
+            float g[8];
+            load_gamma<ANY>(a.gamma, a.gamma_f32, c, n, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[i][e] = (h[i][e] * rstd) * g[e];
+        }
+        uint32_t top = 0;
+        float scale = 0.0f, inv = 0.0f;
+        if (F8 == fqimpl::F8_ROW) {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) top = max(top, absmax8(h[i]));
+            top = row_max<LANES>(top, red, 2 + slot);
+            scale = __builtin_fmaxf(as_f(top) * (1.0f / 448.0f), 0x1p-126f);
+            inv = 1.0f / scale;
+            if (top >= 0x7F800000u) scale = as_f(0x7FC00000u);
+            if (a.scales && live && l == 0) ((float *)a.scales)[row] = scale;
+        }
         slot ^= 1;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            const int c = (i * WPR * 64 + l) * 8;
-            const int n = live ? min(8, (int)a.cols - c) : 0;
+            const uint32_t c = (i * LANES + l) * 8;
+            const int n = live ? min(8, (int)a.cols - (int)c) : 0;
             if (n <= 0) continue;
+            if (F8 != fqimpl::F8_NONE) {
+                if (F8 == fqimpl::F8_MX) {
+                    top = dpp_max_xor2(dpp_max_xor1(absmax8(h[i])));
+                    const uint32_t code = mx8_scale_code(top);
+                    scale = e8m0_value(code);
+                    inv = e8m0_recip(code);
+                    if (top >= 0x7F800000u) scale = as_f(0x7FC00000u);
+                    if (a.scales && (l & 3) == 0)
+                        ((uint8_t *)a.scales)[(base + c) >> 5] = (uint8_t)(top >= 0x7F800000u ? 255u : code);
+                }
+                float q[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[i][e] = r * (g[i][e] - xh[i][e] * dot);
-            if (a.dres) {
-                load8<ANY>((const T *)a.dres + base + c, n, xh[i]);
+                for (int e = 0; e < 8; ++e)
+                    q[e] = F8 == fqimpl::F8_MX ? h[i][e] * inv
+                                               : __builtin_fminf(__builtin_fmaxf(h[i][e] * inv, -448.0f), 448.0f);
+                u32w2 codes = e4m3_encode8(q);
+                if (top >= 0x7F800000u) codes = (u32w2){0x7F7F7F7Fu, 0x7F7F7F7Fu};
+                if (a.codes) {
+                    u32w2 *p = (u32w2 *)((uint8_t *)a.codes + base + c);
+                    if (NT) __builtin_nontemporal_store(codes, p);
+                    else *p = codes;
+                }
+                if (a.y) {
+                    e4m3_decode8(codes, q);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) g[i][e] += xh[i][e];
+                    for (int e = 0; e < 8; ++e) h[i][e] = q[e] * scale;
+                }
             }
-            store8<ANY>((T *)a.dh + base + c, n, g[i]);
-            if (a.dx) store8<ANY>((uint16_t *)a.dx + base + c, n, g[i]);
+            if (a.y) store8<ANY, NT>((uint16_t *)a.y + base + c, n, h[i]);
         }
-    }
-    if (!a.partials) return;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-        const int c = (i * WPR * 64 + l) * 8;
-        const int n = min(8, (int)a.cols - c);
-        if (n > 0) store8<ANY>(a.partials + group * a.cols + c, n, acc[i]);
     }
 }
 
-// dgamma[c] = sum over groups, in the groups' order: a workgroup takes 64
-// columns, its waves every 16th group, and wave 0 adds the 16 sums.
-constexpr int kSumThreads = 1024;
+// ---- backward -----------------------------------------------------------------
+// Stops the compiler from carrying values computed from r across this point:
+// they are computed from it again.
+__device__ __forceinline__ void renew(Raw8<uint16_t> &r) { asm volatile("" : "+v"(r.w)); }
+__device__ __forceinline__ void renew(Raw8<float> &r)
+{
+    asm volatile("" : "+v"(r.a));
+    asm volatile("" : "+v"(r.b));
+}
+
+// A group of LANES lanes walks over rows group, group + groups, ...; T is the
+// stream's type (h, dres, dh).  What bounds the walk is the number of bytes a
+// CU has in flight, so all of a row's loads are issued together, and the row
+// stays as it was loaded (a BF16 element in half a register) and is unpacked
+// twice, before and after the row's sum; gamma waits in LDS.
+template <int LANES, int NCH, typename T, bool ANY, bool NT>
+__global__ __launch_bounds__((threads_of<LANES, kBwdThreads>()), 2) void k_rmsnorm_bwd(fqimpl::NormBwdArgs a)
+{
+    constexpr int kWgThreads = threads_of<LANES, kBwdThreads>(), kGroups = kWgThreads / LANES;
+    // dres with the other loads, unless it is wide and a lane's share long
+    constexpr bool kEarly = sizeof(T) == 2 || NCH <= 4;
+    __shared__ float red[2][16];
+    __shared__ float sums[kGroups > 1 ? kGroups : 1][kGroups > 1 ? LANES * 8 : 1];
+    __shared__ u32w4 gamma[NCH * 2][LANES];
+    const uint32_t l = threadIdx.x % LANES;
+    const int group = group_of<LANES>();
+    const int64_t groups = (int64_t)gridDim.x * kGroups;
+    const float inv_cols = 1.0f / (float)a.cols;
+    float acc[NCH][8];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
+        if (i % kGroups != group) continue;
+        const uint32_t c = (i * LANES + l) * 8;
+        const int n = min(8, (int)a.cols - (int)c);
+        float g[8] = {};
+        if (n > 0) load_gamma<ANY>(a.gamma, a.gamma_f32, c, n, g);
+        gamma[2 * i][l] = (u32w4){as_u(g[0]), as_u(g[1]), as_u(g[2]), as_u(g[3])};
+        gamma[2 * i + 1][l] = (u32w4){as_u(g[4]), as_u(g[5]), as_u(g[6]), as_u(g[7])};
+    }
+    __syncthreads();
+    int slot = 0;
+    // every lane of a workgroup makes the same number of turns (row_sum's barrier)
+    for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.rows; r0 += groups) {
+        const int64_t row = r0 + group;
+        const bool live = row < a.rows;
+        const int64_t base = (live ? row : 0) * a.cols;
+        Raw8<uint16_t> dy[NCH] = {};
+        Raw8<T> h[NCH] = {}, dres[kEarly ? NCH : 1] = {};
+        const float r = live ? a.rstd[row] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const uint32_t c = (i * LANES + l) * 8;
+            const int n = live ? min(8, (int)a.cols - (int)c) : 0;
+            if (n <= 0) continue;
+            load_raw8<ANY, NT>((const T *)a.h + base + c, n, h[i]);
+            load_raw8<ANY, NT>((const uint16_t *)a.dy + base + c, n, dy[i]);
+            if (kEarly && a.dres) load_raw8<ANY, NT>((const T *)a.dres + base + c, n, dres[kEarly ? i : 0]);
+        }
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            float xh[8], d[8], g[8];
+            unpack8(h[i], xh);
+            unpack8(dy[i], d);
+            unpack8(Raw8<float>{gamma[2 * i][l], gamma[2 * i + 1][l]}, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                xh[e] = xh[e] * r;
+                acc[i][e] = __builtin_fmaf(d[e], xh[e], acc[i][e]);
+                dot = __builtin_fmaf(d[e] * g[e], xh[e], dot);
+                asm volatile("" : "+v"(acc[i][e]));      // added here, not at the turn's end
+            }
+            renew(h[i]);
+            renew(dy[i]);
+            __builtin_amdgcn_sched_barrier(0);   // one chunk's temporaries at a time
+        }
+        dot = row_sum<LANES>(dot, red, slot) * inv_cols;
+        slot ^= 1;
+        asm volatile("" ::: "memory");           // gamma is read again
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const uint32_t c = (i * LANES + l) * 8;
+            const int n = live ? min(8, (int)a.cols - (int)c) : 0;
+            if (n <= 0) continue;
+            float xh[8], d[8], g[8], o[8];
+            if (!kEarly && a.dres) load_raw8<ANY, NT>((const T *)a.dres + base + c, n, dres[0]);
+            unpack8(h[i], xh);
+            unpack8(dy[i], d);
+            unpack8(Raw8<float>{gamma[2 * i][l], gamma[2 * i + 1][l]}, g);
+            unpack8(dres[kEarly ? i : 0], o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                o[e] = __builtin_fmaf(r, __builtin_fmaf(-(xh[e] * r), dot, d[e] * g[e]), o[e]);
+            store8<ANY, NT>((T *)a.dh + base + c, n, o);
+            if (a.dx) store8<ANY, NT>((uint16_t *)a.dx + base + c, n, o);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    if (!a.partials) return;
+    // the workgroup's column sums, LANES * 8 columns at a time
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        if (i * LANES * 8 >= a.cols) break;
+        if (kGroups > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sums[group][l * 8 + e] = acc[i][e];
+            __syncthreads();
+            for (int k = threadIdx.x; k < LANES * 8; k += kWgThreads) {
+                const int c = i * LANES * 8 + k;
+                if (c >= a.cols) break;
+                float v = sums[0][k];
+#pragma unroll 8
+                for (int g = 1; g < kGroups; ++g) v += sums[g][k];
+                a.partials[(int64_t)blockIdx.x * a.cols + c] = v;
+            }
+        } else {
+            const uint32_t c = (i * LANES + l) * 8;
+        const int n = min(8, (int)a.cols - (int)c);
+            if (n > 0) store8<ANY>(a.partials + (int64_t)blockIdx.x * a.cols + c, n, acc[i]);
+        }
+    }
+}
+
+// dgamma[c] = sum over the workgroups' sums, in their order: a workgroup takes
+// 16 columns (64-byte pieces of a row), 64 threads each a contiguous share of
+// the rows, and one adds their sums.
+constexpr int kSumCols = 16, kSumThreads = 1024, kSumParts = kSumThreads / kSumCols;
 __global__ __launch_bounds__(kSumThreads) void k_column_sum(const float *__restrict__ partials,
                                                             int64_t groups, int64_t cols,
                                                             float *__restrict__ out)
 {
-    __shared__ float s[kSumThreads / 64][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    __shared__ float s[kSumParts][kSumCols];
+    const int k = threadIdx.x % kSumCols, part = threadIdx.x / kSumCols;
+    const int64_t c = (int64_t)blockIdx.x * kSumCols + k;
     float v = 0.0f;
     if (c < cols)
 #pragma unroll 8
-        for (int64_t g = wave; g < groups; g += kSumThreads / 64) v += partials[g * cols + c];
-    s[wave][lane] = v;
+        for (int64_t g = part; g < groups; g += kSumParts) v += partials[g * cols + c];
+    s[part][k] = v;
     __syncthreads();
-    if (wave || c >= cols) return;
-#pragma unroll
-    for (int w = 1; w < kSumThreads / 64; ++w) v += s[w][lane];
+    if (part || c >= cols) return;
+#pragma unroll 8
+    for (int w = 1; w < kSumParts; ++w) v += s[w][k];
     out[c] = v;
 }
 
 // ---- launch -------------------------------------------------------------------
-// Waves per row and chunks per lane from the width alone.
+// Lanes of a row and chunks per lane from the width alone.
 template <template <int, int> class F, typename A>
 hipError_t by_width(const A &a, hipStream_t st)
 {
-    if (a.cols <= 512) return F<1, 1>::go(a, st);
-    if (a.cols <= 1024) return F<1, 2>::go(a, st);
-    if (a.cols <= 2048) return F<1, 4>::go(a, st);
-    if (a.cols <= 4096) return F<4, 2>::go(a, st);
-    if (a.cols <= 8192) return F<4, 4>::go(a, st);
-    if (a.cols <= 16384) return F<16, 2>::go(a, st);
-    return F<16, 4>::go(a, st);
+    if (a.cols <= 64) return F<8, 1>::go(a, st);
+    if (a.cols <= 128) return F<16, 1>::go(a, st);
+    if (a.cols <= 256) return F<32, 1>::go(a, st);
+    if (a.cols <= 512) return F<64, 1>::go(a, st);
+    if (a.cols <= 1024) return F<128, 1>::go(a, st);
+    if (a.cols <= 2048) return F<256, 1>::go(a, st);
+    if (a.cols <= 4096) return F<512, 1>::go(a, st);
+    if (a.cols <= 8192) return F<1024, 1>::go(a, st);
+    if (a.cols <= 16384) return F<1024, 2>::go(a, st);
+    return F<F<1024, 1>::kLanesMost, 4096 / F<1024, 1>::kLanesMost>::go(a, st);
 }
 
-template <int WPR, int NCH>
+// A grid holds fewer than 2^32 lanes; the kernels walk over what is left.
+constexpr int64_t kMaxGrid = int64_t(1) << 20;
+// Streaming accesses from this many elements on: what a call reads and writes
+// no longer stays in the caches for the next one (forward with 8-bit output
+// 4096x4096: 27.1 us streaming, 32.0 not; 2048x4096: 15.4 and 14.2; backward
+// 31.2 and 32.3, 21.6 and 18.1).
+constexpr int64_t kStreamElems = int64_t(1) << 24;
+
+template <int LANES, int NCH>
 struct Fwd {
-    template <int STREAM, int F8, bool ANY>
+    static constexpr int kLanesMost = 1024;
+    template <int STREAM, int F8, bool ANY, bool NT>
     static hipError_t launch(const fqimpl::NormFwdArgs &a, hipStream_t st)
     {
-        constexpr int kThreads = threads_of<WPR>(), kGroups = kThreads / 64 / WPR;
-        k_rmsnorm_fwd<WPR, NCH, STREAM, F8, ANY>
-            <<<dim3((uint32_t)((a.rows + kGroups - 1) / kGroups)), dim3(kThreads), 0, st>>>(a);
+        constexpr int kWgThreads = threads_of<LANES, kFwdThreads>(), kGroups = kWgThreads / LANES;
+        const int64_t wgs = (a.rows + kGroups - 1) / kGroups;
+        k_rmsnorm_fwd<LANES, NCH, STREAM, F8, ANY, NT>
+            <<<dim3((uint32_t)(wgs < kMaxGrid ? wgs : kMaxGrid)), dim3(kWgThreads), 0, st>>>(a);
         return hipGetLastError();
+    }
+    template <int STREAM, int F8>
+    static hipError_t by_size(const fqimpl::NormFwdArgs &a, hipStream_t st)
+    {
+        return a.rows * a.cols < kStreamElems ? launch<STREAM, F8, false, false>(a, st)
+                                              : launch<STREAM, F8, false, true>(a, st);
     }
     template <int STREAM>
     static hipError_t by_output(const fqimpl::NormFwdArgs &a, hipStream_t st)
     {
-        if (a.f8 == fqimpl::F8_MX) return launch<STREAM, fqimpl::F8_MX, false>(a, st);
-        if (a.f8 == fqimpl::F8_ROW) return launch<STREAM, fqimpl::F8_ROW, false>(a, st);
-        return a.cols % 8 ? launch<STREAM, fqimpl::F8_NONE, true>(a, st)
-                          : launch<STREAM, fqimpl::F8_NONE, false>(a, st);
+        if (a.f8 == fqimpl::F8_MX) return by_size<STREAM, fqimpl::F8_MX>(a, st);
+        if (a.f8 == fqimpl::F8_ROW) return by_size<STREAM, fqimpl::F8_ROW>(a, st);
+        return a.cols % 8 ? launch<STREAM, fqimpl::F8_NONE, true, false>(a, st)
+                          : by_size<STREAM, fqimpl::F8_NONE>(a, st);
     }
     static hipError_t go(const fqimpl::NormFwdArgs &a, hipStream_t st)
     {
@@ -301,15 +400,16 @@ struct Fwd {
     }
 };
 
-template <int WPR, int NCH>
+template <int LANES, int NCH>
 struct Bwd {
+    static constexpr int kLanesMost = 512;      // 1024 lanes would have 128 registers each: too few
     template <typename T>
     static hipError_t launch(const fqimpl::NormBwdArgs &a, hipStream_t st)
     {
-        constexpr int kThreads = threads_of<WPR>(), kGroups = kThreads / 64 / WPR;
-        const uint32_t grid = (uint32_t)(a.groups / kGroups);
-        if (a.cols % 8) k_rmsnorm_bwd<WPR, NCH, T, true><<<dim3(grid), dim3(kThreads), 0, st>>>(a);
-        else k_rmsnorm_bwd<WPR, NCH, T, false><<<dim3(grid), dim3(kThreads), 0, st>>>(a);
+        const dim3 grid((uint32_t)a.groups), block(threads_of<LANES, kBwdThreads>());
+        if (a.cols % 8) k_rmsnorm_bwd<LANES, NCH, T, true, false><<<grid, block, 0, st>>>(a);
+        else if (a.rows * a.cols < kStreamElems) k_rmsnorm_bwd<LANES, NCH, T, false, false><<<grid, block, 0, st>>>(a);
+        else k_rmsnorm_bwd<LANES, NCH, T, false, true><<<grid, block, 0, st>>>(a);
         return hipGetLastError();
     }
     static hipError_t go(const fqimpl::NormBwdArgs &a, hipStream_t st)
@@ -327,13 +427,16 @@ hipError_t launch_rmsnorm_fwd(const NormFwdArgs &a, hipStream_t stream)
     return by_width<Fwd>(a, stream);
 }
 
-// Groups of waves that walk over the rows, a multiple of the groups of a
-// workgroup: enough for two workgroups on each of 256 CUs, no more than rows.
+// Workgroups that walk over the rows, each leaving a row of column sums: two
+// on each of 256 CUs, one where a row has 1024 lanes (or 512 with many
+// registers), no more than there are rows for.
 int64_t rmsnorm_bwd_groups(int64_t rows, int64_t cols)
 {
-    const int64_t per_wg = cols <= 2048 ? 4 : 1;
-    const int64_t wgs = (rows + per_wg - 1) / per_wg;
-    return (wgs < 512 ? wgs : 512) * per_wg;
+    int64_t lanes = 8;
+    while (lanes < 1024 && lanes * 8 < cols) lanes *= 2;
+    const int64_t per_wg = lanes < kBwdThreads ? kBwdThreads / lanes : 1;
+    const int64_t wgs = (rows + per_wg - 1) / per_wg, most = lanes < 1024 ? 512 : 256;
+    return wgs < most ? wgs : most;
 }
 
 hipError_t launch_rmsnorm_bwd(NormBwdArgs a, float *dgamma, hipStream_t stream)
@@ -342,7 +445,7 @@ hipError_t launch_rmsnorm_bwd(NormBwdArgs a, float *dgamma, hipStream_t stream)
     if (!dgamma) a.partials = nullptr;
     hipError_t e = by_width<Bwd>(a, stream);
     if (e != hipSuccess || !dgamma) return e;
-    k_column_sum<<<dim3((uint32_t)((a.cols + 63) / 64)), dim3(kSumThreads), 0, stream>>>(
+    k_column_sum<<<dim3((uint32_t)((a.cols + kSumCols - 1) / kSumCols)), dim3(kSumThreads), 0, stream>>>(
         a.partials, a.groups, a.cols, dgamma);
     return hipGetLastError();
 }

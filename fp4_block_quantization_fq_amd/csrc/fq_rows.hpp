@@ -21,118 +21,150 @@ typedef u32w4 u32w4_any4 __attribute__((aligned(4)));
 // `n` of them exist (8, or fewer in the last chunk of a row whose length is
 // no multiple of 8); missing ones read as 0 and are not written.  ANY: the
 // row may start at any element; gfx950 serves the 16-byte access at element
-// alignment, so only the last chunk goes element by element.
-template <bool ANY>
-__device__ __forceinline__ void load8(const uint16_t *__restrict__ p, int n, float (&v)[8])
+// alignment, so only the last chunk goes element by element.  NT: streaming
+// accesses, for calls whose data is larger than the caches.
+template <bool NT, typename V>
+__device__ __forceinline__ u32w4 load16(const V *p)
 {
-    u32w4 w;
-    if (ANY) {
-        if (n < 8) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < n ? as_f((uint32_t)p[i] << 16) : 0.0f;
-            return;
-        }
-        w = *reinterpret_cast<const u32w4_any *>(p);
+    if (NT) return __builtin_nontemporal_load(reinterpret_cast<const u32w4 *>(p));
+    return *p;
+}
+template <bool NT, typename V>
+__device__ __forceinline__ void store16(V *p, u32w4 v)
+{
+    if (NT) __builtin_nontemporal_store(v, reinterpret_cast<u32w4 *>(p));
+    else *p = v;
+}
+
+// as loaded: 4 registers of BF16 pairs, or 8 of FP32
+template <typename T> struct Raw8;
+template <> struct Raw8<uint16_t> { u32w4 w; };
+template <> struct Raw8<float> { u32w4 a, b; };
+
+template <bool ANY, bool NT = false>
+__device__ __forceinline__ void load_raw8(const uint16_t *__restrict__ p, int n, Raw8<uint16_t> &r)
+{
+    if (!ANY) {
+        r.w = load16<NT>(reinterpret_cast<const u32w4 *>(p));
+    } else if (n >= 8) {
+        r.w = *reinterpret_cast<const u32w4_any *>(p);
     } else {
-        w = *reinterpret_cast<const u32w4 *>(p);
-    }
+        r.w = (u32w4){0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = as_f(lo_bits(w[i]));
-        v[2 * i + 1] = as_f(hi_bits(w[i]));
+        for (int i = 0; i < 8; ++i)
+            if (i < n) r.w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
     }
 }
-template <bool ANY>
-__device__ __forceinline__ void load8(const float *__restrict__ p, int n, float (&v)[8])
+template <bool ANY, bool NT = false>
+__device__ __forceinline__ void load_raw8(const float *__restrict__ p, int n, Raw8<float> &r)
 {
-    u32w4 a, b;
-    if (ANY) {
-        if (n < 8) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
-            return;
-        }
-        a = reinterpret_cast<const u32w4_any4 *>(p)[0];
-        b = reinterpret_cast<const u32w4_any4 *>(p)[1];
+    if (!ANY) {
+        r.a = load16<NT>(reinterpret_cast<const u32w4 *>(p));
+        r.b = load16<NT>(reinterpret_cast<const u32w4 *>(p) + 1);
+    } else if (n >= 8) {
+        r.a = reinterpret_cast<const u32w4_any4 *>(p)[0];
+        r.b = reinterpret_cast<const u32w4_any4 *>(p)[1];
     } else {
-        a = reinterpret_cast<const u32w4 *>(p)[0];
-        b = reinterpret_cast<const u32w4 *>(p)[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            r.a[i] = i < n ? as_u(p[i]) : 0u;
+            r.b[i] = i + 4 < n ? as_u(p[i + 4]) : 0u;
+        }
     }
+}
+__device__ __forceinline__ void unpack8(const Raw8<uint16_t> &r, float (&v)[8])
+{
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[i] = as_f(a[i]);
-        v[4 + i] = as_f(b[i]);
+        v[2 * i] = as_f(lo_bits(r.w[i]));
+        v[2 * i + 1] = as_f(hi_bits(r.w[i]));
     }
+}
+__device__ __forceinline__ void unpack8(const Raw8<float> &r, float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = as_f(r.a[i]);
+        v[4 + i] = as_f(r.b[i]);
+    }
+}
+template <bool ANY, bool NT = false, typename T>
+__device__ __forceinline__ void load8(const T *__restrict__ p, int n, float (&v)[8])
+{
+    Raw8<T> r;
+    load_raw8<ANY, NT>(p, n, r);
+    unpack8(r, v);
 }
 // BF16: each value rounded once, to nearest even.
-template <bool ANY>
+template <bool ANY, bool NT = false>
 __device__ __forceinline__ void store8(uint16_t *__restrict__ p, int n, const float (&v)[8])
 {
     u32w4 w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = bf16_pair_rne(v[2 * i], v[2 * i + 1]);
-    if (ANY) {
-        if (n < 8) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < n) p[i] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
-            return;
-        }
+    if (!ANY) {
+        store16<NT>(reinterpret_cast<u32w4 *>(p), w);
+    } else if (n >= 8) {
         *reinterpret_cast<u32w4_any *>(p) = w;
     } else {
-        *reinterpret_cast<u32w4 *>(p) = w;
-    }
-}
-template <bool ANY>
-__device__ __forceinline__ void store8(float *__restrict__ p, int n, const float (&v)[8])
-{
-    if (ANY && n < 8) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = v[i];
-        return;
+            if (i < n) p[i] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
     }
+}
+template <bool ANY, bool NT = false>
+__device__ __forceinline__ void store8(float *__restrict__ p, int n, const float (&v)[8])
+{
     const u32w4 a = {as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3])};
     const u32w4 b = {as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7])};
-    if (ANY) {
+    if (!ANY) {
+        store16<NT>(reinterpret_cast<u32w4 *>(p), a);
+        store16<NT>(reinterpret_cast<u32w4 *>(p) + 1, b);
+    } else if (n >= 8) {
         reinterpret_cast<u32w4_any4 *>(p)[0] = a;
         reinterpret_cast<u32w4_any4 *>(p)[1] = b;
     } else {
-        reinterpret_cast<u32w4 *>(p)[0] = a;
-        reinterpret_cast<u32w4 *>(p)[1] = b;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = v[i];
     }
 }
 
 // ---- across the wave ----------------------------------------------------------
 // DPP inside a 16-lane row (quad permutes, then the row's halves and the row
 // mirrored, each pairing lanes that hold equal partial results), two lane
-// exchanges across the four rows.  Every lane gets the same value.
+// exchanges across the four rows.  Every lane of a group gets the same value.
 template <int CTRL>
 __device__ __forceinline__ float dpp_f(float v)
 {
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
 }
-__device__ __forceinline__ float wave_sum(float v)
+// Sum over groups of LANES neighbouring lanes.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v)
 {
     v += dpp_f<0xB1>(v);
     v += dpp_f<0x4E>(v);
     v += dpp_f<0x141>(v);
-    v += dpp_f<0x140>(v);
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
+    if (LANES >= 16) v += dpp_f<0x140>(v);
+    if (LANES >= 32) v += __shfl_xor(v, 16);
+    if (LANES >= 64) v += __shfl_xor(v, 32);
     return v;
 }
+__device__ __forceinline__ float wave_sum(float v) { return lanes_sum<64>(v); }
 // maximum over the 16 lanes of a DPP row (values >= 0, or their bits)
 __device__ __forceinline__ uint32_t dpp_max_16lanes(uint32_t v)
 {
     v = dpp_max_8lanes(v);
     return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
 }
-__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v)
 {
-    v = dpp_max_16lanes(v);
-    v = max(v, (uint32_t)__shfl_xor((int)v, 16));
-    return max(v, (uint32_t)__shfl_xor((int)v, 32));
+    v = LANES >= 16 ? dpp_max_16lanes(v) : dpp_max_8lanes(v);
+    if (LANES >= 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+    if (LANES >= 64) v = max(v, (uint32_t)__shfl_xor((int)v, 32));
+    return v;
 }
 
 // bits of the largest magnitude of eight values; a NaN's bits exceed

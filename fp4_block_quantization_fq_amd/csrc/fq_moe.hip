@@ -16,6 +16,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "fq_internal.h"
 #include "fq_rows.hpp"
 
@@ -23,7 +25,6 @@ using namespace fqdev;
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxExperts = fqimpl::kMoeMaxExperts;
@@ -59,63 +60,39 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_count(fqimpl::MoeSortArgs 
 
 __global__ __launch_bounds__(kSortThreads) void k_moe_place(fqimpl::MoeSortArgs a)
 {
-    // next[e]: the row of the next assignment of e; before[w][e]: those of
-    // the waves before w in the present step
-    __shared__ uint32_t next[kMaxExperts], total[kMaxExperts], start[kMaxExperts + 1];
-    __shared__ uint16_t before[kSortWaves][kMaxExperts];
+    // next[e]: the row of the next assignment of e; before[e][w]: e's
+    // assignments in wave w of the present step, then those in the waves before
+    // w (one 32-byte row an expert, so its thread moves it in two accesses)
+    __shared__ uint32_t total[kMaxExperts], next[kMaxExperts], start[kMaxExperts + 1];
+    __shared__ __attribute__((aligned(16))) uint16_t before[kMaxExperts][kSortWaves];
     __shared__ uint32_t wave_sums[kSortWaves];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const int64_t lo = (int64_t)blockIdx.x * a.chunk, hi = min(lo + a.chunk, a.n);
     const uint32_t e = tid;                // kSortThreads == kMaxExperts: one expert a thread
-    // totals, and the counts of the chunks before this one
-    next[e] = 0;
+    u32w4 *mine_before = (u32w4 *)before[e];
+    uint32_t x = expert_of(a.ids, lo + tid, hi, a.E);     // of the first step
+    total[e] = next[e] = 0;
+    if (e < a.E) mine_before[0] = mine_before[1] = (u32w4){0, 0, 0, 0};
     __syncthreads();
-    uint32_t all = 0, mine = 0;
+    // the experts' totals, and the counts of the chunks before this one
     if (gridDim.x == 1) {
-        for (int64_t i = lo + tid; i < hi; i += kSortThreads) {
-            const uint32_t x = expert_of(a.ids, i, a.n, a.E);
-            if (x < a.E) atomicAdd(&next[x], 1u);
+        if (x < a.E) atomicAdd(&total[x], 1u);
+        for (int64_t i = lo + tid + kSortThreads; i < hi; i += kSortThreads) {
+            const uint32_t o = expert_of(a.ids, i, hi, a.E);
+            if (o < a.E) atomicAdd(&total[o], 1u);
         }
-        __syncthreads();
-        all = next[e];
-    } else if (e < a.E) {
-        for (uint32_t b = 0; b < gridDim.x; ++b) {
-            const uint32_t c = a.ws[(size_t)b * a.E + e];
-            all += c;
-            if (b < blockIdx.x) mine += c;
+    } else {
+        for (uint32_t i = tid; i < gridDim.x * a.E; i += kSortThreads) {
+            const uint32_t c = a.ws[i], b = i / a.E, o = i - b * a.E;
+            if (!c) continue;
+            atomicAdd(&total[o], c);
+            if (b < blockIdx.x) atomicAdd(&next[o], c);
         }
     }
-    // starts: exclusive sum of the padded totals over the experts
-    const uint32_t padded = (all + a.align - 1) / a.align * a.align;
-    uint32_t incl = padded;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const uint32_t o = (uint32_t)__shfl_up((int)incl, d);
-        if (lane >= d) incl += o;
-    }
-    if (lane == 63) wave_sums[wave] = incl;
-    __syncthreads();
-    uint32_t first = incl - padded;
-    for (int w = 0; w < wave; ++w) first += wave_sums[w];
-    next[e] = first + mine;
-    total[e] = all;
-    start[e] = first;
-    if (e == kMaxExperts - 1) start[kMaxExperts] = first + padded;
-    __syncthreads();
-    // offsets (padded totals past E are 0, so start[E] is the rows' number)
-    if (blockIdx.x == 0) {
-        for (uint32_t i = tid; i <= a.E; i += kSortThreads) a.offsets[i] = (int32_t)start[i];
-    }
-    // src of the padding rows: the segments' ends and what follows the last one
-    for (uint32_t i = blockIdx.x; i <= a.E; i += gridDim.x) {
-        const uint32_t from = i < a.E ? start[i] + total[i] : start[a.E];
-        const uint32_t to = i < a.E ? start[i + 1] : (uint32_t)a.rows;
-        for (uint32_t r = from + tid; r < to; r += kSortThreads) a.src[r] = -1;
-    }
-    // places, 1024 assignments at a time in their order
+    // assignments a step of 1024 at a time, in their order
+    bool first_step = true;
     for (int64_t i0 = lo; i0 < hi; i0 += kSortThreads) {
         const int64_t i = i0 + tid;
-        const uint32_t x = i < hi ? expert_of(a.ids, i, a.n, a.E) : a.E;
         // lanes of this wave with the same expert
         uint64_t same = ~0ull;
         for (uint32_t bit = 1; bit <= a.E; bit <<= 1) {
@@ -123,74 +100,147 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_place(fqimpl::MoeSortArgs 
             same &= (x & bit) ? m : ~m;
         }
         const uint32_t rank = (uint32_t)__popcll(same & ((1ull << lane) - 1));
-        for (uint32_t j = tid; j < a.E; j += kSortThreads)
-#pragma unroll
-            for (int w = 0; w < kSortWaves; ++w) before[w][j] = 0;
-        __syncthreads();
-        if (x < a.E && rank == 0) before[wave][x] = (uint16_t)__popcll(same);
+        if (x < a.E && rank == 0) before[x][wave] = (uint16_t)__popcll(same);
         __syncthreads();
         uint32_t sum = 0;
         if (e < a.E) {
-            uint32_t c[kSortWaves];
+            u32w4 c[2] = {mine_before[0], mine_before[1]};
 #pragma unroll
-            for (int w = 0; w < kSortWaves; ++w) c[w] = before[w][e];
-#pragma unroll
-            for (int w = 0; w < kSortWaves; ++w) {
-                before[w][e] = (uint16_t)sum;
-                sum += c[w];
+            for (int w = 0; w < kSortWaves; w += 2) {
+                const uint32_t both = c[w / 8][w / 2 % 4], low = both & 0xFFFFu;
+                c[w / 8][w / 2 % 4] = sum | (sum + low) << 16;
+                sum += low + (both >> 16);
             }
+            mine_before[0] = c[0];
+            mine_before[1] = c[1];
+        }
+        if (first_step) {
+            // starts: exclusive sum of the padded totals over the experts
+            const uint32_t all = total[e], padded = (all + a.align - 1) / a.align * a.align;
+            uint32_t incl = padded;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const uint32_t o = (uint32_t)__shfl_up((int)incl, d);
+                if (lane >= d) incl += o;
+            }
+            if (lane == 63) wave_sums[wave] = incl;
+            __syncthreads();
+            uint32_t first = incl - padded;
+#pragma unroll
+            for (int w = 0; w < kSortWaves - 1; ++w) first += w < wave ? wave_sums[w] : 0u;
+            next[e] += first;
+            start[e] = first;
+            if (e == kMaxExperts - 1) start[kMaxExperts] = first + padded;
         }
         __syncthreads();
         if (i < hi) {
             int32_t p = -1;
             if (x < a.E) {
-                p = (int32_t)(next[x] + before[wave][x] + rank);
+                p = (int32_t)(next[x] + before[x][wave] + rank);
                 a.src[p] = (int32_t)i;
             }
             a.pos[i] = p;
         }
+        first_step = false;
+        if (i0 + kSortThreads >= hi) break;
+        x = expert_of(a.ids, i + kSortThreads, hi, a.E);
         __syncthreads();
-        if (e < a.E) next[e] += sum;
+        if (e < a.E) {
+            next[e] += sum;
+            mine_before[0] = mine_before[1] = (u32w4){0, 0, 0, 0};
+        }
         __syncthreads();
     }
+    // offsets (padded totals past E are 0, so start[E] is the rows' number)
+    if (blockIdx.x == 0)
+        for (uint32_t i = tid; i <= a.E; i += kSortThreads) a.offsets[i] = (int32_t)start[i];
+    // src of the padding rows: a wave an expert for the segments' ends, then all
+    // threads for what follows the last one
+    for (uint32_t i = blockIdx.x * kSortWaves + wave; i < a.E; i += gridDim.x * kSortWaves)
+        for (uint32_t r = start[i] + total[i] + lane; r < start[i + 1]; r += 64) a.src[r] = -1;
+    for (int64_t r = (int64_t)start[a.E] + blockIdx.x * kSortThreads + tid; r < a.rows;
+         r += (int64_t)gridDim.x * kSortThreads)
+        a.src[r] = -1;
 }
 
 // ---------------------------------------------------------------------------
-// dispatch
+// rows
 // ---------------------------------------------------------------------------
-// A workgroup per token reads its row once and writes it to its k places; the
-// workgroups after those look through src, 16 rows each, and clear the padding.
+// LANES lanes share a token: 8 for a row of 64 elements up to a wave, or, with
+// LANES 0, a workgroup of as many waves as the row has 64 chunks of 8 elements
+// (512 threads at most, which then walk over the row).  A lane has one chunk
+// and moves it for up to four of the token's assignments at a time, all loads
+// issued together: what bounds these kernels is the bytes a CU has in flight.
+constexpr int kThreads = 256;               // of a workgroup of several tokens
+constexpr int kMostThreads = 512;
 constexpr int kPadRows = 16;
 
+// One token's assignments j0 .. j0 + 3: rows (negative: none) and weights.
+struct Four {
+    int64_t p[4];
+    float w[4];
+};
+template <bool WAVE>
+__device__ __forceinline__ Four four_of(const fqimpl::MoeRowsArgs &a, int64_t t, int j0)
+{
+    Four f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t at = t * a.k + min(j0 + i, (int)a.k - 1);
+        int32_t p = a.pos[at];
+        if (WAVE) p = __builtin_amdgcn_readfirstlane(p);
+        f.p[i] = j0 + i < a.k && (uint32_t)p < (uint64_t)a.rows ? (int64_t)p : -1;
+        f.w[i] = a.weights ? a.weights[at] : 1.0f;
+    }
+    return f;
+}
+
+// +0 into the rows of [block * 16, block * 16 + 16) that hold no assignment.
+template <bool NT>
 __device__ __forceinline__ void clear_padding(const fqimpl::MoeRowsArgs &a, int64_t block,
                                               uint16_t *__restrict__ y)
 {
-    const uint32_t chunks = (uint32_t)(a.H / 8);
-    const u32w4 zero = {0, 0, 0, 0};
-    for (int i = 0; i < kPadRows; ++i) {
-        const int64_t r = block * kPadRows + i;
-        if (r >= a.rows) return;
-        if ((uint64_t)(int64_t)a.src[r] < (uint64_t)(a.T * a.k)) continue;
-        for (uint32_t c = threadIdx.x; c < chunks; c += kThreads)
-            *(u32w4 *)(y + r * a.H + c * 8) = zero;
+    const uint32_t chunks = (uint32_t)(a.H / 8), lane = threadIdx.x & 63;
+    const int64_t r0 = block * kPadRows;
+    bool pad = false;
+    if (lane < kPadRows && r0 + lane < a.rows)
+        pad = (uint64_t)(int64_t)a.src[r0 + lane] >= (uint64_t)(a.T * a.k);
+    for (uint64_t left = __ballot(pad); left; left &= left - 1) {
+        uint16_t *row = y + (r0 + __builtin_ctzll(left)) * a.H;
+        for (uint32_t c = threadIdx.x; c < chunks; c += blockDim.x)
+            store16<NT>((u32w4 *)(row + c * 8), (u32w4){0, 0, 0, 0});
     }
 }
 
-template <int F8>
-__global__ __launch_bounds__(kThreads) void k_moe_dispatch(fqimpl::MoeRowsArgs a)
+// Token of this lane's group in unit `b` of the work (a workgroup's share), and
+// its first chunk.
+template <int LANES>
+__device__ __forceinline__ int64_t token_of(uint32_t b)
 {
-    uint16_t *y = (uint16_t *)a.rows_out;
-    if (blockIdx.x >= a.T) return clear_padding(a, (int64_t)blockIdx.x - a.T, y);
-    const int64_t t = blockIdx.x;
-    const uint32_t chunks = (uint32_t)(a.H / 8);
-    for (uint32_t c = threadIdx.x; c < chunks; c += kThreads) {
+    if (LANES == 0) return b;
+    constexpr int kLanes = LANES ? LANES : 64;
+    const int g = threadIdx.x / kLanes;
+    return (int64_t)b * (kThreads / kLanes) + (LANES == 64 ? __builtin_amdgcn_readfirstlane(g) : g);
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t chunk_of()
+{
+    return LANES ? threadIdx.x % (LANES ? LANES : 64) : threadIdx.x;
+}
+
+template <int LANES, int F8, bool NT>
+__device__ __forceinline__ void dispatch_unit(const fqimpl::MoeRowsArgs &a, uint32_t b,
+                                              uint32_t chunks, uint16_t *__restrict__ y)
+{
+    const int64_t t = token_of<LANES>(b);
+    if (t >= a.T) return;
+    for (uint32_t c = chunk_of<LANES>(); c < chunks; c += LANES ? LANES : blockDim.x) {
         u32w4 v;
         if (F8 == fqimpl::F8_NONE) {
-            v = *(const u32w4 *)((const uint16_t *)a.x + t * a.H + c * 8);
+            v = load16<NT>((const u32w4 *)((const uint16_t *)a.x + t * a.H + c * 8));
         } else {
-            float f[8];
+            float f[8], s;
             e4m3_decode8(*(const u32w2 *)((const uint8_t *)a.x + t * a.H + c * 8), f);
-            float s;
             if (F8 == fqimpl::F8_MX) {
                 const uint32_t code = ((const uint8_t *)a.scales)[t * (a.H / 32) + c / 4];
                 s = code == 255u ? as_f(0x7FC00000u) : e8m0_value(code);
@@ -200,64 +250,158 @@ __global__ __launch_bounds__(kThreads) void k_moe_dispatch(fqimpl::MoeRowsArgs a
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = bf16_pair_rne(f[2 * i] * s, f[2 * i + 1] * s);
         }
-        for (int j = 0; j < a.k; ++j) {
-            const int64_t p = a.pos[t * a.k + j];
-            if ((uint64_t)p < (uint64_t)a.rows) *(u32w4 *)(y + p * a.H + c * 8) = v;
+        for (int j0 = 0; j0 < a.k; j0 += 4) {
+            const Four f = four_of<LANES == 0 || LANES == 64>(a, t, j0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (f.p[i] >= 0) store16<NT>((u32w4 *)(y + f.p[i] * a.H + c * 8), v);
         }
     }
 }
 
-// ---------------------------------------------------------------------------
-// combine
-// ---------------------------------------------------------------------------
-__global__ __launch_bounds__(kThreads) void k_moe_combine(fqimpl::MoeRowsArgs a)
+// y[pos[t, j]] = x[t]; the units from `work` on clear the padding.
+template <int LANES, int F8, bool NT>
+__global__ __launch_bounds__(LANES ? kThreads : kMostThreads) void k_moe_dispatch(
+    fqimpl::MoeRowsArgs a, uint32_t work, uint32_t units)
 {
-    const uint16_t *y = (const uint16_t *)a.y;
-    const int64_t t = blockIdx.x;
+    uint16_t *y = (uint16_t *)a.rows_out;
     const uint32_t chunks = (uint32_t)(a.H / 8);
-    for (uint32_t c = threadIdx.x; c < chunks; c += kThreads) {
-        float acc[8] = {};
-        for (int j = 0; j < a.k; ++j) {
-            const int64_t p = a.pos[t * a.k + j];
-            if ((uint64_t)p >= (uint64_t)a.rows) continue;
-            const float w = a.weights ? a.weights[t * a.k + j] : 1.0f;
-            float v[8];
-            load8<false>(y + p * a.H + c * 8, 8, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] += w * v[e];
-        }
-        store8<false>((uint16_t *)a.out + t * a.H + c * 8, 8, acc);
+    for (uint32_t b = blockIdx.x; b < units; b += gridDim.x) {
+        if (b < work) dispatch_unit<LANES, F8, NT>(a, b, chunks, y);
+        else clear_padding<NT>(a, (int64_t)b - work, y);
     }
 }
 
-// A wave per assignment; the waves of one token are neighbours, so dout's row
-// comes from memory once.  The workgroups after those clear the padding.
-__global__ __launch_bounds__(kThreads) void k_moe_combine_bwd(fqimpl::MoeRowsArgs a, uint32_t work)
+template <int LANES, bool NT>
+__device__ __forceinline__ void combine_unit(const fqimpl::MoeRowsArgs &a, uint32_t b,
+                                             uint32_t chunks)
 {
-    uint16_t *dy = (uint16_t *)a.rows_out;
-    if (blockIdx.x >= work) return clear_padding(a, (int64_t)blockIdx.x - work, dy);
-    const int64_t i = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
-    if (i >= a.T * a.k) return;
-    const int64_t t = i / a.k, p = a.pos[i];
-    const uint32_t lane = threadIdx.x & 63, chunks = (uint32_t)(a.H / 8);
-    float dot = 0.0f;
-    if ((uint64_t)p < (uint64_t)a.rows) {
-        const float w = a.weights[i];
-        for (uint32_t c = lane; c < chunks; c += 64) {
-            float d[8], v[8];
-            load8<false>((const uint16_t *)a.dout + t * a.H + c * 8, 8, d);
-            load8<false>((const uint16_t *)a.y + p * a.H + c * 8, 8, v);
+    const uint16_t *__restrict__ y = (const uint16_t *)a.y;
+    const int64_t t = token_of<LANES>(b);
+    if (t >= a.T) return;
+    for (uint32_t c = chunk_of<LANES>(); c < chunks; c += LANES ? LANES : blockDim.x) {
+        float acc[8] = {};
+        for (int j0 = 0; j0 < a.k; j0 += 4) {
+            const Four f = four_of<LANES == 0 || LANES == 64>(a, t, j0);
+            Raw8<uint16_t> r[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                dot += d[e] * v[e];
-                d[e] = w * d[e];
+            for (int i = 0; i < 4; ++i)
+                if (f.p[i] >= 0) load_raw8<false, NT>(y + f.p[i] * a.H + c * 8, 8, r[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (f.p[i] < 0) continue;
+                float v[8];
+                unpack8(r[i], v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(f.w[i], v[e], acc[e]);
             }
-            store8<false>(dy + p * a.H + c * 8, 8, d);
         }
-        dot = wave_sum(dot);
+        store8<false, NT>((uint16_t *)a.out + t * a.H + c * 8, 8, acc);
     }
-    if (lane == 0) a.dweights[i] = dot;
 }
+
+// out[t] = sum_j w[t, j] * y[pos[t, j]]
+template <int LANES, bool NT>
+__global__ __launch_bounds__(LANES ? kThreads : kMostThreads) void k_moe_combine(
+    fqimpl::MoeRowsArgs a, uint32_t work)
+{
+    const uint32_t chunks = (uint32_t)(a.H / 8);
+    for (uint32_t b = blockIdx.x; b < work; b += gridDim.x) combine_unit<LANES, NT>(a, b, chunks);
+}
+
+template <int LANES, bool NT>
+__device__ __forceinline__ void combine_bwd_unit(const fqimpl::MoeRowsArgs &a, uint32_t b,
+                                                 uint32_t chunks, uint16_t *__restrict__ dy,
+                                                 float (*part)[kMostThreads / 64])
+{
+    const uint16_t *__restrict__ y = (const uint16_t *)a.y;
+    const int64_t t = token_of<LANES>(b);
+    if (t >= a.T) return;                       // not with LANES 0, which has barriers
+    const uint32_t c0 = chunk_of<LANES>();
+    for (int j0 = 0; j0 < a.k; j0 += 4) {
+        const Four f = four_of<LANES == 0 || LANES == 64>(a, t, j0);
+        float dot[4] = {};
+        for (uint32_t c = c0; c < chunks; c += LANES ? LANES : blockDim.x) {
+            float d[8];
+            Raw8<uint16_t> r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (f.p[i] >= 0) load_raw8<false, NT>(y + f.p[i] * a.H + c * 8, 8, r[i]);
+            load8<false>((const uint16_t *)a.dout + t * a.H + c * 8, 8, d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (f.p[i] < 0) continue;
+                float v[8];
+                unpack8(r[i], v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dot[i] = __builtin_fmaf(d[e], v[e], dot[i]);
+                    v[e] = f.w[i] * d[e];
+                }
+                store8<false, NT>(dy + f.p[i] * a.H + c * 8, 8, v);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dot[i] = lanes_sum<LANES ? LANES : 64>(dot[i]);
+        if (LANES) {
+            if (c0 == 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (j0 + i < a.k) a.dweights[t * a.k + j0 + i] = dot[i];
+            continue;
+        }
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) part[i][threadIdx.x >> 6] = dot[i];
+        __syncthreads();
+        if (threadIdx.x < 4 && j0 + (int)threadIdx.x < a.k) {
+            float v = part[threadIdx.x][0];
+            for (uint32_t w = 1; w < blockDim.x / 64; ++w) v += part[threadIdx.x][w];
+            a.dweights[t * a.k + j0 + threadIdx.x] = v;
+        }
+        __syncthreads();
+    }
+}
+
+// dy[pos[t, j]] = w[t, j] * dout[t], dw[t, j] = <dout[t], y[pos[t, j]]>; the
+// units from `work` on clear the padding.
+template <int LANES, bool NT>
+__global__ __launch_bounds__(LANES ? kThreads : kMostThreads) void k_moe_combine_bwd(
+    fqimpl::MoeRowsArgs a, uint32_t work, uint32_t units)
+{
+    __shared__ float part[4][kMostThreads / 64];
+    uint16_t *dy = (uint16_t *)a.rows_out;
+    const uint32_t chunks = (uint32_t)(a.H / 8);
+    for (uint32_t b = blockIdx.x; b < units; b += gridDim.x) {
+        if (b < work) combine_bwd_unit<LANES, NT>(a, b, chunks, dy, part);
+        else clear_padding<NT>(a, (int64_t)b - work, dy);
+    }
+}
+
+// ---- launch -------------------------------------------------------------------
+// A grid holds fewer than 2^32 lanes; the kernels walk over what is left.
+constexpr uint32_t kMaxGrid = 1u << 22;
+
+// Lanes of a token from the width alone: launch(lanes, units of work, threads).
+template <typename F>
+hipError_t by_width(const fqimpl::MoeRowsArgs &a, F launch)
+{
+    const int64_t chunks = a.H / 8;
+    const auto shared = [&](auto lanes) {
+        const int64_t per = kThreads / decltype(lanes)::value;
+        return launch(lanes, (uint32_t)((a.T + per - 1) / per), (uint32_t)kThreads);
+    };
+    if (chunks <= 8) return shared(std::integral_constant<int, 8>());
+    if (chunks <= 16) return shared(std::integral_constant<int, 16>());
+    if (chunks <= 32) return shared(std::integral_constant<int, 32>());
+    if (chunks <= 64) return shared(std::integral_constant<int, 64>());
+    const int64_t threads = (chunks + 63) / 64 * 64;
+    return launch(std::integral_constant<int, 0>(), (uint32_t)a.T,
+                  (uint32_t)(threads < kMostThreads ? threads : kMostThreads));
+}
+
+// Streaming accesses from this many elements of rows on.
+constexpr int64_t kStreamElems = int64_t(1) << 24;
 
 }  // namespace
 
@@ -265,9 +409,11 @@ namespace fqimpl {
 
 uint32_t moe_sort_chunk(int64_t n)
 {
+    // one workgroup while it needs no more than two steps; then a step each, as
+    // far as the number of workgroups allows
+    if (n <= 2 * kSortThreads) return 2 * kSortThreads;
     const int64_t c = (n + kMoeMaxChunks - 1) / kMoeMaxChunks;
-    const int64_t least = 2 * kSortThreads;
-    return (uint32_t)(c <= least ? least : (c + kSortThreads - 1) / kSortThreads * kSortThreads);
+    return (uint32_t)((c + kSortThreads - 1) / kSortThreads * kSortThreads);
 }
 
 hipError_t launch_moe_sort(MoeSortArgs a, hipStream_t stream)
@@ -283,27 +429,55 @@ hipError_t launch_moe_sort(MoeSortArgs a, hipStream_t stream)
     return hipGetLastError();
 }
 
+template <int F8>
+static hipError_t dispatch(const MoeRowsArgs &a, hipStream_t stream)
+{
+    const uint32_t pads = (uint32_t)((a.rows + kPadRows - 1) / kPadRows);
+    return by_width(a, [&](auto lanes, uint32_t work, uint32_t threads) {
+        constexpr int kLanes = decltype(lanes)::value;
+        const uint32_t units = work + pads;
+        const dim3 grid(units < kMaxGrid ? units : kMaxGrid), block(threads);
+        if (a.rows * a.H < kStreamElems)
+            k_moe_dispatch<kLanes, F8, false><<<grid, block, 0, stream>>>(a, work, units);
+        else
+            k_moe_dispatch<kLanes, F8, true><<<grid, block, 0, stream>>>(a, work, units);
+        return hipGetLastError();
+    });
+}
+
 hipError_t launch_moe_dispatch(int f8, const MoeRowsArgs &a, hipStream_t stream)
 {
-    const dim3 grid((uint32_t)(a.T + (a.rows + kPadRows - 1) / kPadRows)), block(kThreads);
-    if (f8 == F8_MX) k_moe_dispatch<F8_MX><<<grid, block, 0, stream>>>(a);
-    else if (f8 == F8_ROW) k_moe_dispatch<F8_ROW><<<grid, block, 0, stream>>>(a);
-    else k_moe_dispatch<F8_NONE><<<grid, block, 0, stream>>>(a);
-    return hipGetLastError();
+    if (f8 == F8_MX) return dispatch<F8_MX>(a, stream);
+    if (f8 == F8_ROW) return dispatch<F8_ROW>(a, stream);
+    return dispatch<F8_NONE>(a, stream);
 }
 
 hipError_t launch_moe_combine(const MoeRowsArgs &a, hipStream_t stream)
 {
-    k_moe_combine<<<dim3((uint32_t)a.T), dim3(kThreads), 0, stream>>>(a);
-    return hipGetLastError();
+    return by_width(a, [&](auto lanes, uint32_t work, uint32_t threads) {
+        constexpr int kLanes = decltype(lanes)::value;
+        const dim3 grid(work < kMaxGrid ? work : kMaxGrid), block(threads);
+        if (a.T * a.k * a.H < kStreamElems)
+            k_moe_combine<kLanes, false><<<grid, block, 0, stream>>>(a, work);
+        else
+            k_moe_combine<kLanes, true><<<grid, block, 0, stream>>>(a, work);
+        return hipGetLastError();
+    });
 }
 
 hipError_t launch_moe_combine_bwd(const MoeRowsArgs &a, hipStream_t stream)
 {
-    const uint32_t work = (uint32_t)((a.T * a.k + kThreads / 64 - 1) / (kThreads / 64));
     const uint32_t pads = (uint32_t)((a.rows + kPadRows - 1) / kPadRows);
-    k_moe_combine_bwd<<<dim3(work + pads), dim3(kThreads), 0, stream>>>(a, work);
-    return hipGetLastError();
+    return by_width(a, [&](auto lanes, uint32_t work, uint32_t threads) {
+        constexpr int kLanes = decltype(lanes)::value;
+        const uint32_t units = work + pads;
+        const dim3 grid(units < kMaxGrid ? units : kMaxGrid), block(threads);
+        if (a.rows * a.H < kStreamElems)
+            k_moe_combine_bwd<kLanes, false><<<grid, block, 0, stream>>>(a, work, units);
+        else
+            k_moe_combine_bwd<kLanes, true><<<grid, block, 0, stream>>>(a, work, units);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace fqimpl

@@ -45,6 +45,7 @@ EXPORTED = (
     "fq_qlinear_bwd_retain", "fq_rmsnorm_fwd", "fq_rmsnorm_bwd_workspace_size",
     "fq_rmsnorm_bwd", "fq_moe_rows", "fq_moe_sort_workspace_size", "fq_moe_sort",
     "fq_moe_dispatch", "fq_moe_combine", "fq_moe_combine_bwd", "fq_adamw_step",
+    "fq_adamw_plan_size", "fq_adamw_plan", "fq_adamw_step_plan",
 )
 
 
@@ -192,6 +193,12 @@ def lib() -> ctypes.CDLL:
         L.fq_adamw_step.argtypes = [ctypes.POINTER(FqAdamWHyper), ctypes.POINTER(FqAdamWTensor),
                                     i64, vp]
         L.fq_adamw_step.restype = ctypes.c_int
+        L.fq_adamw_plan_size.argtypes = [i64]
+        L.fq_adamw_plan_size.restype = sz
+        L.fq_adamw_plan.argtypes = [ctypes.POINTER(FqAdamWTensor), i64, i32, vp, sz]
+        L.fq_adamw_plan.restype = ctypes.c_int
+        L.fq_adamw_step_plan.argtypes = [ctypes.POINTER(FqAdamWHyper), vp, vp, vp]
+        L.fq_adamw_step_plan.restype = ctypes.c_int
         L.fq_status_string.argtypes = [ctypes.c_int]
         L.fq_status_string.restype = ctypes.c_char_p
         L.fq_last_error.argtypes = []
@@ -879,17 +886,17 @@ def adamw_state(n: int, device, f8: bool = False) -> dict:
 
 
 class AdamWPlan:
-    """The tensors of an optimizer as the library takes them, checked once.  It
-    holds the tensors it was made from; their contents may change between
-    steps, the tensors may not."""
+    """The tensors of an optimizer as the library takes them, checked once and
+    laid out in device memory, so that a step is one launch.  It holds the
+    tensors it was made from; their contents may change between steps, the
+    tensors may not."""
 
     def __init__(self, tensors):
         torch = _torch()
         self.tensors = list(tensors)
-        self.array = (FqAdamWTensor * len(self.tensors))()
+        array = (FqAdamWTensor * len(self.tensors))()
         self.f8 = bool(self.tensors) and self.tensors[0].m.dtype != torch.float32
-        self.table = ctypes.addressof(self.array)
-        for i, (s, t) in enumerate(zip(self.array, self.tensors)):
+        for i, (s, t) in enumerate(zip(array, self.tensors)):
             n, name = t.w.numel(), f"tensor {i}: "
             s.n = n
             s.w = _typed(t.w, torch.float32, n, name + "w")
@@ -905,6 +912,12 @@ class AdamWPlan:
                 s.m = _typed(t.m, torch.float32, n, name + "m")
                 s.v = _typed(t.v, torch.float32, n, name + "v")
             s.lr_mult, s.weight_decay = t.lr_mult, t.weight_decay
+        self.state_type = FQ_STATE_F8 if self.f8 else FQ_STATE_F32
+        nbytes = lib().fq_adamw_plan_size(len(array))
+        self.host = torch.empty(nbytes, dtype=torch.uint8)        # 64-byte aligned
+        self.address = self.host.data_ptr()
+        _check(lib().fq_adamw_plan(array, len(array), self.state_type, self.address, nbytes))
+        self.device = self.host.to(self.tensors[0].w.device) if self.tensors else None
 
 
 def adamw_plan(tensors) -> AdamWPlan:
@@ -917,8 +930,8 @@ def fq_adamw_step(plan: AdamWPlan, lr: float, step: int, beta1: float = 0.9, bet
     grad_scale is an FP32 device scalar the gradients are multiplied by; seed
     keys the stochastic rounding of 8-bit moments."""
     st = (_binding_module or _binding()).adamw_step(
-        plan.table, len(plan.array), FQ_STATE_F8 if plan.f8 else FQ_STATE_F32, lr, beta1, beta2,
-        eps, step, seed, grad_scale, stream)
+        plan.address, plan.device, plan.state_type, lr, beta1, beta2, eps, step, seed, grad_scale,
+        stream)
     if st:
         _check(st)
 

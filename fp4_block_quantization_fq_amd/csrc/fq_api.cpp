@@ -1121,6 +1121,95 @@ fq_status check_moe_rows(int64_t T, int64_t k, int64_t H, int64_t rows, int64_t 
     return FQ_OK;
 }
 
+fq_status check_adamw_hyper(const fq_adamw_hyper *hyper)
+{
+    if (!hyper) return fail(FQ_ERR_NULL, "hyper is NULL");
+    const fq_adamw_hyper &h = *hyper;
+    if (h.reserved != 0) return fail(FQ_ERR_DESC, "hyper->reserved must be 0");
+    if (h.state_type != FQ_STATE_F32 && h.state_type != FQ_STATE_F8)
+        return fail(FQ_ERR_DESC, "hyper->state_type=%d is not FQ_STATE_F32/F8", h.state_type);
+    if (!(h.beta1 >= 0 && h.beta1 < 1 && h.beta2 >= 0 && h.beta2 < 1))
+        return fail(FQ_ERR_DESC, "beta1 and beta2 must be in [0, 1)");
+    if (!(h.eps >= 0) || !std::isfinite(h.lr) || !std::isfinite(h.eps))
+        return fail(FQ_ERR_DESC, "lr must be finite and eps finite and >= 0");
+    if (h.step < 1 || h.step > 0xFFFFFFFFll)
+        return fail(FQ_ERR_DESC, "step=%lld must be in [1, 2^32)", (long long)h.step);
+    FQ_TRY(check_ptr(h.grad_scale, "hyper->grad_scale", false, 4));
+    return FQ_OK;
+}
+
+fq_status check_adamw_tensors(const fq_adamw_tensor *tensors, int64_t count, bool f8)
+{
+    if (count < 0 || count > kMaxDim)
+        return fail(FQ_ERR_SHAPE, "count=%lld must be >= 0 and below 2^31", (long long)count);
+    if (count && !tensors) return fail(FQ_ERR_NULL, "tensors is NULL");
+    for (int64_t i = 0; i < count; ++i) {
+        const fq_adamw_tensor &t = tensors[i];
+        if (t.reserved != 0)
+            return fail(FQ_ERR_DESC, "tensors[%lld].reserved must be 0", (long long)i);
+        if (t.g_type != FQ_TYPE_BF16 && t.g_type != FQ_TYPE_F32)
+            return fail(FQ_ERR_DESC, "tensors[%lld].g_type=%d is not FQ_TYPE_BF16/F32",
+                        (long long)i, t.g_type);
+        if (t.n < 0 || t.n > kMaxElems)
+            return fail(FQ_ERR_SHAPE, "tensors[%lld].n=%lld must be in [0, 2^34]", (long long)i,
+                        (long long)t.n);
+        if (!std::isfinite(t.lr_mult) || !std::isfinite(t.weight_decay))
+            return fail(FQ_ERR_DESC, "tensors[%lld]: lr_mult and weight_decay must be finite",
+                        (long long)i);
+        if (t.n == 0) continue;
+        const void *need[] = {t.w, t.g, t.m, t.v};
+        for (const void *p : need) {
+            if (!p) return fail(FQ_ERR_NULL, "tensors[%lld]: w, g, m or v is NULL", (long long)i);
+            if (!aligned(p, 16))
+                return fail(FQ_ERR_ALIGN, "tensors[%lld]: w, g, m or v is not 16-byte aligned",
+                            (long long)i);
+        }
+        if (!aligned(t.w_bf16, 16))
+            return fail(FQ_ERR_ALIGN, "tensors[%lld].w_bf16 is not 16-byte aligned", (long long)i);
+        if (f8 && (!t.m_scale || !t.v_scale))
+            return fail(FQ_ERR_NULL, "tensors[%lld]: m_scale or v_scale is NULL", (long long)i);
+        if (f8 && !(aligned(t.m_scale, 4) && aligned(t.v_scale, 4)))
+            return fail(FQ_ERR_ALIGN, "tensors[%lld]: m_scale or v_scale is not 4-byte aligned",
+                        (long long)i);
+    }
+    return FQ_OK;
+}
+
+fqimpl::AdamWStep adamw_step_of(const fq_adamw_hyper &h)
+{
+    fqimpl::AdamWStep a = {};
+    a.lr = (float)h.lr;
+    a.beta1 = (float)h.beta1;
+    a.one_beta1 = (float)(1.0 - h.beta1);
+    a.beta2 = (float)h.beta2;
+    a.one_beta2 = (float)(1.0 - h.beta2);
+    a.eps = (float)h.eps;
+    a.inv_bc1 = (float)(1.0 / (1.0 - std::pow(h.beta1, (double)h.step)));
+    a.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(h.beta2, (double)h.step)));
+    a.grad_scale = h.grad_scale;
+    a.step = (uint32_t)h.step;
+    a.seed_lo = (uint32_t)h.seed;
+    a.seed_hi = (uint32_t)(h.seed >> 32);
+    return a;
+}
+
+fqimpl::AdamWTensor adamw_entry(const fq_adamw_tensor &t)
+{
+    return {t.w, t.w_bf16, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n,
+            t.lr_mult, t.weight_decay, t.g_type == FQ_TYPE_F32};
+}
+
+// The image of a plan: this header, then for each tensor that has elements its
+// entry, and after all entries their first tiles and their numbers in the list.
+struct AdamWPlan {
+    uint64_t magic;
+    uint32_t count, tiles;
+    int32_t state_type, reserved;
+    int64_t padding[5];      // entries at a multiple of 64 bytes
+};
+constexpr uint64_t kPlanMagic = 0x4E4C50574D414441ull;
+static_assert(sizeof(AdamWPlan) == 64, "plan header");
+
 }  // namespace
 
 extern "C" {
@@ -1345,85 +1434,96 @@ fq_status fq_moe_combine_bwd(const void *dout_bf16, const void *y_bf16, const fl
 fq_status fq_adamw_step(const fq_adamw_hyper *hyper, const fq_adamw_tensor *tensors,
                         int64_t count, void *stream)
 {
-    if (!hyper) return fail(FQ_ERR_NULL, "hyper is NULL");
-    const fq_adamw_hyper &h = *hyper;
-    if (h.reserved != 0) return fail(FQ_ERR_DESC, "hyper->reserved must be 0");
-    if (h.state_type != FQ_STATE_F32 && h.state_type != FQ_STATE_F8)
-        return fail(FQ_ERR_DESC, "hyper->state_type=%d is not FQ_STATE_F32/F8", h.state_type);
-    if (!(h.beta1 >= 0 && h.beta1 < 1 && h.beta2 >= 0 && h.beta2 < 1))
-        return fail(FQ_ERR_DESC, "beta1 and beta2 must be in [0, 1)");
-    if (!(h.eps >= 0) || !std::isfinite(h.lr) || !std::isfinite(h.eps))
-        return fail(FQ_ERR_DESC, "lr must be finite and eps finite and >= 0");
-    if (h.step < 1 || h.step > 0xFFFFFFFFll)
-        return fail(FQ_ERR_DESC, "step=%lld must be in [1, 2^32)", (long long)h.step);
-    FQ_TRY(check_ptr(h.grad_scale, "hyper->grad_scale", false, 4));
-    if (count < 0 || count > kMaxDim)
-        return fail(FQ_ERR_SHAPE, "count=%lld must be >= 0 and below 2^31", (long long)count);
-    if (count && !tensors) return fail(FQ_ERR_NULL, "tensors is NULL");
-    const bool f8 = h.state_type == FQ_STATE_F8;
-    for (int64_t i = 0; i < count; ++i) {
-        const fq_adamw_tensor &t = tensors[i];
-        if (t.reserved != 0)
-            return fail(FQ_ERR_DESC, "tensors[%lld].reserved must be 0", (long long)i);
-        if (t.g_type != FQ_TYPE_BF16 && t.g_type != FQ_TYPE_F32)
-            return fail(FQ_ERR_DESC, "tensors[%lld].g_type=%d is not FQ_TYPE_BF16/F32",
-                        (long long)i, t.g_type);
-        if (t.n < 0 || t.n > kMaxElems)
-            return fail(FQ_ERR_SHAPE, "tensors[%lld].n=%lld must be in [0, 2^34]", (long long)i,
-                        (long long)t.n);
-        if (!std::isfinite(t.lr_mult) || !std::isfinite(t.weight_decay))
-            return fail(FQ_ERR_DESC, "tensors[%lld]: lr_mult and weight_decay must be finite",
-                        (long long)i);
-        if (t.n == 0) continue;
-        const void *need[] = {t.w, t.g, t.m, t.v};
-        for (const void *p : need) {
-            if (!p) return fail(FQ_ERR_NULL, "tensors[%lld]: w, g, m or v is NULL", (long long)i);
-            if (!aligned(p, 16))
-                return fail(FQ_ERR_ALIGN, "tensors[%lld]: w, g, m or v is not 16-byte aligned",
-                            (long long)i);
-        }
-        if (!aligned(t.w_bf16, 16))
-            return fail(FQ_ERR_ALIGN, "tensors[%lld].w_bf16 is not 16-byte aligned", (long long)i);
-        if (f8 && (!t.m_scale || !t.v_scale))
-            return fail(FQ_ERR_NULL, "tensors[%lld]: m_scale or v_scale is NULL", (long long)i);
-        if (f8 && !(aligned(t.m_scale, 4) && aligned(t.v_scale, 4)))
-            return fail(FQ_ERR_ALIGN, "tensors[%lld]: m_scale or v_scale is not 4-byte aligned",
-                        (long long)i);
-    }
+    FQ_TRY(check_adamw_hyper(hyper));
+    const bool f8 = hyper->state_type == FQ_STATE_F8;
+    FQ_TRY(check_adamw_tensors(tensors, count, f8));
     fqimpl::AdamWArgs a;
-    a.lr = (float)h.lr;
-    a.beta1 = (float)h.beta1;
-    a.one_beta1 = (float)(1.0 - h.beta1);
-    a.beta2 = (float)h.beta2;
-    a.one_beta2 = (float)(1.0 - h.beta2);
-    a.eps = (float)h.eps;
-    a.inv_bc1 = (float)(1.0 / (1.0 - std::pow(h.beta1, (double)h.step)));
-    a.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(h.beta2, (double)h.step)));
-    a.grad_scale = h.grad_scale;
-    a.step = (uint32_t)h.step;
-    a.seed_lo = (uint32_t)h.seed;
-    a.seed_hi = (uint32_t)(h.seed >> 32);
-    a.count = 0;
-    uint32_t grid = 0;
+    a.step = adamw_step_of(*hyper);
     for (int64_t i = 0; i < count; ++i) {
         const fq_adamw_tensor &t = tensors[i];
-        if (t.n) {
-            const uint32_t wgs = fqimpl::adamw_workgroups(t.n);
-            // a launch's grid stays well below 2^31 workgroups
-            if (a.count == fqimpl::kAdamWTensors || (a.count && grid + (uint64_t)wgs > (1u << 30))) {
-                FQ_TRY(device_status(fqimpl::launch_adamw(a, f8, grid, (hipStream_t)stream),
-                                     "AdamW launch"));
-                a.count = grid = 0;
-            }
-            a.first[a.count] = grid;
-            a.index[a.count] = (uint32_t)i;
-            a.t[a.count++] = {t.w, t.w_bf16, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n,
-                              t.lr_mult, t.weight_decay, t.g_type == FQ_TYPE_F32};
-            grid += wgs;
+        if (!t.n) continue;
+        const uint32_t tiles = fqimpl::adamw_tiles(t.n, f8);
+        uint32_t &n = a.step.count;
+        if (n == fqimpl::kAdamWTensors || a.step.tiles + (uint64_t)tiles > 0xFFFFFFFFull) {
+            FQ_TRY(device_status(fqimpl::launch_adamw(a, f8, (hipStream_t)stream), "AdamW launch"));
+            n = a.step.tiles = 0;
         }
+        a.first[n] = a.step.tiles;
+        a.index[n] = (uint32_t)i;
+        a.t[n++] = adamw_entry(t);
+        a.step.tiles += tiles;
     }
-    if (!a.count) return ok();
-    return device_status(fqimpl::launch_adamw(a, f8, grid, (hipStream_t)stream), "AdamW launch");
+    if (!a.step.count) return ok();
+    return device_status(fqimpl::launch_adamw(a, f8, (hipStream_t)stream), "AdamW launch");
+}
+
+size_t fq_adamw_plan_size(int64_t count)
+{
+    if (count < 0 || count > kMaxDim) {
+        fail(FQ_ERR_SHAPE, "count=%lld must be >= 0 and below 2^31", (long long)count);
+        return 0;
+    }
+    return sizeof(AdamWPlan) + (size_t)count * (sizeof(fqimpl::AdamWTensor) + 2 * sizeof(uint32_t));
+}
+
+fq_status fq_adamw_plan(const fq_adamw_tensor *tensors, int64_t count, int32_t state_type,
+                        void *plan, size_t plan_bytes)
+{
+    if (state_type != FQ_STATE_F32 && state_type != FQ_STATE_F8)
+        return fail(FQ_ERR_DESC, "state_type=%d is not FQ_STATE_F32/F8", state_type);
+    const bool f8 = state_type == FQ_STATE_F8;
+    FQ_TRY(check_adamw_tensors(tensors, count, f8));
+    FQ_TRY(check_ptr(plan, "plan", true));
+    const size_t need = fq_adamw_plan_size(count);
+    if (plan_bytes < need)
+        return fail(FQ_ERR_WORKSPACE, "plan %zu bytes < %zu required", plan_bytes, need);
+    uint64_t live = 0, tiles = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        live += tensors[i].n > 0;
+        tiles += fqimpl::adamw_tiles(tensors[i].n, f8);
+    }
+    if (tiles > 0xFFFFFFFFull)
+        return fail(FQ_ERR_SHAPE, "a plan's tensors must have fewer than 2^42 elements");
+    memset(plan, 0, need);
+    AdamWPlan *p = (AdamWPlan *)plan;
+    p->magic = kPlanMagic;
+    p->count = (uint32_t)live;
+    p->tiles = (uint32_t)tiles;
+    p->state_type = state_type;
+    auto *entries = (fqimpl::AdamWTensor *)(p + 1);
+    auto *first = (uint32_t *)(entries + live), *index = first + live;
+    uint32_t n = 0, at = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (!tensors[i].n) continue;
+        entries[n] = adamw_entry(tensors[i]);
+        first[n] = at;
+        index[n++] = (uint32_t)i;
+        at += fqimpl::adamw_tiles(tensors[i].n, f8);
+    }
+    return ok();
+}
+
+fq_status fq_adamw_step_plan(const fq_adamw_hyper *hyper, const void *plan,
+                             const void *plan_device, void *stream)
+{
+    FQ_TRY(check_adamw_hyper(hyper));
+    FQ_TRY(check_ptr(plan, "plan", true));
+    const AdamWPlan &p = *(const AdamWPlan *)plan;
+    if (p.magic != kPlanMagic) return fail(FQ_ERR_DESC, "plan was not made by fq_adamw_plan");
+    if (p.state_type != hyper->state_type)
+        return fail(FQ_ERR_DESC, "hyper->state_type=%d is not the plan's %d", hyper->state_type,
+                    p.state_type);
+    if (!p.count) return ok();
+    FQ_TRY(check_ptr(plan_device, "plan_device", true));
+    fqimpl::AdamWStep a = adamw_step_of(*hyper);
+    a.count = p.count;
+    a.tiles = p.tiles;
+    const auto *entries = (const fqimpl::AdamWTensor *)((const AdamWPlan *)plan_device + 1);
+    const auto *first = (const uint32_t *)(entries + p.count);
+    return device_status(fqimpl::launch_adamw_plan(a, entries, first, first + p.count,
+                                                   p.state_type == FQ_STATE_F8,
+                                                   (hipStream_t)stream),
+                         "AdamW launch");
 }
 
 }  // extern "C"

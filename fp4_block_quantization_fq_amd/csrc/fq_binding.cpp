@@ -319,14 +319,14 @@ PyObject *moe_combine_bwd(PyObject *, PyObject *const *args, Py_ssize_t nargs)
     });
 }
 
-// (address of the tensors' table, their number, state_type, lr, beta1, beta2,
-//  eps, step, seed, grad_scale, stream)
+// (address of the plan in host memory, the plan in device memory or None,
+//  state_type, lr, beta1, beta2, eps, step, seed, grad_scale, stream)
 PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t nargs)
 {
     Call c(args, nargs, 11);
     if (!c.ok) return nullptr;
-    const auto *tensors = (const fq_adamw_tensor *)(uintptr_t)c.u64(0);
-    const long long count = c.i64(1);
+    const void *plan = (const void *)(uintptr_t)c.u64(0);
+    const void *plan_device = c.bytes(1, 0, "plan");
     fq_adamw_hyper h = {};
     h.state_type = (int32_t)c.i64(2);
     h.lr = c.f64(3);
@@ -337,7 +337,7 @@ PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t nargs)
     h.seed = c.u64(8);
     h.grad_scale = (const float *)c.typed(9, at::kFloat, 1, "grad_scale");
     void *st = c.stream(10);
-    return launch(c, [&] { return fq_adamw_step(&h, tensors, count, st); });
+    return launch(c, [&] { return fq_adamw_step_plan(&h, plan, plan_device, st); });
 }
 
 // A tensor without storage or strides throws where it is asked for them: that

@@ -210,16 +210,23 @@ struct AdamWTensor {
     float lr_mult, weight_decay;
     int g_f32;
 };
-struct AdamWArgs {
+struct AdamWStep {           // what all tensors of a launch share
     uint32_t count;          // tensors of this launch, all with n > 0
+    uint32_t tiles;          // of all of them
     float lr, beta1, one_beta1, beta2, one_beta2, eps, inv_bc1, inv_sqrt_bc2;
     const float *grad_scale; // device scalar or null
     uint32_t step, seed_lo, seed_hi;
-    uint32_t first[kAdamWTensors];          // first workgroup of each tensor
+};
+struct AdamWArgs {
+    AdamWStep step;
+    uint32_t first[kAdamWTensors];          // first tile of each tensor
     uint32_t index[kAdamWTensors];          // number of each tensor in the whole list
     AdamWTensor t[kAdamWTensors];
 };
-uint32_t adamw_workgroups(int64_t n);       // workgroups that n elements take
-hipError_t launch_adamw(const AdamWArgs &a, bool f8, uint32_t grid, hipStream_t stream);
+uint32_t adamw_tiles(int64_t n, bool f8);   // tiles that n elements take
+hipError_t launch_adamw(const AdamWArgs &a, bool f8, hipStream_t stream);
+// The same with the table in device memory.
+hipError_t launch_adamw_plan(const AdamWStep &a, const AdamWTensor *t, const uint32_t *first,
+                             const uint32_t *index, bool f8, hipStream_t stream);
 
 }  // namespace fqimpl

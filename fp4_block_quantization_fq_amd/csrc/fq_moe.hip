@@ -170,7 +170,10 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_place(fqimpl::MoeSortArgs 
 // LANES 0, a workgroup of as many waves as the row has 64 chunks of 8 elements
 // (512 threads at most, which then walk over the row).  A lane has one chunk
 // and moves it for up to four of the token's assignments at a time, all loads
-// issued together: what bounds these kernels is the bytes a CU has in flight.
+// issued together: what bounds these kernels is the bytes a CU has in flight
+// (a wave a token instead of 360 lanes: combine 46.2 us instead of 41.6 at 8192
+// tokens of 2880, 7.6 instead of 3.2 at 16; 8 lanes instead of a wave for rows
+// of 64: 8.5 instead of 25.7 at 65536 tokens).
 constexpr int kThreads = 256;               // of a workgroup of several tokens
 constexpr int kMostThreads = 512;
 constexpr int kPadRows = 16;
@@ -237,7 +240,7 @@ __device__ __forceinline__ void dispatch_unit(const fqimpl::MoeRowsArgs &a, uint
     for (uint32_t c = chunk_of<LANES>(); c < chunks; c += LANES ? LANES : blockDim.x) {
         u32w4 v;
         if (F8 == fqimpl::F8_NONE) {
-            v = load16<NT>((const u32w4 *)((const uint16_t *)a.x + t * a.H + c * 8));
+            v = *(const u32w4 *)((const uint16_t *)a.x + t * a.H + c * 8);
         } else {
             float f[8], s;
             e4m3_decode8(*(const u32w2 *)((const uint8_t *)a.x + t * a.H + c * 8), f);
@@ -400,8 +403,12 @@ hipError_t by_width(const fqimpl::MoeRowsArgs &a, F launch)
                   (uint32_t)(threads < kMostThreads ? threads : kMostThreads));
 }
 
-// Streaming accesses from this many elements of rows on.
-constexpr int64_t kStreamElems = int64_t(1) << 24;
+// Streaming accesses from this many elements of sorted rows on, where they
+// leave the caches.  Of 8192 tokens (94 M elements) and 2048 (24 M): combine
+// 41.6 us streaming, 46.8 not, and 13.1, 12.1; dispatch (its stores) 41.3, 50.6
+// and 15.6, 15.5; combine's backward 76, 90 and 25.5, 29.2, of 1024 tokens (12 M)
+// 16.0, 14.5.
+constexpr int64_t kStreamForward = int64_t(1) << 25, kStreamBwd = int64_t(1) << 24;
 
 }  // namespace
 
@@ -437,7 +444,7 @@ static hipError_t dispatch(const MoeRowsArgs &a, hipStream_t stream)
         constexpr int kLanes = decltype(lanes)::value;
         const uint32_t units = work + pads;
         const dim3 grid(units < kMaxGrid ? units : kMaxGrid), block(threads);
-        if (a.rows * a.H < kStreamElems)
+        if (a.T * a.k * a.H < kStreamForward)
             k_moe_dispatch<kLanes, F8, false><<<grid, block, 0, stream>>>(a, work, units);
         else
             k_moe_dispatch<kLanes, F8, true><<<grid, block, 0, stream>>>(a, work, units);
@@ -457,7 +464,7 @@ hipError_t launch_moe_combine(const MoeRowsArgs &a, hipStream_t stream)
     return by_width(a, [&](auto lanes, uint32_t work, uint32_t threads) {
         constexpr int kLanes = decltype(lanes)::value;
         const dim3 grid(work < kMaxGrid ? work : kMaxGrid), block(threads);
-        if (a.T * a.k * a.H < kStreamElems)
+        if (a.T * a.k * a.H < kStreamForward)
             k_moe_combine<kLanes, false><<<grid, block, 0, stream>>>(a, work);
         else
             k_moe_combine<kLanes, true><<<grid, block, 0, stream>>>(a, work);
@@ -472,7 +479,7 @@ hipError_t launch_moe_combine_bwd(const MoeRowsArgs &a, hipStream_t stream)
         constexpr int kLanes = decltype(lanes)::value;
         const uint32_t units = work + pads;
         const dim3 grid(units < kMaxGrid ? units : kMaxGrid), block(threads);
-        if (a.rows * a.H < kStreamElems)
+        if (a.T * a.k * a.H < kStreamBwd)
             k_moe_combine_bwd<kLanes, false><<<grid, block, 0, stream>>>(a, work, units);
         else
             k_moe_combine_bwd<kLanes, true><<<grid, block, 0, stream>>>(a, work, units);

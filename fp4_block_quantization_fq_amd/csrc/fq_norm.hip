@@ -55,7 +55,7 @@ template <int LANES>
 __device__ __forceinline__ float row_sum(float v, float (*red)[16], int slot)
 {
     if (LANES <= 64) return lanes_sum<LANES>(v);
-    v = wave_sum(v);
+    v = lanes_sum<64>(v);
     const int wave = threadIdx.x >> 6, first = group_of<LANES>() * (LANES / 64);
     if ((threadIdx.x & 63) == 0) red[slot][wave] = v;
     __syncthreads();
@@ -147,7 +147,7 @@ __global__ __launch_bounds__((threads_of<LANES, kFwdThreads>())) void k_rmsnorm_
         float scale = 0.0f, inv = 0.0f;
         if (F8 == fqimpl::F8_ROW) {
 #pragma unroll
-            for (int i = 0; i < NCH; ++i) top = max(top, absmax8(h[i]));
+            for (int i = 0; i < NCH; ++i) top = max(top, absmax(h[i]));
             top = row_max<LANES>(top, red, 2 + slot);
             scale = __builtin_fmaxf(as_f(top) * (1.0f / 448.0f), 0x1p-126f);
             inv = 1.0f / scale;
@@ -162,7 +162,7 @@ __global__ __launch_bounds__((threads_of<LANES, kFwdThreads>())) void k_rmsnorm_
             if (n <= 0) continue;
             if (F8 != fqimpl::F8_NONE) {
                 if (F8 == fqimpl::F8_MX) {
-                    top = dpp_max_xor2(dpp_max_xor1(absmax8(h[i])));
+                    top = dpp_max_xor2(dpp_max_xor1(absmax(h[i])));
                     const uint32_t code = mx8_scale_code(top);
                     scale = e8m0_value(code);
                     inv = e8m0_recip(code);

@@ -132,13 +132,25 @@ __device__ __forceinline__ void store8(float *__restrict__ p, int n, const float
 
 // ---- across the wave ----------------------------------------------------------
 // DPP inside a 16-lane row (quad permutes, then the row's halves and the row
-// mirrored, each pairing lanes that hold equal partial results), two lane
-// exchanges across the four rows.  Every lane of a group gets the same value.
+// mirrored, each pairing lanes that hold equal partial results), and swaps of
+// rows with a copy of the same value across the four rows: the two results hold
+// one row's value and its neighbour's in both rows' lanes.  Every lane of a
+// group gets the same value.
 template <int CTRL>
 __device__ __forceinline__ float dpp_f(float v)
 {
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
 }
+template <int ROWS, typename F>
+__device__ __forceinline__ uint32_t across_rows(uint32_t v, F join)
+{
+    const auto r = ROWS == 1 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                             : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return join(r[0], r[1]);
+}
+__device__ __forceinline__ uint32_t add_f32(uint32_t a, uint32_t b) { return as_u(as_f(a) + as_f(b)); }
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return max(a, b); }
+
 // Sum over groups of LANES neighbouring lanes.
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float v)
@@ -147,33 +159,29 @@ __device__ __forceinline__ float lanes_sum(float v)
     v += dpp_f<0x4E>(v);
     v += dpp_f<0x141>(v);
     if (LANES >= 16) v += dpp_f<0x140>(v);
-    if (LANES >= 32) v += __shfl_xor(v, 16);
-    if (LANES >= 64) v += __shfl_xor(v, 32);
+    if (LANES >= 32) v = as_f(across_rows<1>(as_u(v), add_f32));
+    if (LANES >= 64) v = as_f(across_rows<2>(as_u(v), add_f32));
     return v;
 }
-__device__ __forceinline__ float wave_sum(float v) { return lanes_sum<64>(v); }
-// maximum over the 16 lanes of a DPP row (values >= 0, or their bits)
-__device__ __forceinline__ uint32_t dpp_max_16lanes(uint32_t v)
-{
-    v = dpp_max_8lanes(v);
-    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
-}
+// Maximum over groups of LANES neighbouring lanes (values >= 0, or their bits).
 template <int LANES>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v)
 {
-    v = LANES >= 16 ? dpp_max_16lanes(v) : dpp_max_8lanes(v);
-    if (LANES >= 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16));
-    if (LANES >= 64) v = max(v, (uint32_t)__shfl_xor((int)v, 32));
+    v = dpp_max_8lanes(v);
+    if (LANES >= 16) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
+    if (LANES >= 32) v = across_rows<1>(v, max_u32);
+    if (LANES >= 64) v = across_rows<2>(v, max_u32);
     return v;
 }
 
-// bits of the largest magnitude of eight values; a NaN's bits exceed
-// infinity's, which exceed every finite value's
-__device__ __forceinline__ uint32_t absmax8(const float (&v)[8])
+// bits of the largest magnitude of N values; a NaN's bits exceed infinity's,
+// which exceed every finite value's
+template <int N>
+__device__ __forceinline__ uint32_t absmax(const float (&v)[N])
 {
     uint32_t m = as_u(v[0]) & 0x7FFFFFFFu;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = max(m, as_u(v[i]) & 0x7FFFFFFFu);
+    for (int i = 1; i < N; ++i) m = max(m, as_u(v[i]) & 0x7FFFFFFFu);
     return m;
 }
 

@@ -568,6 +568,19 @@ typedef struct {
 fq_status fq_adamw_step(const fq_adamw_hyper *hyper, const fq_adamw_tensor *tensors,
                         int64_t count, void *stream);
 
+/* The same list for many steps, in one launch a step whatever its length
+ * (fq_adamw_step launches once per 32 tensors).  fq_adamw_plan checks the
+ * tensors as fq_adamw_step does and writes fq_adamw_plan_size bytes to `plan`
+ * (host memory, 16-byte aligned); the caller keeps them and copies them to
+ * device memory once (16-byte aligned).  fq_adamw_step_plan takes both copies;
+ * hyper->state_type must be the plan's.  A plan holds the tensors' addresses:
+ * their contents may change between steps, where they are may not. */
+size_t fq_adamw_plan_size(int64_t count);
+fq_status fq_adamw_plan(const fq_adamw_tensor *tensors, int64_t count, int32_t state_type,
+                        void *plan, size_t plan_bytes);
+fq_status fq_adamw_step_plan(const fq_adamw_hyper *hyper, const void *plan,
+                             const void *plan_device, void *stream);
+
 /* Static description of a status code. */
 const char *fq_status_string(fq_status s);
 

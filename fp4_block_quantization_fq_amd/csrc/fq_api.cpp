@@ -1296,9 +1296,11 @@ fq_status fq_rmsnorm_bwd(const void *dy_bf16, const void *h, int32_t stream_type
     a.cols = cols;
     a.dh = dh;
     a.dx = dx_bf16;
+    a.dgamma = dgamma;
     a.partials = (float *)ws;
     a.groups = 0;
-    return device_status(fqimpl::launch_rmsnorm_bwd(a, dgamma, (hipStream_t)stream),
+    a.few = false;
+    return device_status(fqimpl::launch_rmsnorm_bwd(a, (hipStream_t)stream),
                          "norm backward launch");
 }
 
@@ -1316,9 +1318,7 @@ int64_t fq_moe_rows(int64_t tokens, int64_t k, int64_t experts, int64_t align)
 size_t fq_moe_sort_workspace_size(int64_t tokens, int64_t k, int64_t experts)
 {
     if (check_moe(tokens, k, experts) != FQ_OK) return 0;
-    const int64_t n = tokens * k, chunk = fqimpl::moe_sort_chunk(n);
-    const int64_t chunks = (n + chunk - 1) / chunk;
-    return chunks > 1 ? (size_t)chunks * experts * sizeof(uint32_t) : 0;
+    return fqimpl::moe_sort_counts(tokens * k, experts) * sizeof(uint32_t);
 }
 
 fq_status fq_moe_sort(const int32_t *experts_of, int64_t tokens, int64_t k, int64_t experts,

@@ -158,12 +158,14 @@ struct NormBwdArgs {
     int64_t rows, cols;
     void *dh;                // in h's type (may be dres)
     void *dx;                // BF16 copy of dh, or null
-    float *partials;         // groups * cols column sums
-    int64_t groups;
+    float *dgamma;           // FP32 [cols] or null
+    float *partials;         // groups * cols column sums (workspace)
+    int64_t groups;          // set by the launcher, as the next
+    bool few;                // rows and dgamma in one launch
 };
 // groups of column sums the backward leaves (its workspace holds as many rows)
 int64_t rmsnorm_bwd_groups(int64_t rows, int64_t cols);
-hipError_t launch_rmsnorm_bwd(NormBwdArgs a, float *dgamma, hipStream_t stream);
+hipError_t launch_rmsnorm_bwd(NormBwdArgs a, hipStream_t stream);
 
 // fq_moe.hip
 constexpr int kMoeMaxExperts = 1024;
@@ -176,10 +178,10 @@ struct MoeSortArgs {
     int32_t *offsets;        // [E + 1]
     int32_t *pos;            // [n]
     int32_t *src;            // [rows]
-    uint32_t *ws;            // counts of every chunk and expert
+    uint32_t *ws;            // counts of every chunk and expert (not for few assignments)
     uint32_t chunk;
 };
-uint32_t moe_sort_chunk(int64_t n);         // assignments of a workgroup
+size_t moe_sort_counts(int64_t n, int64_t E);   // counts that the workspace holds
 hipError_t launch_moe_sort(MoeSortArgs a, hipStream_t stream);
 struct MoeRowsArgs {
     int64_t T, k, H, rows;

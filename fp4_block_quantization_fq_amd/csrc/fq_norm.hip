@@ -209,7 +209,7 @@ __device__ __forceinline__ void renew(Raw8<float> &r)
 // stays as it was loaded (a BF16 element in half a register) and is unpacked
 // twice, before and after the row's sum; gamma waits in LDS.
 template <int LANES, int NCH, typename T, bool ANY, bool NT>
-__global__ __launch_bounds__((threads_of<LANES, kBwdThreads>()), 2) void k_rmsnorm_bwd(fqimpl::NormBwdArgs a)
+__device__ __forceinline__ void bwd_rows(const fqimpl::NormBwdArgs &a, uint32_t workgroups)
 {
     constexpr int kWgThreads = threads_of<LANES, kBwdThreads>(), kGroups = kWgThreads / LANES;
     // dres with the other loads, unless it is wide and a lane's share long
@@ -219,7 +219,7 @@ __global__ __launch_bounds__((threads_of<LANES, kBwdThreads>()), 2) void k_rmsno
     __shared__ u32w4 gamma[NCH * 2][LANES];
     const uint32_t l = threadIdx.x % LANES;
     const int group = group_of<LANES>();
-    const int64_t groups = (int64_t)gridDim.x * kGroups;
+    const int64_t groups = (int64_t)workgroups * kGroups;
     const float inv_cols = 1.0f / (float)a.cols;
     float acc[NCH][8];
 #pragma unroll
@@ -319,6 +319,60 @@ __global__ __launch_bounds__((threads_of<LANES, kBwdThreads>()), 2) void k_rmsno
     }
 }
 
+template <int LANES, int NCH, typename T, bool ANY, bool NT>
+__global__ __launch_bounds__((threads_of<LANES, kBwdThreads>()), 2) void k_rmsnorm_bwd(fqimpl::NormBwdArgs a)
+{
+    bwd_rows<LANES, NCH, T, ANY, NT>(a, gridDim.x);
+}
+
+// dgamma of 64 columns (eight lanes of 8) over all rows, by one workgroup.
+template <int THREADS, typename T, bool ANY>
+__device__ __forceinline__ void column_sums(const fqimpl::NormBwdArgs &a, int64_t c0)
+{
+    constexpr int kWaves = THREADS / 64;
+    __shared__ float sums[kWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c = c0 + (threadIdx.x % 8) * 8;
+    const int n = (int)max((int64_t)0, min((int64_t)8, a.cols - c));
+    float acc[8] = {};
+    if (n > 0)
+#pragma unroll 4
+        for (int64_t row = threadIdx.x / 8; row < a.rows; row += THREADS / 8) {
+            float d[8], h[8];
+            load8<ANY>((const uint16_t *)a.dy + row * a.cols + c, n, d);
+            load8<ANY>((const T *)a.h + row * a.cols + c, n, h);
+            const float r = a.rstd[row];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(d[e], h[e] * r, acc[e]);
+        }
+    // lanes with the same columns are eight apart
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        acc[e] += dpp_f<0x128>(acc[e]);
+        acc[e] = as_f(across_rows<1>(as_u(acc[e]), add_f32));
+        acc[e] = as_f(across_rows<2>(as_u(acc[e]), add_f32));
+    }
+    if (lane < 8)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sums[wave][lane * 8 + e] = acc[e];
+    __syncthreads();
+    if (threadIdx.x >= 64 || c0 + threadIdx.x >= a.cols) return;
+    float v = sums[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v += sums[w][threadIdx.x];
+    a.dgamma[c0 + threadIdx.x] = v;
+}
+
+// The backward of few rows in one launch: the workgroups from a.groups on do
+// dgamma, which needs no row's sum, 64 columns each, reading dy and h again.
+template <int LANES, int NCH, typename T, bool ANY>
+__global__ __launch_bounds__((threads_of<LANES, kBwdThreads>())) void k_rmsnorm_bwd_few(fqimpl::NormBwdArgs a)
+{
+    constexpr int kWgThreads = threads_of<LANES, kBwdThreads>();
+    if (blockIdx.x >= a.groups) column_sums<kWgThreads, T, ANY>(a, (blockIdx.x - a.groups) * 64);
+    else bwd_rows<LANES, NCH, T, ANY, false>(a, (uint32_t)a.groups);
+}
+
 // dgamma[c] = sum over the workgroups' sums, in their order: a workgroup takes
 // 16 columns (64-byte pieces of a row), 64 threads each a contiguous share of
 // the rows, and one adds their sums.
@@ -400,6 +454,12 @@ struct Fwd {
     }
 };
 
+// The gradients of the rows and of gamma in one launch while there are few rows:
+// reading dy and h again, from the caches, then takes less than a second launch
+// (one and two: 333x1000 FP32 3.6 and 8.3 us, 333x2880 4.7 and 9.6, 1024x2880 9.3
+// and 12.5, 2048x2880 15.2 and 14.7, 4096x512 18.9 and 8.5).
+constexpr int64_t kFewRows = 1024;
+
 template <int LANES, int NCH>
 struct Bwd {
     static constexpr int kLanesMost = 512;      // 1024 lanes would have 128 registers each: too few
@@ -407,6 +467,12 @@ struct Bwd {
     static hipError_t launch(const fqimpl::NormBwdArgs &a, hipStream_t st)
     {
         const dim3 grid((uint32_t)a.groups), block(threads_of<LANES, kBwdThreads>());
+        if (a.few) {
+            const dim3 all((uint32_t)(a.groups + (a.cols + 63) / 64));
+            if (a.cols % 8) k_rmsnorm_bwd_few<LANES, NCH, T, true><<<all, block, 0, st>>>(a);
+            else k_rmsnorm_bwd_few<LANES, NCH, T, false><<<all, block, 0, st>>>(a);
+            return hipGetLastError();
+        }
         if (a.cols % 8) k_rmsnorm_bwd<LANES, NCH, T, true, false><<<grid, block, 0, st>>>(a);
         else if (a.rows * a.cols < kStreamElems) k_rmsnorm_bwd<LANES, NCH, T, false, false><<<grid, block, 0, st>>>(a);
         else k_rmsnorm_bwd<LANES, NCH, T, false, true><<<grid, block, 0, st>>>(a);
@@ -439,14 +505,22 @@ int64_t rmsnorm_bwd_groups(int64_t rows, int64_t cols)
     return wgs < most ? wgs : most;
 }
 
-hipError_t launch_rmsnorm_bwd(NormBwdArgs a, float *dgamma, hipStream_t stream)
+static bool few_rows(const NormBwdArgs &a)
+{
+    // a gradient written over dy or h would be read as one of them
+    return a.dgamma && a.rows <= kFewRows && a.dh != a.h && a.dh != a.dy && a.dx != a.h &&
+           a.dx != a.dy;
+}
+
+hipError_t launch_rmsnorm_bwd(NormBwdArgs a, hipStream_t stream)
 {
     a.groups = rmsnorm_bwd_groups(a.rows, a.cols);
-    if (!dgamma) a.partials = nullptr;
-    hipError_t e = by_width<Bwd>(a, stream);
-    if (e != hipSuccess || !dgamma) return e;
+    a.few = few_rows(a);
+    if (!a.dgamma || a.few) a.partials = nullptr;
+    const hipError_t e = by_width<Bwd>(a, stream);
+    if (e != hipSuccess || !a.partials) return e;
     k_column_sum<<<dim3((uint32_t)((a.cols + kSumCols - 1) / kSumCols)), dim3(kSumThreads), 0, stream>>>(
-        a.partials, a.groups, a.cols, dgamma);
+        a.partials, a.groups, a.cols, a.dgamma);
     return hipGetLastError();
 }
 

@@ -83,11 +83,15 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_place(fqimpl::MoeSortArgs 
     // total[e]: assignments from this chunk on (all, from the workspace), next[e]:
     // those before it
     if (!a.ws) {
-        // each chunk starts at a multiple of the stride: one side for a whole turn
-#pragma unroll 8
-        for (int64_t i = tid; i < a.n; i += kSortThreads) {
-            const uint32_t o = expert_of(a.ids, i, a.n, a.E);
-            if (o < a.E) atomicAdd(i < lo ? &next[o] : &total[o], 1u);
+        constexpr int kBatch = kCountAll / kSortThreads;     // loads in flight together
+        uint32_t o[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            o[u] = (uint32_t)a.ids[min((int64_t)(u * kSortThreads + tid), a.n - 1)];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t i = u * kSortThreads + tid;
+            if (i < a.n && o[u] < a.E) atomicAdd(i < lo ? &next[o[u]] : &total[o[u]], 1u);
         }
     } else {
         for (uint32_t i = tid; i < gridDim.x * a.E; i += kSortThreads) {

@@ -334,17 +334,29 @@ __device__ __forceinline__ void column_sums(const fqimpl::NormBwdArgs &a, int64_
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t c = c0 + (threadIdx.x % 8) * 8;
     const int n = (int)max((int64_t)0, min((int64_t)8, a.cols - c));
+    constexpr int kBatch = 4, kStep = THREADS / 8;     // rows in flight together
     float acc[8] = {};
-    if (n > 0)
-#pragma unroll 4
-        for (int64_t row = threadIdx.x / 8; row < a.rows; row += THREADS / 8) {
-            float d[8], h[8];
-            load8<ANY>((const uint16_t *)a.dy + row * a.cols + c, n, d);
-            load8<ANY>((const T *)a.h + row * a.cols + c, n, h);
-            const float r = a.rstd[row];
+    for (int64_t row0 = threadIdx.x / 8; n > 0 && row0 < a.rows; row0 += kBatch * kStep) {
+        Raw8<uint16_t> dy[kBatch];
+        Raw8<T> hr[kBatch];
+        float r[kBatch];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(d[e], h[e] * r, acc[e]);
+        for (int b = 0; b < kBatch; ++b) {
+            const int64_t row = min(row0 + b * kStep, a.rows - 1);
+            load_raw8<ANY>((const uint16_t *)a.dy + row * a.cols + c, n, dy[b]);
+            load_raw8<ANY>((const T *)a.h + row * a.cols + c, n, hr[b]);
+            r[b] = a.rstd[row];
         }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (row0 + b * kStep >= a.rows) break;
+            float d[8], h[8];
+            unpack8(dy[b], d);
+            unpack8(hr[b], h);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(d[e], h[e] * r[b], acc[e]);
+        }
+    }
     // lanes with the same columns are eight apart
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -449,16 +461,21 @@ struct Fwd {
     }
     static hipError_t go(const fqimpl::NormFwdArgs &a, hipStream_t st)
     {
-        if (!a.res) return by_output<0>(a, st);
+        // Without a residual a lane has half the bytes in flight: half the lanes,
+        // two chunks each (16384x2880 in BF16 37.0 us instead of 40.5, with 8-bit
+        // rows 47 instead of 58; 8471x6304 with MX blocks 54 instead of 72)
+        constexpr int kHalf = LANES > 64 ? 2 : 1;
+        if (!a.res) return Fwd<LANES / kHalf, NCH * kHalf>::template by_output<0>(a, st);
         return a.stream_f32 ? by_output<2>(a, st) : by_output<1>(a, st);
     }
 };
 
-// The gradients of the rows and of gamma in one launch while there are few rows:
-// reading dy and h again, from the caches, then takes less than a second launch
-// (one and two: 333x1000 FP32 3.6 and 8.3 us, 333x2880 4.7 and 9.6, 1024x2880 9.3
-// and 12.5, 2048x2880 15.2 and 14.7, 4096x512 18.9 and 8.5).
-constexpr int64_t kFewRows = 1024;
+// The gradients of the rows and of gamma in one launch while reading dy and h
+// again, from the caches, takes less than a second launch and its column sums
+// (one and two: 333x1000 FP32 3.6 and 8.3 us, 1024x2880 9.3 and 12.5, 2048x2880
+// 15.2 and 14.7, 654x6072 12.2 and 14.7, 1024x6072 17.6 and 16.7; rows that start
+// at any element 412x6073 11.3 and 16.1, 654x6073 18.9 and 17.8).
+constexpr int64_t kFewRows = 1024, kFewElems = int64_t(1) << 22, kFewElemsAny = int64_t(1) << 21;
 
 template <int LANES, int NCH>
 struct Bwd {
@@ -493,29 +510,36 @@ hipError_t launch_rmsnorm_fwd(const NormFwdArgs &a, hipStream_t stream)
     return by_width<Fwd>(a, stream);
 }
 
+// Workgroups that would take all rows at once.
+static int64_t rows_workgroups(int64_t rows, int64_t cols)
+{
+    int64_t lanes = 8;
+    while (lanes < kBwdThreads && lanes * 8 < cols) lanes *= 2;
+    const int64_t per_wg = kBwdThreads / lanes;
+    return (rows + per_wg - 1) / per_wg;
+}
+
 // Workgroups that walk over the rows, each leaving a row of column sums: two
 // on each of 256 CUs, one where a row has 1024 lanes (or 512 with many
 // registers), no more than there are rows for.
 int64_t rmsnorm_bwd_groups(int64_t rows, int64_t cols)
 {
-    int64_t lanes = 8;
-    while (lanes < 1024 && lanes * 8 < cols) lanes *= 2;
-    const int64_t per_wg = lanes < kBwdThreads ? kBwdThreads / lanes : 1;
-    const int64_t wgs = (rows + per_wg - 1) / per_wg, most = lanes < 1024 ? 512 : 256;
+    const int64_t wgs = rows_workgroups(rows, cols), most = cols <= kBwdThreads * 8 ? 512 : 256;
     return wgs < most ? wgs : most;
 }
 
 static bool few_rows(const NormBwdArgs &a)
 {
     // a gradient written over dy or h would be read as one of them
-    return a.dgamma && a.rows <= kFewRows && a.dh != a.h && a.dh != a.dy && a.dx != a.h &&
+    return a.dgamma && a.rows <= kFewRows &&
+           a.rows * a.cols <= (a.cols % 8 ? kFewElemsAny : kFewElems) && a.dh != a.h && a.dh != a.dy && a.dx != a.h &&
            a.dx != a.dy;
 }
 
 hipError_t launch_rmsnorm_bwd(NormBwdArgs a, hipStream_t stream)
 {
-    a.groups = rmsnorm_bwd_groups(a.rows, a.cols);
     a.few = few_rows(a);
+    a.groups = a.few ? rows_workgroups(a.rows, a.cols) : rmsnorm_bwd_groups(a.rows, a.cols);
     if (!a.dgamma || a.few) a.partials = nullptr;
     const hipError_t e = by_width<Bwd>(a, stream);
     if (e != hipSuccess || !a.partials) return e;

@@ -78,13 +78,72 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, float (*red)[16], int sl
     return v;
 }
 
-// gamma of eight columns in either type
+// Rows whose length is no multiple of 8 (ANY) start at any element.  A lane's
+// chunks lie where 8-element boundaries of the whole array are, so that all of
+// them but a row's first and last are 16-byte accesses: `shift` elements of the
+// first one belong to the row before, and element e of the chunk at `pos` is
+// column pos - shift + e.
+struct Span {
+    int lo, hi;              // the row's elements of a chunk; hi 0: none
+};
 template <bool ANY>
-__device__ __forceinline__ void load_gamma(const void *gamma, int f32, int64_t c, int n,
-                                           float (&g)[8])
+__device__ __forceinline__ Span span_of(uint32_t pos, int shift, int64_t cols, bool live)
 {
-    if (f32) load8<ANY>((const float *)gamma + c, n, g);
-    else load8<ANY>((const uint16_t *)gamma + c, n, g);
+    if (!ANY) return {0, live && pos < cols ? 8 : 0};
+    const int lo = max(0, shift - (int)pos), hi = min(8, (int)cols + shift - (int)pos);
+    return live && hi > lo ? Span{lo, hi} : Span{0, 0};
+}
+__device__ __forceinline__ bool inside(int e, Span s) { return e >= s.lo && e < s.hi; }
+
+__device__ __forceinline__ void clear_outside(Raw8<uint16_t> &r, Span s)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r.w[i] &= (inside(2 * i, s) ? 0xFFFFu : 0u) | (inside(2 * i + 1, s) ? 0xFFFF0000u : 0u);
+}
+__device__ __forceinline__ void clear_outside(Raw8<float> &r, Span s)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r.a[i] = inside(i, s) ? r.a[i] : 0u;
+        r.b[i] = inside(i + 4, s) ? r.b[i] : 0u;
+    }
+}
+// The chunk of an array at p (a chunk boundary) + pos; `left` elements of the
+// array are left from p on.  What is not the row's reads as 0.
+template <bool ANY, bool NT, typename T>
+__device__ __forceinline__ void load_span(const T *__restrict__ p, uint32_t pos, Span s, int left,
+                                          Raw8<T> &r)
+{
+    if (!ANY) return load_raw8<false, NT>(p + pos, 8, r);
+    if ((int)pos + 8 <= left) load_raw8<false, NT>(p + pos, 8, r);
+    else load_raw8<true>(p + pos, left - (int)pos, r);
+    if (s.lo > 0 || s.hi < 8) clear_outside(r, s);
+}
+template <bool ANY, bool NT, typename T>
+__device__ __forceinline__ void store_span(T *__restrict__ p, uint32_t pos, Span s, const float (&v)[8])
+{
+    if (!ANY || (s.lo == 0 && s.hi == 8)) return store8<false, NT>(p + pos, 8, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (inside(e, s)) store1(p + pos + e, v[e]);
+}
+// gamma of a chunk's columns in either type, 0 outside the row
+template <bool ANY, typename T>
+__device__ __forceinline__ void load_columns(const T *__restrict__ gamma, uint32_t pos, int shift,
+                                             Span s, float (&g)[8])
+{
+    const T *q = gamma + ((int)pos - shift);
+    if (s.lo == 0 && s.hi == 8) return load8<ANY>(q, 8, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = inside(e, s) ? load1(q + e) : 0.0f;
+}
+template <bool ANY>
+__device__ __forceinline__ void load_gamma(const void *gamma, int f32, uint32_t pos, int shift,
+                                           Span s, float (&g)[8])
+{
+    if (f32) load_columns<ANY>((const float *)gamma, pos, shift, s, g);
+    else load_columns<ANY>((const uint16_t *)gamma, pos, shift, s, g);
 }
 
 template <int STREAM> struct StreamType { typedef uint16_t type; };
@@ -105,28 +164,37 @@ __global__ __launch_bounds__((threads_of<LANES, kFwdThreads>())) void k_rmsnorm_
         const int64_t row = r0 + group;
         const bool live = row < a.rows;
         const int64_t base = (live ? row : 0) * a.cols;
+        const int shift = ANY ? (int)(base & 7) : 0;
+        const int64_t start = base - shift;
+        const int left = (int)min(a.rows * a.cols - start, (int64_t)1 << 30);
         float h[NCH][8];
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            const uint32_t c = (i * LANES + l) * 8;
-            const int n = live ? min(8, (int)a.cols - (int)c) : 0;
-            if (n <= 0) {
+            const uint32_t pos = (i * LANES + l) * 8;
+            const Span s = span_of<ANY>(pos, shift, a.cols, live);
+            if (s.hi == 0) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
                 continue;
             }
-            load8<ANY, NT>((const uint16_t *)a.x + base + c, n, h[i]);
+            Raw8<uint16_t> x;
+            load_span<ANY, NT>((const uint16_t *)a.x + start, pos, s, left, x);
             if (STREAM) {
+                Raw8<T> res;
                 float r[8];
-                load8<ANY, NT>((const T *)a.res + base + c, n, r);
+                load_span<ANY, NT>((const T *)a.res + start, pos, s, left, res);
+                unpack8(x, h[i]);
+                unpack8(res, r);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     h[i][e] = h[i][e] + r[e];
                     // the norm sees the stream's stored value, as the backward will
                     if (STREAM == 1) h[i][e] = (float)(__bf16)h[i][e];
                 }
-                store8<ANY, NT>((T *)a.h + base + c, n, h[i]);
+                store_span<ANY, NT>((T *)a.h + start, pos, s, h[i]);
+            } else {
+                unpack8(x, h[i]);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss += h[i][e] * h[i][e];
@@ -135,11 +203,11 @@ __global__ __launch_bounds__((threads_of<LANES, kFwdThreads>())) void k_rmsnorm_
         if (a.rstd && live && l == 0) a.rstd[row] = rstd;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            const uint32_t c = (i * LANES + l) * 8;
-            const int n = live ? min(8, (int)a.cols - (int)c) : 0;
-            if (n <= 0) continue;
+            const uint32_t pos = (i * LANES + l) * 8;
+            const Span s = span_of<ANY>(pos, shift, a.cols, live);
+            if (s.hi == 0) continue;
             float g[8];
-            load_gamma<ANY>(a.gamma, a.gamma_f32, c, n, g);
+            load_gamma<ANY>(a.gamma, a.gamma_f32, pos, shift, s, g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[i][e] = (h[i][e] * rstd) * g[e];
         }
@@ -157,10 +225,11 @@ __global__ __launch_bounds__((threads_of<LANES, kFwdThreads>())) void k_rmsnorm_
         slot ^= 1;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            const uint32_t c = (i * LANES + l) * 8;
-            const int n = live ? min(8, (int)a.cols - (int)c) : 0;
-            if (n <= 0) continue;
-            if (F8 != fqimpl::F8_NONE) {
+            const uint32_t pos = (i * LANES + l) * 8;
+            const Span s = span_of<ANY>(pos, shift, a.cols, live);
+            if (s.hi == 0) continue;
+            if (F8 != fqimpl::F8_NONE) {          // not with ANY
+                const int64_t at = base + pos;
                 if (F8 == fqimpl::F8_MX) {
                     top = dpp_max_xor2(dpp_max_xor1(absmax(h[i])));
                     const uint32_t code = mx8_scale_code(top);
@@ -168,7 +237,7 @@ __global__ __launch_bounds__((threads_of<LANES, kFwdThreads>())) void k_rmsnorm_
                     inv = e8m0_recip(code);
                     if (top >= 0x7F800000u) scale = as_f(0x7FC00000u);
                     if (a.scales && (l & 3) == 0)
-                        ((uint8_t *)a.scales)[(base + c) >> 5] = (uint8_t)(top >= 0x7F800000u ? 255u : code);
+                        ((uint8_t *)a.scales)[at >> 5] = (uint8_t)(top >= 0x7F800000u ? 255u : code);
                 }
                 float q[8];
 #pragma unroll
@@ -178,7 +247,7 @@ __global__ __launch_bounds__((threads_of<LANES, kFwdThreads>())) void k_rmsnorm_
                 u32w2 codes = e4m3_encode8(q);
                 if (top >= 0x7F800000u) codes = (u32w2){0x7F7F7F7Fu, 0x7F7F7F7Fu};
                 if (a.codes) {
-                    u32w2 *p = (u32w2 *)((uint8_t *)a.codes + base + c);
+                    u32w2 *p = (u32w2 *)((uint8_t *)a.codes + at);
                     if (NT) __builtin_nontemporal_store(codes, p);
                     else *p = codes;
                 }
@@ -188,7 +257,7 @@ __global__ __launch_bounds__((threads_of<LANES, kFwdThreads>())) void k_rmsnorm_
                     for (int e = 0; e < 8; ++e) h[i][e] = q[e] * scale;
                 }
             }
-            if (a.y) store8<ANY, NT>((uint16_t *)a.y + base + c, n, h[i]);
+            if (a.y) store_span<ANY, NT>((uint16_t *)a.y + start, pos, s, h[i]);
         }
     }
 }
@@ -207,51 +276,67 @@ __device__ __forceinline__ void renew(Raw8<float> &r)
 // stream's type (h, dres, dh).  What bounds the walk is the number of bytes a
 // CU has in flight, so all of a row's loads are issued together, and the row
 // stays as it was loaded (a BF16 element in half a register) and is unpacked
-// twice, before and after the row's sum; gamma waits in LDS.
+// twice, before and after the row's sum.  A lane's share of gamma stays in
+// registers, or in LDS where it has several chunks.  A group's rows are
+// `groups` apart, a multiple of 8 if it has more than one: they all have the
+// same shift, so a lane's columns stay the same ones.
 template <int LANES, int NCH, typename T, bool ANY, bool NT>
 __device__ __forceinline__ void bwd_rows(const fqimpl::NormBwdArgs &a, uint32_t workgroups)
 {
     constexpr int kWgThreads = threads_of<LANES, kBwdThreads>(), kGroups = kWgThreads / LANES;
+    static_assert(NCH == 1 || kGroups == 1, "several chunks a lane only where a row fills the workgroup");
     // dres with the other loads, unless it is wide and a lane's share long
     constexpr bool kEarly = sizeof(T) == 2 || NCH <= 4;
+    constexpr bool kGammaLds = NCH > 1;
     __shared__ float red[2][16];
     __shared__ float sums[kGroups > 1 ? kGroups : 1][kGroups > 1 ? LANES * 8 : 1];
-    __shared__ u32w4 gamma[NCH * 2][LANES];
+    __shared__ u32w4 gamma_lds[kGammaLds ? NCH * 2 : 1][kGammaLds ? LANES : 1];
     const uint32_t l = threadIdx.x % LANES;
     const int group = group_of<LANES>();
     const int64_t groups = (int64_t)workgroups * kGroups;
     const float inv_cols = 1.0f / (float)a.cols;
-    float acc[NCH][8];
+    const auto shift_of = [&](int g) {
+        return ANY ? (int)(((int64_t)blockIdx.x * kGroups + g) * a.cols & 7) : 0;
+    };
+    const int shift = shift_of(group);
+    float gamma[8], acc[NCH][8];
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
-        if (i % kGroups != group) continue;
-        const uint32_t c = (i * LANES + l) * 8;
-        const int n = min(8, (int)a.cols - (int)c);
-        float g[8] = {};
-        if (n > 0) load_gamma<ANY>(a.gamma, a.gamma_f32, c, n, g);
-        gamma[2 * i][l] = (u32w4){as_u(g[0]), as_u(g[1]), as_u(g[2]), as_u(g[3])};
-        gamma[2 * i + 1][l] = (u32w4){as_u(g[4]), as_u(g[5]), as_u(g[6]), as_u(g[7])};
+        const uint32_t pos = (i * LANES + l) * 8;
+        load_gamma<ANY>(a.gamma, a.gamma_f32, pos, shift, span_of<ANY>(pos, shift, a.cols, true), gamma);
+        if (kGammaLds) {             // each lane reads its own
+            gamma_lds[2 * i][l] = (u32w4){as_u(gamma[0]), as_u(gamma[1]), as_u(gamma[2]), as_u(gamma[3])};
+            gamma_lds[2 * i + 1][l] = (u32w4){as_u(gamma[4]), as_u(gamma[5]), as_u(gamma[6]), as_u(gamma[7])};
+        }
     }
-    __syncthreads();
+    const auto gamma_of = [&](int i, float (&g)[8]) {
+        if (kGammaLds) {
+            unpack8(Raw8<float>{gamma_lds[2 * i][l], gamma_lds[2 * i + 1][l]}, g);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = gamma[e];
+        }
+    };
     int slot = 0;
     // every lane of a workgroup makes the same number of turns (row_sum's barrier)
     for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < a.rows; r0 += groups) {
         const int64_t row = r0 + group;
         const bool live = row < a.rows;
-        const int64_t base = (live ? row : 0) * a.cols;
+        const int64_t start = live ? row * a.cols - shift : 0;
+        const int left = (int)min(a.rows * a.cols - start, (int64_t)1 << 30);
         Raw8<uint16_t> dy[NCH] = {};
         Raw8<T> h[NCH] = {}, dres[kEarly ? NCH : 1] = {};
         const float r = live ? a.rstd[row] : 0.0f;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            const uint32_t c = (i * LANES + l) * 8;
-            const int n = live ? min(8, (int)a.cols - (int)c) : 0;
-            if (n <= 0) continue;
-            load_raw8<ANY, NT>((const T *)a.h + base + c, n, h[i]);
-            load_raw8<ANY, NT>((const uint16_t *)a.dy + base + c, n, dy[i]);
-            if (kEarly && a.dres) load_raw8<ANY, NT>((const T *)a.dres + base + c, n, dres[kEarly ? i : 0]);
+            const uint32_t pos = (i * LANES + l) * 8;
+            const Span s = span_of<ANY>(pos, shift, a.cols, live);
+            if (s.hi == 0) continue;
+            load_span<ANY, NT>((const T *)a.h + start, pos, s, left, h[i]);
+            load_span<ANY, NT>((const uint16_t *)a.dy + start, pos, s, left, dy[i]);
+            if (kEarly && a.dres) load_span<ANY, NT>((const T *)a.dres + start, pos, s, left, dres[kEarly ? i : 0]);
         }
         float dot = 0.0f;
 #pragma unroll
@@ -259,7 +344,7 @@ __device__ __forceinline__ void bwd_rows(const fqimpl::NormBwdArgs &a, uint32_t 
             float xh[8], d[8], g[8];
             unpack8(h[i], xh);
             unpack8(dy[i], d);
-            unpack8(Raw8<float>{gamma[2 * i][l], gamma[2 * i + 1][l]}, g);
+            gamma_of(i, g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 xh[e] = xh[e] * r;
@@ -273,49 +358,51 @@ __device__ __forceinline__ void bwd_rows(const fqimpl::NormBwdArgs &a, uint32_t 
         }
         dot = row_sum<LANES>(dot, red, slot) * inv_cols;
         slot ^= 1;
-        asm volatile("" ::: "memory");           // gamma is read again
+        if (kGammaLds) asm volatile("" ::: "memory");    // gamma is read again
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            const uint32_t c = (i * LANES + l) * 8;
-            const int n = live ? min(8, (int)a.cols - (int)c) : 0;
-            if (n <= 0) continue;
+            const uint32_t pos = (i * LANES + l) * 8;
+            const Span s = span_of<ANY>(pos, shift, a.cols, live);
+            if (s.hi == 0) continue;
             float xh[8], d[8], g[8], o[8];
-            if (!kEarly && a.dres) load_raw8<ANY, NT>((const T *)a.dres + base + c, n, dres[0]);
+            if (!kEarly && a.dres) load_span<ANY, NT>((const T *)a.dres + start, pos, s, left, dres[0]);
             unpack8(h[i], xh);
             unpack8(dy[i], d);
-            unpack8(Raw8<float>{gamma[2 * i][l], gamma[2 * i + 1][l]}, g);
+            gamma_of(i, g);
             unpack8(dres[kEarly ? i : 0], o);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 o[e] = __builtin_fmaf(r, __builtin_fmaf(-(xh[e] * r), dot, d[e] * g[e]), o[e]);
-            store8<ANY, NT>((T *)a.dh + base + c, n, o);
-            if (a.dx) store8<ANY, NT>((uint16_t *)a.dx + base + c, n, o);
+            store_span<ANY, NT>((T *)a.dh + start, pos, s, o);
+            if (a.dx) store_span<ANY, NT>((uint16_t *)a.dx + start, pos, s, o);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (!a.partials) return;
-    // the workgroup's column sums, LANES * 8 columns at a time
+    // the workgroup's column sums; its groups may have different shifts
+    float *out = a.partials + (int64_t)blockIdx.x * a.cols;
+    if (kGroups > 1) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sums[group][l * 8 + e] = acc[0][e];
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.cols; c += kWgThreads) {
+            float v = sums[0][c + shift_of(0)];
+#pragma unroll 8
+            for (int g = 1; g < kGroups; ++g) v += sums[g][c + shift_of(g)];
+            out[c] = v;
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-        if (i * LANES * 8 >= a.cols) break;
-        if (kGroups > 1) {
-            __syncthreads();
+        const uint32_t pos = (i * LANES + l) * 8;
+        const Span s = span_of<ANY>(pos, shift, a.cols, true);
+        float *at = out + ((int)pos - shift);
+        if (s.lo == 0 && s.hi == 8) store8<ANY>(at, 8, acc[i]);
+        else
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sums[group][l * 8 + e] = acc[i][e];
-            __syncthreads();
-            for (int k = threadIdx.x; k < LANES * 8; k += kWgThreads) {
-                const int c = i * LANES * 8 + k;
-                if (c >= a.cols) break;
-                float v = sums[0][k];
-#pragma unroll 8
-                for (int g = 1; g < kGroups; ++g) v += sums[g][k];
-                a.partials[(int64_t)blockIdx.x * a.cols + c] = v;
-            }
-        } else {
-            const uint32_t c = (i * LANES + l) * 8;
-        const int n = min(8, (int)a.cols - (int)c);
-            if (n > 0) store8<ANY>(a.partials + (int64_t)blockIdx.x * a.cols + c, n, acc[i]);
-        }
+            for (int e = 0; e < 8; ++e)
+                if (inside(e, s)) at[e] = acc[i][e];
     }
 }
 
@@ -409,20 +496,26 @@ __global__ __launch_bounds__(kSumThreads) void k_column_sum(const float *__restr
 }
 
 // ---- launch -------------------------------------------------------------------
-// Lanes of a row and chunks per lane from the width alone.
+// Lanes of a row and chunks per lane from the width alone; rows that start at
+// any element take up to 7 more than their own.
+int64_t width_of(int64_t cols) { return cols % 8 ? cols + 7 : cols; }
+
 template <template <int, int> class F, typename A>
 hipError_t by_width(const A &a, hipStream_t st)
 {
-    if (a.cols <= 64) return F<8, 1>::go(a, st);
-    if (a.cols <= 128) return F<16, 1>::go(a, st);
-    if (a.cols <= 256) return F<32, 1>::go(a, st);
-    if (a.cols <= 512) return F<64, 1>::go(a, st);
-    if (a.cols <= 1024) return F<128, 1>::go(a, st);
-    if (a.cols <= 2048) return F<256, 1>::go(a, st);
-    if (a.cols <= 4096) return F<512, 1>::go(a, st);
-    if (a.cols <= 8192) return F<1024, 1>::go(a, st);
-    if (a.cols <= 16384) return F<1024, 2>::go(a, st);
-    return F<F<1024, 1>::kLanesMost, 4096 / F<1024, 1>::kLanesMost>::go(a, st);
+    const int64_t width = width_of(a.cols);
+    if (width <= 64) return F<8, 1>::go(a, st);
+    if (width <= 128) return F<16, 1>::go(a, st);
+    if (width <= 256) return F<32, 1>::go(a, st);
+    if (width <= 512) return F<64, 1>::go(a, st);
+    if (width <= 1024) return F<128, 1>::go(a, st);
+    if (width <= 2048) return F<256, 1>::go(a, st);
+    if (width <= 4096) return F<512, 1>::go(a, st);
+    if (width <= 8192) return F<1024, 1>::go(a, st);
+    if (width <= 16384) return F<1024, 2>::go(a, st);
+    constexpr int kLanes = F<1024, 1>::kLanesMost;
+    if (width <= 32768) return F<kLanes, 4096 / kLanes>::go(a, st);
+    return F<kLanes, 4096 / kLanes + 1>::go(a, st);
 }
 
 // A grid holds fewer than 2^32 lanes; the kernels walk over what is left.
@@ -448,16 +541,19 @@ struct Fwd {
     template <int STREAM, int F8>
     static hipError_t by_size(const fqimpl::NormFwdArgs &a, hipStream_t st)
     {
-        return a.rows * a.cols < kStreamElems ? launch<STREAM, F8, false, false>(a, st)
-                                              : launch<STREAM, F8, false, true>(a, st);
+        const bool nt = a.rows * a.cols >= kStreamElems;
+        if constexpr (F8 == fqimpl::F8_NONE)
+            if (a.cols % 8)
+                return nt ? launch<STREAM, F8, true, true>(a, st) : launch<STREAM, F8, true, false>(a, st);
+        if constexpr (LANES * NCH > 4096) return hipErrorInvalidValue;     // wider than any row
+        else return nt ? launch<STREAM, F8, false, true>(a, st) : launch<STREAM, F8, false, false>(a, st);
     }
     template <int STREAM>
     static hipError_t by_output(const fqimpl::NormFwdArgs &a, hipStream_t st)
     {
         if (a.f8 == fqimpl::F8_MX) return by_size<STREAM, fqimpl::F8_MX>(a, st);
         if (a.f8 == fqimpl::F8_ROW) return by_size<STREAM, fqimpl::F8_ROW>(a, st);
-        return a.cols % 8 ? launch<STREAM, fqimpl::F8_NONE, true, false>(a, st)
-                          : by_size<STREAM, fqimpl::F8_NONE>(a, st);
+        return by_size<STREAM, fqimpl::F8_NONE>(a, st);
     }
     static hipError_t go(const fqimpl::NormFwdArgs &a, hipStream_t st)
     {
@@ -483,16 +579,21 @@ struct Bwd {
     template <typename T>
     static hipError_t launch(const fqimpl::NormBwdArgs &a, hipStream_t st)
     {
-        const dim3 grid((uint32_t)a.groups), block(threads_of<LANES, kBwdThreads>());
-        if (a.few) {
-            const dim3 all((uint32_t)(a.groups + (a.cols + 63) / 64));
-            if (a.cols % 8) k_rmsnorm_bwd_few<LANES, NCH, T, true><<<all, block, 0, st>>>(a);
-            else k_rmsnorm_bwd_few<LANES, NCH, T, false><<<all, block, 0, st>>>(a);
-            return hipGetLastError();
-        }
-        if (a.cols % 8) k_rmsnorm_bwd<LANES, NCH, T, true, false><<<grid, block, 0, st>>>(a);
-        else if (a.rows * a.cols < kStreamElems) k_rmsnorm_bwd<LANES, NCH, T, false, false><<<grid, block, 0, st>>>(a);
-        else k_rmsnorm_bwd<LANES, NCH, T, false, true><<<grid, block, 0, st>>>(a);
+        if (a.cols % 8) return by_size<T, true>(a, st);
+        if constexpr (LANES * NCH > 4096) return hipErrorInvalidValue;     // wider than any row
+        else return by_size<T, false>(a, st);
+    }
+    template <typename T, bool ANY>
+    static hipError_t by_size(const fqimpl::NormBwdArgs &a, hipStream_t st)
+    {
+        const dim3 block(threads_of<LANES, kBwdThreads>());
+        const uint32_t grid = (uint32_t)a.groups;
+        if (a.few)
+            k_rmsnorm_bwd_few<LANES, NCH, T, ANY><<<dim3(grid + (uint32_t)((a.cols + 63) / 64)), block, 0, st>>>(a);
+        else if (a.rows * a.cols >= kStreamElems)
+            k_rmsnorm_bwd<LANES, NCH, T, ANY, true><<<dim3(grid), block, 0, st>>>(a);
+        else
+            k_rmsnorm_bwd<LANES, NCH, T, ANY, false><<<dim3(grid), block, 0, st>>>(a);
         return hipGetLastError();
     }
     static hipError_t go(const fqimpl::NormBwdArgs &a, hipStream_t st)
@@ -514,7 +615,7 @@ hipError_t launch_rmsnorm_fwd(const NormFwdArgs &a, hipStream_t stream)
 static int64_t rows_workgroups(int64_t rows, int64_t cols)
 {
     int64_t lanes = 8;
-    while (lanes < kBwdThreads && lanes * 8 < cols) lanes *= 2;
+    while (lanes < kBwdThreads && lanes * 8 < width_of(cols)) lanes *= 2;
     const int64_t per_wg = kBwdThreads / lanes;
     return (rows + per_wg - 1) / per_wg;
 }
@@ -524,7 +625,7 @@ static int64_t rows_workgroups(int64_t rows, int64_t cols)
 // registers), no more than there are rows for.
 int64_t rmsnorm_bwd_groups(int64_t rows, int64_t cols)
 {
-    const int64_t wgs = rows_workgroups(rows, cols), most = cols <= kBwdThreads * 8 ? 512 : 256;
+    const int64_t wgs = rows_workgroups(rows, cols), most = width_of(cols) <= kBwdThreads * 8 ? 512 : 256;
     return wgs < most ? wgs : most;
 }
 

@@ -88,6 +88,11 @@ __device__ __forceinline__ void unpack8(const Raw8<float> &r, float (&v)[8])
         v[4 + i] = as_f(r.b[i]);
     }
 }
+__device__ __forceinline__ float load1(const uint16_t *p) { return as_f((uint32_t)*p << 16); }
+__device__ __forceinline__ float load1(const float *p) { return *p; }
+__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = (uint16_t)bf16_pair_rne(v, v); }
+__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
+
 template <bool ANY, bool NT = false, typename T>
 __device__ __forceinline__ void load8(const T *__restrict__ p, int n, float (&v)[8])
 {

@@ -57,17 +57,20 @@ __device__ __forceinline__ float state_scale(uint32_t top, float per_largest)
 }
 
 // Elements at .. at + n - 1 of an array (n <= 4, or 8 codes); missing ones
-// read as 0 and are not written.
+// read as 0 and are not written.  A tail's loads repeat its last element rather
+// than branch, so that they are in flight together.
 template <bool NT>
 __device__ __forceinline__ void get4(const float *p, int64_t at, int n, float (&v)[4])
 {
     u32w4 r = {0, 0, 0, 0};
     if (n == 4) {
         r = load16<NT>((const u32w4 *)(p + at));
-    } else {
+    } else if (n) {
+        float e[3];
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (i < n) r[i] = as_u(p[at + i]);
+        for (int i = 0; i < 3; ++i) e[i] = p[at + min(i, n - 1)];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) r[i] = i < n ? as_u(e[i]) : 0u;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = as_f(r[i]);
@@ -78,10 +81,12 @@ __device__ __forceinline__ void get4(const uint16_t *p, int64_t at, int n, float
     u32w2 r = {0, 0};
     if (n == 4) {
         r = NT ? __builtin_nontemporal_load((const u32w2 *)(p + at)) : *(const u32w2 *)(p + at);
-    } else {
+    } else if (n) {
+        uint16_t e[3];
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (i < n) r[i / 2] |= (uint32_t)p[at + i] << (16 * (i % 2));
+        for (int i = 0; i < 3; ++i) e[i] = p[at + min(i, n - 1)];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) r[i / 2] |= i < n ? (uint32_t)e[i] << (16 * (i % 2)) : 0u;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = as_f(i % 2 ? hi_bits(r[i / 2]) : lo_bits(r[i / 2]));
@@ -115,9 +120,12 @@ __device__ __forceinline__ u32w2 get_codes(const uint8_t *p, int n)
 {
     if (n == 8) return NT ? __builtin_nontemporal_load((const u32w2 *)p) : *(const u32w2 *)p;
     u32w2 c = {0, 0};
+    if (n == 0) return c;
+    uint8_t e[7];
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (i < n) c[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
+    for (int i = 0; i < 7; ++i) e[i] = p[min(i, n - 1)];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) c[i / 4] |= i < n ? (uint32_t)e[i] << (8 * (i % 4)) : 0u;
     return c;
 }
 template <bool NT>

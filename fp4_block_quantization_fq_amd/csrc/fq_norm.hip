@@ -136,7 +136,13 @@ __device__ __forceinline__ void load_columns(const T *__restrict__ gamma, uint32
     const T *q = gamma + ((int)pos - shift);
     if (s.lo == 0 && s.hi == 8) return load8<ANY>(q, 8, g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = inside(e, s) ? load1(q + e) : 0.0f;
+    for (int e = 0; e < 8; ++e) g[e] = 0.0f;
+    if (!ANY || s.hi == 0) return;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = load1(q + min(max(e, s.lo), s.hi - 1));   // in flight together
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = inside(e, s) ? v[e] : 0.0f;
 }
 template <bool ANY>
 __device__ __forceinline__ void load_gamma(const void *gamma, int f32, uint32_t pos, int shift,
@@ -419,8 +425,9 @@ __device__ __forceinline__ void column_sums(const fqimpl::NormBwdArgs &a, int64_
     constexpr int kWaves = THREADS / 64;
     __shared__ float sums[kWaves][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = c0 + (threadIdx.x % 8) * 8;
-    const int n = (int)max((int64_t)0, min((int64_t)8, a.cols - c));
+    // the last lane's eight columns end with the row; some are its neighbour's too
+    const int64_t mine = c0 + (threadIdx.x % 8) * 8, c = max((int64_t)0, min(mine, a.cols - 8));
+    const int n = mine < a.cols ? (int)min((int64_t)8, a.cols) : 0;
     constexpr int kBatch = 4, kStep = THREADS / 8;     // rows in flight together
     float acc[8] = {};
     for (int64_t row0 = threadIdx.x / 8; n > 0 && row0 < a.rows; row0 += kBatch * kStep) {
@@ -453,7 +460,8 @@ __device__ __forceinline__ void column_sums(const fqimpl::NormBwdArgs &a, int64_
     }
     if (lane < 8)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sums[wave][lane * 8 + e] = acc[e];
+        for (int e = 0; e < 8; ++e)
+            if (c + e >= mine && e < n) sums[wave][c + e - c0] = acc[e];
     __syncthreads();
     if (threadIdx.x >= 64 || c0 + threadIdx.x >= a.cols) return;
     float v = sums[0][threadIdx.x];

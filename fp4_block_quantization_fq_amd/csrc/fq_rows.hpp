@@ -50,9 +50,12 @@ __device__ __forceinline__ void load_raw8(const uint16_t *__restrict__ p, int n,
         r.w = *reinterpret_cast<const u32w4_any *>(p);
     } else {
         r.w = (u32w4){0, 0, 0, 0};
+        if (n <= 0) return;
+        uint16_t v[7];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) r.w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+        for (int i = 0; i < 7; ++i) v[i] = p[min(i, n - 1)];     // in flight together
+#pragma unroll
+        for (int i = 0; i < 7; ++i) r.w[i / 2] |= i < n ? (uint32_t)v[i] << (16 * (i & 1)) : 0u;
     }
 }
 template <bool ANY, bool NT = false>
@@ -65,10 +68,15 @@ __device__ __forceinline__ void load_raw8(const float *__restrict__ p, int n, Ra
         r.a = reinterpret_cast<const u32w4_any4 *>(p)[0];
         r.b = reinterpret_cast<const u32w4_any4 *>(p)[1];
     } else {
+        r.a = r.b = (u32w4){0, 0, 0, 0};
+        if (n <= 0) return;
+        float v[7];
+#pragma unroll
+        for (int i = 0; i < 7; ++i) v[i] = p[min(i, n - 1)];     // in flight together
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            r.a[i] = i < n ? as_u(p[i]) : 0u;
-            r.b[i] = i + 4 < n ? as_u(p[i + 4]) : 0u;
+            r.a[i] = i < n ? as_u(v[i]) : 0u;
+            if (i < 3) r.b[i] = i + 4 < n ? as_u(v[i + 4]) : 0u;
         }
     }
 }

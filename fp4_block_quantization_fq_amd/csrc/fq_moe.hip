@@ -191,21 +191,22 @@ constexpr int kThreads = 256;               // of a workgroup of several tokens
 constexpr int kMostThreads = 512;
 constexpr int kPadRows = 16;
 
-// One token's assignments j0 .. j0 + 3: rows (negative: none) and weights.
+// Four assignments from `first` on, those before `end`: rows (negative: none)
+// and weights.
 struct Four {
     int64_t p[4];
     float w[4];
 };
-template <bool WAVE>
-__device__ __forceinline__ Four four_of(const fqimpl::MoeRowsArgs &a, int64_t t, int j0)
+template <int LANES>
+__device__ __forceinline__ Four four_of(const fqimpl::MoeRowsArgs &a, int64_t first, int64_t end)
 {
     Four f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int64_t at = t * a.k + min(j0 + i, (int)a.k - 1);
+        const int64_t at = min(first + i, end - 1);
         int32_t p = a.pos[at];
-        if (WAVE) p = __builtin_amdgcn_readfirstlane(p);
-        f.p[i] = j0 + i < a.k && (uint32_t)p < (uint64_t)a.rows ? (int64_t)p : -1;
+        if (LANES == 0 || LANES == 64) p = __builtin_amdgcn_readfirstlane(p);    // a wave has one token
+        f.p[i] = first + i < end && (uint32_t)p < (uint64_t)a.rows ? (int64_t)p : -1;
         f.w[i] = a.weights ? a.weights[at] : 1.0f;
     }
     return f;
@@ -266,8 +267,8 @@ __device__ __forceinline__ void dispatch_unit(const fqimpl::MoeRowsArgs &a, uint
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = bf16_pair_rne(f[2 * i] * s, f[2 * i + 1] * s);
         }
-        for (int j0 = 0; j0 < a.k; j0 += 4) {
-            const Four f = four_of<LANES == 0 || LANES == 64>(a, t, j0);
+        for (int64_t j = t * a.k; j < (t + 1) * a.k; j += 4) {
+            const Four f = four_of<LANES>(a, j, (t + 1) * a.k);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (f.p[i] >= 0) store16<NT>((u32w4 *)(y + f.p[i] * a.H + c * 8), v);
@@ -288,17 +289,21 @@ __global__ __launch_bounds__(LANES ? kThreads : kMostThreads) void k_moe_dispatc
     }
 }
 
-template <int LANES, bool NT>
+// out[t] = sum_j w[t, j] * y[pos[t, j]].  K 0: any k, a token at a time.  K 1 or
+// 2: that k, and a group takes the tokens of four assignments together.
+template <int LANES, int K, bool NT>
 __device__ __forceinline__ void combine_unit(const fqimpl::MoeRowsArgs &a, uint32_t b,
                                              uint32_t chunks)
 {
+    constexpr int kTokens = K ? 4 / K : 1, kEach = K ? K : 4;      // of four assignments
     const uint16_t *__restrict__ y = (const uint16_t *)a.y;
-    const int64_t t = token_of<LANES>(b);
+    const int64_t t = token_of<LANES>(b) * kTokens;
     if (t >= a.T) return;
     for (uint32_t c = chunk_of<LANES>(); c < chunks; c += LANES ? LANES : blockDim.x) {
-        float acc[8] = {};
-        for (int j0 = 0; j0 < a.k; j0 += 4) {
-            const Four f = four_of<LANES == 0 || LANES == 64>(a, t, j0);
+        float acc[kTokens][8] = {};
+        const int64_t end = K ? a.T * K : (t + 1) * a.k;
+        for (int64_t j = t * a.k; j < end; j += 4) {
+            const Four f = four_of<LANES>(a, j, end);
             Raw8<uint16_t> r[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -309,46 +314,54 @@ __device__ __forceinline__ void combine_unit(const fqimpl::MoeRowsArgs &a, uint3
                 float v[8];
                 unpack8(r[i], v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(f.w[i], v[e], acc[e]);
+                for (int e = 0; e < 8; ++e)
+                    acc[i / kEach][e] = __builtin_fmaf(f.w[i], v[e], acc[i / kEach][e]);
             }
+            if (K) break;
         }
-        store8<false, NT>((uint16_t *)a.out + t * a.H + c * 8, 8, acc);
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i)
+            if (i == 0 || t + i < a.T)
+                store8<false, NT>((uint16_t *)a.out + (t + i) * a.H + c * 8, 8, acc[i]);
     }
 }
 
-// out[t] = sum_j w[t, j] * y[pos[t, j]]
-template <int LANES, bool NT>
+template <int LANES, int K, bool NT>
 __global__ __launch_bounds__(LANES ? kThreads : kMostThreads) void k_moe_combine(
     fqimpl::MoeRowsArgs a, uint32_t work)
 {
     const uint32_t chunks = (uint32_t)(a.H / 8);
-    for (uint32_t b = blockIdx.x; b < work; b += gridDim.x) combine_unit<LANES, NT>(a, b, chunks);
+    for (uint32_t b = blockIdx.x; b < work; b += gridDim.x) combine_unit<LANES, K, NT>(a, b, chunks);
 }
 
-template <int LANES, bool NT>
+template <int LANES, int K, bool NT>
 __device__ __forceinline__ void combine_bwd_unit(const fqimpl::MoeRowsArgs &a, uint32_t b,
                                                  uint32_t chunks, uint16_t *__restrict__ dy,
                                                  float (*part)[kMostThreads / 64])
 {
+    constexpr int kTokens = K ? 4 / K : 1, kEach = K ? K : 4;
     const uint16_t *__restrict__ y = (const uint16_t *)a.y;
-    const int64_t t = token_of<LANES>(b);
+    const int64_t t = token_of<LANES>(b) * kTokens;
     if (t >= a.T) return;                       // not with LANES 0, which has barriers
     const uint32_t c0 = chunk_of<LANES>();
-    for (int j0 = 0; j0 < a.k; j0 += 4) {
-        const Four f = four_of<LANES == 0 || LANES == 64>(a, t, j0);
+    const int64_t end = K ? a.T * K : (t + 1) * a.k;
+    for (int64_t j = t * a.k; j < end; j += 4) {
+        const Four f = four_of<LANES>(a, j, end);
         float dot[4] = {};
         for (uint32_t c = c0; c < chunks; c += LANES ? LANES : blockDim.x) {
-            float d[8];
-            Raw8<uint16_t> r[4];
+            Raw8<uint16_t> r[4], dr[kTokens];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (f.p[i] >= 0) load_raw8<false, NT>(y + f.p[i] * a.H + c * 8, 8, r[i]);
-            load8<false>((const uint16_t *)a.dout + t * a.H + c * 8, 8, d);
+#pragma unroll
+            for (int i = 0; i < kTokens; ++i)
+                load_raw8<false>((const uint16_t *)a.dout + min(t + i, a.T - 1) * a.H + c * 8, 8, dr[i]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (f.p[i] < 0) continue;
-                float v[8];
+                float v[8], d[8];
                 unpack8(r[i], v);
+                unpack8(dr[i / kEach], d);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     dot[i] = __builtin_fmaf(d[e], v[e], dot[i]);
@@ -363,25 +376,26 @@ __device__ __forceinline__ void combine_bwd_unit(const fqimpl::MoeRowsArgs &a, u
             if (c0 == 0)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (j0 + i < a.k) a.dweights[t * a.k + j0 + i] = dot[i];
-            continue;
-        }
-        if ((threadIdx.x & 63) == 0)
+                    if (j + i < end) a.dweights[j + i] = dot[i];
+        } else {
+            if ((threadIdx.x & 63) == 0)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) part[i][threadIdx.x >> 6] = dot[i];
-        __syncthreads();
-        if (threadIdx.x < 4 && j0 + (int)threadIdx.x < a.k) {
-            float v = part[threadIdx.x][0];
-            for (uint32_t w = 1; w < blockDim.x / 64; ++w) v += part[threadIdx.x][w];
-            a.dweights[t * a.k + j0 + threadIdx.x] = v;
+                for (int i = 0; i < 4; ++i) part[i][threadIdx.x >> 6] = dot[i];
+            __syncthreads();
+            if (threadIdx.x < 4 && j + threadIdx.x < end) {
+                float v = part[threadIdx.x][0];
+                for (uint32_t w = 1; w < blockDim.x / 64; ++w) v += part[threadIdx.x][w];
+                a.dweights[j + threadIdx.x] = v;
+            }
+            __syncthreads();
         }
-        __syncthreads();
+        if (K) break;
     }
 }
 
 // dy[pos[t, j]] = w[t, j] * dout[t], dw[t, j] = <dout[t], y[pos[t, j]]>; the
 // units from `work` on clear the padding.
-template <int LANES, bool NT>
+template <int LANES, int K, bool NT>
 __global__ __launch_bounds__(LANES ? kThreads : kMostThreads) void k_moe_combine_bwd(
     fqimpl::MoeRowsArgs a, uint32_t work, uint32_t units)
 {
@@ -389,7 +403,7 @@ __global__ __launch_bounds__(LANES ? kThreads : kMostThreads) void k_moe_combine
     uint16_t *dy = (uint16_t *)a.rows_out;
     const uint32_t chunks = (uint32_t)(a.H / 8);
     for (uint32_t b = blockIdx.x; b < units; b += gridDim.x) {
-        if (b < work) combine_bwd_unit<LANES, NT>(a, b, chunks, dy, part);
+        if (b < work) combine_bwd_unit<LANES, K, NT>(a, b, chunks, dy, part);
         else clear_padding<NT>(a, (int64_t)b - work, dy);
     }
 }
@@ -398,22 +412,36 @@ __global__ __launch_bounds__(LANES ? kThreads : kMostThreads) void k_moe_combine
 // A grid holds fewer than 2^32 lanes; the kernels walk over what is left.
 constexpr uint32_t kMaxGrid = 1u << 22;
 
-// Lanes of a token from the width alone: launch(lanes, units of work, threads).
+// Lanes of a group from the width alone: launch(lanes, units of work, threads)
+// for `groups` groups.
 template <typename F>
-hipError_t by_width(const fqimpl::MoeRowsArgs &a, F launch)
+hipError_t by_width(const fqimpl::MoeRowsArgs &a, int64_t groups, F launch)
 {
     const int64_t chunks = a.H / 8;
     const auto shared = [&](auto lanes) {
         const int64_t per = kThreads / decltype(lanes)::value;
-        return launch(lanes, (uint32_t)((a.T + per - 1) / per), (uint32_t)kThreads);
+        return launch(lanes, (uint32_t)((groups + per - 1) / per), (uint32_t)kThreads);
     };
     if (chunks <= 8) return shared(std::integral_constant<int, 8>());
     if (chunks <= 16) return shared(std::integral_constant<int, 16>());
     if (chunks <= 32) return shared(std::integral_constant<int, 32>());
     if (chunks <= 64) return shared(std::integral_constant<int, 64>());
     const int64_t threads = (chunks + 63) / 64 * 64;
-    return launch(std::integral_constant<int, 0>(), (uint32_t)a.T,
+    return launch(std::integral_constant<int, 0>(), (uint32_t)groups,
                   (uint32_t)(threads < kMostThreads ? threads : kMostThreads));
+}
+
+// Four assignments a group, of several tokens where k is 1 or 2 and there are
+// many tokens: launch(k or 0, groups).  Rows of 2880: 16384 tokens with k = 1
+// 34.6 us, one at a time 64.3, with k = 2 50.3 and 67.1; 2048 tokens 6.5 and
+// 8.2; of fewer there are too few groups (1024 with k = 2 5.3 and 5.5).
+constexpr int64_t kManyTokens = 2048;
+template <typename F>
+hipError_t by_k(const fqimpl::MoeRowsArgs &a, F launch)
+{
+    if (a.k == 1 && a.T >= kManyTokens) return launch(std::integral_constant<int, 1>(), (a.T + 3) / 4);
+    if (a.k == 2 && a.T >= kManyTokens) return launch(std::integral_constant<int, 2>(), (a.T + 1) / 2);
+    return launch(std::integral_constant<int, 0>(), a.T);
 }
 
 // Streaming accesses from this many elements of sorted rows on, where they
@@ -458,7 +486,7 @@ template <int F8>
 static hipError_t dispatch(const MoeRowsArgs &a, hipStream_t stream)
 {
     const uint32_t pads = (uint32_t)((a.rows + kPadRows - 1) / kPadRows);
-    return by_width(a, [&](auto lanes, uint32_t work, uint32_t threads) {
+    return by_width(a, a.T, [&](auto lanes, uint32_t work, uint32_t threads) {
         constexpr int kLanes = decltype(lanes)::value;
         const uint32_t units = work + pads;
         const dim3 grid(units < kMaxGrid ? units : kMaxGrid), block(threads);
@@ -479,29 +507,33 @@ hipError_t launch_moe_dispatch(int f8, const MoeRowsArgs &a, hipStream_t stream)
 
 hipError_t launch_moe_combine(const MoeRowsArgs &a, hipStream_t stream)
 {
-    return by_width(a, [&](auto lanes, uint32_t work, uint32_t threads) {
-        constexpr int kLanes = decltype(lanes)::value;
-        const dim3 grid(work < kMaxGrid ? work : kMaxGrid), block(threads);
-        if (a.T * a.k * a.H < kStreamForward)
-            k_moe_combine<kLanes, false><<<grid, block, 0, stream>>>(a, work);
-        else
-            k_moe_combine<kLanes, true><<<grid, block, 0, stream>>>(a, work);
-        return hipGetLastError();
+    return by_k(a, [&](auto k, int64_t groups) {
+        return by_width(a, groups, [&](auto lanes, uint32_t work, uint32_t threads) {
+            constexpr int kLanes = decltype(lanes)::value, K = decltype(k)::value;
+            const dim3 grid(work < kMaxGrid ? work : kMaxGrid), block(threads);
+            if (a.T * a.k * a.H < kStreamForward)
+                k_moe_combine<kLanes, K, false><<<grid, block, 0, stream>>>(a, work);
+            else
+                k_moe_combine<kLanes, K, true><<<grid, block, 0, stream>>>(a, work);
+            return hipGetLastError();
+        });
     });
 }
 
 hipError_t launch_moe_combine_bwd(const MoeRowsArgs &a, hipStream_t stream)
 {
     const uint32_t pads = (uint32_t)((a.rows + kPadRows - 1) / kPadRows);
-    return by_width(a, [&](auto lanes, uint32_t work, uint32_t threads) {
-        constexpr int kLanes = decltype(lanes)::value;
-        const uint32_t units = work + pads;
-        const dim3 grid(units < kMaxGrid ? units : kMaxGrid), block(threads);
-        if (a.T * a.k * a.H < kStreamBwd)
-            k_moe_combine_bwd<kLanes, false><<<grid, block, 0, stream>>>(a, work, units);
-        else
-            k_moe_combine_bwd<kLanes, true><<<grid, block, 0, stream>>>(a, work, units);
-        return hipGetLastError();
+    return by_k(a, [&](auto k, int64_t groups) {
+        return by_width(a, groups, [&](auto lanes, uint32_t work, uint32_t threads) {
+            constexpr int kLanes = decltype(lanes)::value, K = decltype(k)::value;
+            const uint32_t units = work + pads;
+            const dim3 grid(units < kMaxGrid ? units : kMaxGrid), block(threads);
+            if (a.T * a.k * a.H < kStreamBwd)
+                k_moe_combine_bwd<kLanes, K, false><<<grid, block, 0, stream>>>(a, work, units);
+            else
+                k_moe_combine_bwd<kLanes, K, true><<<grid, block, 0, stream>>>(a, work, units);
+            return hipGetLastError();
+        });
     });
 }
 

@@ -22,7 +22,8 @@ typedef u32w4 u32w4_any4 __attribute__((aligned(4)));
 // no multiple of 8); missing ones read as 0 and are not written.  ANY: the
 // row may start at any element; gfx950 serves the 16-byte access at element
 // alignment, so only the last chunk goes element by element.  NT: streaming
-// accesses, for calls whose data is larger than the caches.
+// accesses, for calls whose data is larger than the caches; not for FP32, whose
+// two accesses use half of each line and have to meet in the cache.
 template <bool NT, typename V>
 __device__ __forceinline__ u32w4 load16(const V *p)
 {
@@ -62,8 +63,8 @@ template <bool ANY, bool NT = false>
 __device__ __forceinline__ void load_raw8(const float *__restrict__ p, int n, Raw8<float> &r)
 {
     if (!ANY) {
-        r.a = load16<NT>(reinterpret_cast<const u32w4 *>(p));
-        r.b = load16<NT>(reinterpret_cast<const u32w4 *>(p) + 1);
+        r.a = reinterpret_cast<const u32w4 *>(p)[0];
+        r.b = reinterpret_cast<const u32w4 *>(p)[1];
     } else if (n >= 8) {
         r.a = reinterpret_cast<const u32w4_any4 *>(p)[0];
         r.b = reinterpret_cast<const u32w4_any4 *>(p)[1];
@@ -131,8 +132,8 @@ __device__ __forceinline__ void store8(float *__restrict__ p, int n, const float
     const u32w4 a = {as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3])};
     const u32w4 b = {as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7])};
     if (!ANY) {
-        store16<NT>(reinterpret_cast<u32w4 *>(p), a);
-        store16<NT>(reinterpret_cast<u32w4 *>(p) + 1, b);
+        reinterpret_cast<u32w4 *>(p)[0] = a;
+        reinterpret_cast<u32w4 *>(p)[1] = b;
     } else if (n >= 8) {
         reinterpret_cast<u32w4_any4 *>(p)[0] = a;
         reinterpret_cast<u32w4_any4 *>(p)[1] = b;

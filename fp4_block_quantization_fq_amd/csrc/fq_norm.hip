@@ -534,6 +534,14 @@ constexpr int64_t kMaxGrid = int64_t(1) << 20;
 // 31.2 and 32.3, 21.6 and 18.1).
 constexpr int64_t kStreamElems = int64_t(1) << 24;
 
+// Two chunks a lane instead of one: without a residual, where a lane has only 16
+// bytes to load (16384x2880 in BF16 37.0 us instead of 40.5, with 8-bit rows 47
+// instead of 58; 8471x6304 with MX blocks 54 instead of 72), and with one up to
+// this many elements, whose workgroups then fit the CUs at once (1777x4096 in
+// BF16 10.1 us instead of 11.4, 3000x4096 18.8 and 19.0, with an FP32 stream 22.1
+// and 20.7).  Not of few rows (16x4096 3.4 us instead of 3.2).
+constexpr int64_t kHalfRows = 512, kHalfElems = int64_t(1) << 23;
+
 template <int LANES, int NCH>
 struct Fwd {
     static constexpr int kLanesMost = 1024;
@@ -563,14 +571,18 @@ struct Fwd {
         if (a.f8 == fqimpl::F8_ROW) return by_size<STREAM, fqimpl::F8_ROW>(a, st);
         return by_size<STREAM, fqimpl::F8_NONE>(a, st);
     }
+    static hipError_t by_stream(const fqimpl::NormFwdArgs &a, hipStream_t st)
+    {
+        if (!a.res) return by_output<0>(a, st);
+        return a.stream_f32 ? by_output<2>(a, st) : by_output<1>(a, st);
+    }
     static hipError_t go(const fqimpl::NormFwdArgs &a, hipStream_t st)
     {
-        // Without a residual a lane has half the bytes in flight: half the lanes,
-        // two chunks each (16384x2880 in BF16 37.0 us instead of 40.5, with 8-bit
-        // rows 47 instead of 58; 8471x6304 with MX blocks 54 instead of 72)
+        // half the lanes, two chunks each, where that keeps enough in flight
         constexpr int kHalf = LANES > 64 ? 2 : 1;
-        if (!a.res) return Fwd<LANES / kHalf, NCH * kHalf>::template by_output<0>(a, st);
-        return a.stream_f32 ? by_output<2>(a, st) : by_output<1>(a, st);
+        if (a.rows >= kHalfRows && (!a.res || a.rows * a.cols < kHalfElems))
+            return Fwd<LANES / kHalf, NCH * kHalf>::by_stream(a, st);
+        return by_stream(a, st);
     }
 };
 

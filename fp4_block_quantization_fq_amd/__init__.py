@@ -301,6 +301,13 @@ def _binding():
     return _binding_module
 
 
+def _matrix(t, name: str):
+    """(rows, cols) of a matrix operand."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return t.shape
+
+
 def _allocating(stream):
     """Outputs and workspaces that a call makes for itself belong to the stream
     it runs on, so their memory is not handed out again while it still works."""
@@ -716,7 +723,7 @@ def fq_rmsnorm_fwd(x, gamma, eps: float, res=None, f8: int = FQ_F8_NONE, h=None,
     if res is not None and h is None or (y is None if f8 == FQ_F8_NONE
                                          else codes is None or scales is None):
         torch = _torch()
-        rows, cols = x.shape
+        rows, cols = _matrix(x, "x")
         with _allocating(stream):
             if res is not None and h is None:
                 h = torch.empty_like(res)
@@ -752,7 +759,7 @@ def fq_rmsnorm_bwd(dy, h, gamma, rstd, dres=None, dh=None, dx=None, dgamma=None,
         dgamma = ws = None
     if dh is None or (need_dgamma and (dgamma is None or ws is None)):
         torch = _torch()
-        rows, cols = dy.shape
+        rows, cols = _matrix(dy, "dy")
         with _allocating(stream):
             if dh is None:
                 dh = torch.empty_like(h)
@@ -796,7 +803,7 @@ def fq_moe_sort(experts_of, experts: int, align: int = 1, out: MoeSorted | None 
     expert's segment padded to a multiple of `align` rows."""
     if out is None or ws is None:
         torch = _torch()
-        tokens, k = experts_of.shape
+        tokens, k = _matrix(experts_of, "experts_of")
         dev = experts_of.device
         with _allocating(stream):
             if out is None:
@@ -819,7 +826,7 @@ def fq_moe_dispatch(x, q: MoeSorted, f8: int = FQ_F8_NONE, scales=None, y=None, 
     x BF16 [tokens, cols], or the codes of 8-bit rows with their scales."""
     if y is None:
         with _allocating(stream):
-            y = _torch().empty((q.src.numel(), x.shape[1]), dtype=_torch().bfloat16,
+            y = _torch().empty((q.src.numel(), _matrix(x, "x")[1]), dtype=_torch().bfloat16,
                                device=x.device)
     st = (_binding_module or _binding()).moe_dispatch(x, f8, scales, q.pos, q.src, y, stream)
     if st:
@@ -832,7 +839,7 @@ def fq_moe_combine(y, q: MoeSorted, weights=None, out=None, stream=None):
     backward of fq_moe_dispatch)."""
     if out is None:
         with _allocating(stream):
-            out = _torch().empty((q.pos.shape[0], y.shape[1]), dtype=_torch().bfloat16,
+            out = _torch().empty((_matrix(q.pos, "pos")[0], _matrix(y, "y")[1]), dtype=_torch().bfloat16,
                                  device=y.device)
     st = (_binding_module or _binding()).moe_combine(y, weights, q.pos, q.src, out, stream)
     if st:
@@ -846,7 +853,7 @@ def fq_moe_combine_bwd(dout, y, q: MoeSorted, weights, dy=None, dweights=None, s
         torch = _torch()
         with _allocating(stream):
             if dy is None:
-                dy = torch.empty((q.src.numel(), dout.shape[1]), dtype=torch.bfloat16,
+                dy = torch.empty((q.src.numel(), _matrix(dout, "dout")[1]), dtype=torch.bfloat16,
                                  device=dout.device)
             if dweights is None:
                 dweights = torch.empty(tuple(q.pos.shape), dtype=torch.float32,

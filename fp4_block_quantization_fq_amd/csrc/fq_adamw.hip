@@ -142,16 +142,21 @@ __device__ __forceinline__ void put_codes(uint8_t *p, int n, u32w2 c)
 }
 
 // The tensor that tile `tile` belongs to: the last one that starts at or before
-// it.  In a plan all lanes look at 64 starts at a time; the arguments' short
-// table is bisected in scalar code.
+// it.  In a plan the wave looks at 64 starts at once, first at those of 64 parts
+// of the list; the arguments' short table is bisected in scalar code.
 __device__ __forceinline__ uint32_t tensor_of(const uint32_t *__restrict__ first, uint32_t count,
                                               uint32_t tile)
 {
+    const uint32_t lane = threadIdx.x & 63, part = (count + 63) / 64;
+    const auto starts = [&](uint32_t at, uint32_t end) {
+        return (uint32_t)__popcll(__ballot(at < end && first[at] <= tile));
+    };
     uint32_t n = 0;
-    for (uint32_t at = threadIdx.x & 63; n < count; at += 64) {
-        const uint64_t m = __ballot(at < count && first[at] <= tile);
-        n += (uint32_t)__popcll(m);
-        if (m != ~0ull) break;
+    if (part > 1) n = (starts(lane * part, count) - 1) * part;
+    for (const uint32_t end = part > 1 ? min(n + part, count) : count; n < end;) {
+        const uint32_t m = starts(n + lane, end);
+        n += m;
+        if (m < 64) break;
     }
     return (uint32_t)__builtin_amdgcn_readfirstlane((int)n) - 1;
 }

@@ -213,19 +213,31 @@ __device__ __forceinline__ Four four_of(const fqimpl::MoeRowsArgs &a, int64_t fi
 }
 
 // +0 into the rows of [block * 16, block * 16 + 16) that hold no assignment.
-template <bool NT>
+template <int LANES, bool NT>
 __device__ __forceinline__ void clear_padding(const fqimpl::MoeRowsArgs &a, int64_t block,
                                               uint16_t *__restrict__ y)
 {
-    const uint32_t chunks = (uint32_t)(a.H / 8), lane = threadIdx.x & 63;
+    const uint32_t chunks = (uint32_t)(a.H / 8);
     const int64_t r0 = block * kPadRows;
+    const u32w4 zero = {0, 0, 0, 0};
+    if (LANES) {                           // a row for each group of lanes
+        constexpr int kLanes = LANES ? LANES : 64;
+        const uint32_t c = threadIdx.x % kLanes;
+        for (int i = threadIdx.x / kLanes; i < kPadRows; i += kThreads / kLanes) {
+            const int64_t r = r0 + i;
+            if (r >= a.rows || (uint64_t)(int64_t)a.src[r] < (uint64_t)(a.T * a.k)) continue;
+            if (c < chunks) store16<NT>((u32w4 *)(y + r * a.H + c * 8), zero);
+        }
+        return;
+    }
+    const uint32_t lane = threadIdx.x & 63;
     bool pad = false;
     if (lane < kPadRows && r0 + lane < a.rows)
         pad = (uint64_t)(int64_t)a.src[r0 + lane] >= (uint64_t)(a.T * a.k);
     for (uint64_t left = __ballot(pad); left; left &= left - 1) {
         uint16_t *row = y + (r0 + __builtin_ctzll(left)) * a.H;
         for (uint32_t c = threadIdx.x; c < chunks; c += blockDim.x)
-            store16<NT>((u32w4 *)(row + c * 8), (u32w4){0, 0, 0, 0});
+            store16<NT>((u32w4 *)(row + c * 8), zero);
     }
 }
 
@@ -285,7 +297,7 @@ __global__ __launch_bounds__(LANES ? kThreads : kMostThreads) void k_moe_dispatc
     const uint32_t chunks = (uint32_t)(a.H / 8);
     for (uint32_t b = blockIdx.x; b < units; b += gridDim.x) {
         if (b < work) dispatch_unit<LANES, F8, NT>(a, b, chunks, y);
-        else clear_padding<NT>(a, (int64_t)b - work, y);
+        else clear_padding<LANES, NT>(a, (int64_t)b - work, y);
     }
 }
 
@@ -404,7 +416,7 @@ __global__ __launch_bounds__(LANES ? kThreads : kMostThreads) void k_moe_combine
     const uint32_t chunks = (uint32_t)(a.H / 8);
     for (uint32_t b = blockIdx.x; b < units; b += gridDim.x) {
         if (b < work) combine_bwd_unit<LANES, K, NT>(a, b, chunks, dy, part);
-        else clear_padding<NT>(a, (int64_t)b - work, dy);
+        else clear_padding<LANES, NT>(a, (int64_t)b - work, dy);
     }
 }
 

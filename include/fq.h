@@ -462,8 +462,8 @@ size_t fq_rmsnorm_bwd_workspace_size(int64_t rows, int64_t cols);
  *   dh = r * (g - xh * mean(g * xh)) + dres,   dgamma = sum over rows of dy * xh.
  * h of stream_type is the forward's h (x in BF16 where it had no residual),
  * rstd the forward's r.  dres (same type, may be NULL) is the gradient that
- * reaches h from elsewhere; dh (same type, may be dres) is the gradient of
- * both x and res; dx, if given, receives it rounded to BF16 (the gradient of x
+ * reaches h from elsewhere; dh (same type, may be dres, h or dy) is the gradient
+ * of both x and res; dx, if given, receives it rounded to BF16 (the gradient of x
  * beside an FP32 stream).  dgamma FP32 [cols] may be NULL, then no workspace
  * is needed.  FP32 sums in a fixed order: equal calls give equal bits.  The
  * rounding to 8 bits is passed straight through. */

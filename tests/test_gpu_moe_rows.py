@@ -82,3 +82,10 @@ def test_more_tokens_than_a_grid_takes():
     dy, dw = fq.fq_moe_combine_bwd(x, y, q, w)
     assert torch.equal(dy, 2 * y)
     assert torch.equal(dw, torch.where(ids >= 0, (x.float() ** 2).sum(1, keepdim=True), torch.zeros_like(w)))
+
+
+@pytest.mark.parametrize("k", [3, 4, 5, 6, 7, 8, 9, 13, 16, 17, 64])
+@pytest.mark.parametrize("T", [1, 37, 513])
+@pytest.mark.parametrize("H", [64, 136, 512, 1056])
+def test_assignments_of_a_token(T, k, H):
+    test_widths(T, k, H)

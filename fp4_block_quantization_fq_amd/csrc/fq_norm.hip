@@ -544,6 +544,18 @@ constexpr int64_t kStreamElems = int64_t(1) << 24;
 // and 20.7).  Not of few rows (16x4096 3.4 us instead of 3.2).
 constexpr int64_t kHalfRows = 512, kHalfElems = int64_t(1) << 23;
 
+// Widths just over a power of two would leave up to half of the lanes without
+// work.  Up to 5 / 8 of the next one a row of a call of many takes five waves
+// (of two chunks) instead of eight (or sixteen) in BF16, and ten in the backward:
+// with a residual 16384x2336 53.3 us instead of 59.7, 9000x5120 63.7 instead of
+// 68.8, 9000x4095, which starts at any element, 61.3 instead of 71.5, without one
+// 37.3 instead of 41.8.  Not with an FP32 stream, whose lanes have as many bytes
+// in flight as two chunks (9000x5120 96 us with ten waves and with sixteen, 102
+// with five), and rows of 2336 without a residual take four waves of two chunks
+// (9000x2337 23.1 us, five waves 25.9).
+template <int LANES, int NCH>
+bool five_eighths(int64_t cols) { return LANES >= 512 && NCH == 1 && width_of(cols) <= 5 * LANES; }
+
 template <int LANES, int NCH>
 struct Fwd {
     static constexpr int kLanesMost = 1024;
@@ -582,8 +594,15 @@ struct Fwd {
     {
         // half the lanes, two chunks each, where that keeps enough in flight
         constexpr int kHalf = LANES > 64 ? 2 : 1;
-        if (a.rows >= kHalfRows && (!a.res || a.rows * a.cols < kHalfElems))
-            return Fwd<LANES / kHalf, NCH * kHalf>::by_stream(a, st);
+        const bool half = a.rows >= kHalfRows && (!a.res || a.rows * a.cols < kHalfElems);
+        if (five_eighths<LANES, NCH>(a.cols) && a.rows >= kHalfRows && !(a.res && a.stream_f32)) {
+            if constexpr (LANES == 512 && NCH == 1)
+                if (!half) return Fwd<320, 1>::template by_output<1>(a, st);
+            if constexpr (LANES == 1024 && NCH == 1)
+                return a.res ? Fwd<320, 2>::template by_output<1>(a, st)
+                             : Fwd<320, 2>::template by_output<0>(a, st);
+        }
+        if (half) return Fwd<LANES / kHalf, NCH * kHalf>::by_stream(a, st);
         return by_stream(a, st);
     }
 };
@@ -620,6 +639,8 @@ struct Bwd {
     }
     static hipError_t go(const fqimpl::NormBwdArgs &a, hipStream_t st)
     {
+        if constexpr (LANES == 1024 && NCH == 1)
+            if (five_eighths<LANES, NCH>(a.cols)) return Bwd<640, 1>::go(a, st);
         return a.stream_f32 ? launch<float>(a, st) : launch<uint16_t>(a, st);
     }
 };
@@ -642,13 +663,26 @@ static int64_t rows_workgroups(int64_t rows, int64_t cols)
     return (rows + per_wg - 1) / per_wg;
 }
 
-// Workgroups that walk over the rows, each leaving a row of column sums: two
-// on each of 256 CUs, one where a row has 1024 lanes (or 512 with many
-// registers), no more than there are rows for.
+// Workgroups that walk over the rows, each leaving a row of column sums, no more
+// than there are rows for: two on each of 256 CUs, one where a row has 640 lanes
+// or more (or 512 with many registers).  In streaming calls two also of 640
+// lanes, except of FP32 rows of whole chunks (9000x5120 BF16 68.8 us, one 77.8,
+// FP32 142 and 133; 9000x4095 64.2 and 83.5, FP32 118 and 131), and three of BF16
+// rows that start at any element and fill more than a wave (12836x2337 55.5 us,
+// two 63.3; 38560x778 50.4 and 54.2; 61224x490 51.7 and 48.0, 1711x2337 16.0 and
+// 15.1, FP32 17355x2881 167 and 161).
+static int64_t bwd_groups(int64_t rows, int64_t cols, bool f32)
+{
+    const int64_t wgs = rows_workgroups(rows, cols), width = width_of(cols);
+    const bool any = cols % 8, large = rows * cols >= kStreamElems;
+    int64_t most = width <= kBwdThreads * 8 ? 512 : 256;
+    if (large && width > 512 && width <= 4096 && any && !f32) most = 768;
+    if (large && width > 4096 && width <= 5120 && (any || !f32)) most = 512;
+    return wgs < most ? wgs : most;
+}
 int64_t rmsnorm_bwd_groups(int64_t rows, int64_t cols)
 {
-    const int64_t wgs = rows_workgroups(rows, cols), most = width_of(cols) <= kBwdThreads * 8 ? 512 : 256;
-    return wgs < most ? wgs : most;
+    return bwd_groups(rows, cols, false);          // of FP32 rows there are no more
 }
 
 static bool few_rows(const NormBwdArgs &a)
@@ -662,7 +696,8 @@ static bool few_rows(const NormBwdArgs &a)
 hipError_t launch_rmsnorm_bwd(NormBwdArgs a, hipStream_t stream)
 {
     a.few = few_rows(a);
-    a.groups = a.few ? rows_workgroups(a.rows, a.cols) : rmsnorm_bwd_groups(a.rows, a.cols);
+    a.groups = a.few ? rows_workgroups(a.rows, a.cols)
+                       : bwd_groups(a.rows, a.cols, a.stream_f32);
     if (!a.dgamma || a.few) a.partials = nullptr;
     const hipError_t e = by_width<Bwd>(a, stream);
     if (e != hipSuccess || !a.partials) return e;

@@ -10,7 +10,7 @@
 // Both passes are bound by memory: one read of every input and one write of
 // every output, a row staying in registers between the statistic and its use.
 //  * LANES lanes share a row (8 for a row of 64 elements, up to a workgroup of
-//    1024), each holding NCH chunks of 8 consecutive elements (16-byte BF16
+//    1024; powers of two, or 5/8 of one), each holding NCH chunks of 8 consecutive elements (16-byte BF16
 //    accesses); chunk i of lane l is i * LANES + l, so neighbouring lanes read
 //    neighbouring chunks.  One chunk a lane up to 8192 columns: many short
 //    waves keep the loads of some rows in flight while others wait for their
@@ -22,7 +22,7 @@
 //    workgroups' sums go to the workspace, and a second kernel adds those, all
 //    in a fixed order (no atomics, the same bits on every call).
 // Forward 16384x4096 with 8-bit output 98 us (6.2 TB/s), backward 8192x2880 37 us
-// (5.1 TB/s, 4.5 us of it the second kernel); one row 2.6 us.
+// (5.1 TB/s, 4 us of it the second kernel); one row 2.6 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -483,25 +483,29 @@ __global__ __launch_bounds__((threads_of<LANES, kBwdThreads>())) void k_rmsnorm_
 }
 
 // dgamma[c] = sum over the workgroups' sums, in their order: a workgroup takes
-// 16 columns (64-byte pieces of a row), 64 threads each every 64th row, and one
-// adds their sums.
+// 16 columns (64-byte pieces of a row), 64 threads each every 64th row; a wave
+// joins its four sums of a column and one thread the sixteen waves' (512x2880
+// 2.4 us; one thread adding all 64 sums 2.8).
 constexpr int kSumCols = 16, kSumThreads = 1024, kSumParts = kSumThreads / kSumCols;
 __global__ __launch_bounds__(kSumThreads) void k_column_sum(const float *__restrict__ partials,
                                                             int64_t groups, int64_t cols,
                                                             float *__restrict__ out)
 {
-    __shared__ float s[kSumParts][kSumCols];
+    __shared__ float s[kSumThreads / 64][kSumCols];
     const int k = threadIdx.x % kSumCols, part = threadIdx.x / kSumCols;
     const int64_t c = (int64_t)blockIdx.x * kSumCols + k;
     float v = 0.0f;
     if (c < cols)
 #pragma unroll 8
         for (int64_t g = part; g < groups; g += kSumParts) v += partials[g * cols + c];
-    s[part][k] = v;
+    // four parts of a wave, 16 lanes apart, then the waves
+    v = as_f(across_rows<1>(as_u(v), add_f32));
+    v = as_f(across_rows<2>(as_u(v), add_f32));
+    if (part % 4 == 0) s[part / 4][k] = v;
     __syncthreads();
     if (part || c >= cols) return;
-#pragma unroll 8
-    for (int w = 1; w < kSumParts; ++w) v += s[w][k];
+#pragma unroll
+    for (int w = 1; w < kSumThreads / 64; ++w) v += s[w][k];
     out[c] = v;
 }
 

@@ -612,11 +612,14 @@ struct Fwd {
 };
 
 // The gradients of the rows and of gamma in one launch while reading dy and h
-// again, from the caches, takes less than a second launch and its column sums
-// (one and two: 333x1000 FP32 3.6 and 8.3 us, 1024x2880 9.3 and 12.5, 2048x2880
-// 15.2 and 14.7, 654x6072 12.2 and 14.7, 1024x6072 17.6 and 16.7; rows that start
-// at any element 412x6073 11.3 and 16.1, 654x6073 18.9 and 17.8).
-constexpr int64_t kFewRows = 1024, kFewElems = int64_t(1) << 22, kFewElemsAny = int64_t(1) << 21;
+// again, from the caches, takes less than a second launch and its column sums,
+// which grows with the rows (one and two, on inputs of three calls in turn:
+// 333x1000 FP32 4.3 and 5.7 us, 512x2880 7.7 and 10.4, 640x2880 9.1 and 10.9,
+// 640x1000 7.0 and 6.2, 640x4096 9.6 and 13.1, 768x2880 10.5 and 10.9, 768x1000
+// 8.6 and 6.5, 1024x2880 14.4 and 11.6; 640x6072 11.8 and 13.8, FP32 16.6 and
+// 16.5; rows that start at any element 320x6073 9.6 and 14.2, 640x6073 17.1 and
+// 15.3).
+constexpr int64_t kFewRows = 640, kFewElems = int64_t(1) << 22, kFewElemsAny = int64_t(1) << 21;
 
 template <int LANES, int NCH>
 struct Bwd {

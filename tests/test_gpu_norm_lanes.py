@@ -52,7 +52,8 @@ def test_forward_of_many_rows_8bit(rows, cols, f8, stream):
 
 @pytest.mark.parametrize("rows, cols", [(1, 4096 + 8), (5, 4095), (300, 5120), (300, 5119), (1024, 4095), (1500, 4500),
                                         (4098, 4095), (4100, 4104), (3280, 5120), (3290, 5113), (3300, 5114), (33000, 513),
-                                        (8200, 2049), (4200, 4001), (16500, 1017)])
+                                        (8200, 2049), (4200, 4001), (16500, 1017), (640, 2880), (641, 2880), (640, 1000),
+                                        (641, 1001), (640, 3001), (640, 6072), (640, 64), (641, 64), (639, 4104)])
 @pytest.mark.parametrize("stream", ["bf16", "f32"])
 def test_backward(rows, cols, stream):
     x, res, gamma, h = inputs(rows, cols, stream, seed=rows)

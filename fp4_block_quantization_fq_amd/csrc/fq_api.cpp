@@ -1115,8 +1115,10 @@ fq_status check_moe_rows(int64_t T, int64_t k, int64_t H, int64_t rows, int64_t 
                     (long long)unit);
     if (rows < 1 || rows > kMaxDim)
         return fail(FQ_ERR_SHAPE, "rows=%lld must be >= 1 and below 2^31", (long long)rows);
-    if (H > kMaxElems / (rows > T ? rows : T))
-        return fail(FQ_ERR_SHAPE, "cols=%lld: rows*cols and tokens*cols must be at most 2^34",
+    // the kernels number a row's elements in 32 bits
+    if (H > kMaxDim || H > kMaxElems / (rows > T ? rows : T))
+        return fail(FQ_ERR_SHAPE,
+                    "cols=%lld must be below 2^31, rows*cols and tokens*cols at most 2^34",
                     (long long)H);
     return FQ_OK;
 }

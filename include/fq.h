@@ -495,9 +495,11 @@ fq_status fq_moe_sort(const int32_t *experts_of, int64_t tokens, int64_t k, int6
 /* Rows of the tokens in the sorted order: y[pos[t, j]] = x[t], +0 in rows
  * without an assignment.  y BF16 [rows, cols]; x BF16 [tokens, cols], or with
  * f8 the codes and scales of fq_rmsnorm_fwd, decoded on the way (rounded to
- * BF16).  cols a multiple of 8 (32 with f8).  pos and src as fq_moe_sort wrote
- * them; entries outside [0, rows) or [0, tokens * k) count as -1.  Its
- * backward is fq_moe_combine without weights. */
+ * BF16).  cols a multiple of 8 (32 with f8) below 2^31, rows below 2^31, rows *
+ * cols and tokens * cols at most 2^34, here and in the next two; tokens and k as
+ * for fq_moe_sort.  pos and src as fq_moe_sort wrote them; entries outside [0,
+ * rows) or [0, tokens * k) count as -1.  Its backward is fq_moe_combine without
+ * weights. */
 fq_status fq_moe_dispatch(const void *x, int32_t f8, const void *scales, int64_t tokens,
                           int64_t k, int64_t cols, int64_t rows, const int32_t *pos,
                           const int32_t *src, void *y_bf16, void *stream);

@@ -288,6 +288,14 @@ def _stream(stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _raw_stream(stream) -> int:
+    """Handle of a stream, or of the current one of the current device."""
+    if stream is not None:
+        return stream.cuda_stream
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+
+
 _binding_module = None
 
 
@@ -896,7 +904,9 @@ class AdamWPlan:
     """The tensors of an optimizer as the library takes them, checked once and
     laid out in device memory, so that a step is one launch.  It holds the
     tensors it was made from; their contents may change between steps, the
-    tensors may not."""
+    tensors may not.  Making one copies its table, so not while a graph is
+    captured; a captured step reads the table at every replay: keep the plan as
+    long as the graph."""
 
     def __init__(self, tensors):
         torch = _torch()
@@ -925,6 +935,18 @@ class AdamWPlan:
         self.address = self.host.data_ptr()
         _check(lib().fq_adamw_plan(array, len(array), self.state_type, self.address, nbytes))
         self.device = self.host.to(self.tensors[0].w.device) if self.tensors else None
+        self._streams = {_raw_stream(None)} if self.tensors else set()
+
+    def _read_on(self, stream):
+        """The table's memory belongs to the stream that it was made on; a step on
+        another one makes it that one's too, so that it is not handed out again
+        while that step still takes its pointers from it."""
+        if self.device is None:
+            return
+        raw = _raw_stream(stream)
+        if raw not in self._streams:
+            self.device.record_stream(_torch().cuda.current_stream() if stream is None else stream)
+            self._streams.add(raw)
 
 
 def adamw_plan(tensors) -> AdamWPlan:
@@ -936,6 +958,7 @@ def fq_adamw_step(plan: AdamWPlan, lr: float, step: int, beta1: float = 0.9, bet
     """One AdamW step (in place) over a plan's tensors.  step counts from 1;
     grad_scale is an FP32 device scalar the gradients are multiplied by; seed
     keys the stochastic rounding of 8-bit moments."""
+    plan._read_on(stream)
     st = (_binding_module or _binding()).adamw_step(
         plan.address, plan.device, plan.state_type, lr, beta1, beta2, eps, step, seed, grad_scale,
         stream)

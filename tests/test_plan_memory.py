@@ -1,0 +1,28 @@
+"""Where an AdamW plan's two copies lie and how long: shown with a stand-in for
+the device's memory, without a device."""
+import os
+from types import SimpleNamespace
+
+import pytest
+
+import fp4_block_quantization_fq_amd as fq
+
+
+@pytest.fixture(autouse=True)
+def built():
+    if not os.path.exists(fq.LIB_PATH):
+        pytest.skip("libfq.so not built")
+
+
+def test_the_table_belongs_to_every_stream_that_reads_it(monkeypatch):
+    """A step on another stream than the plan was made on marks the table's memory
+    as used there before it launches, once for each stream."""
+    events = []
+    plan = fq.adamw_plan([])
+    plan.device = SimpleNamespace(record_stream=lambda s: events.append(("record", s.cuda_stream)))
+    monkeypatch.setattr(fq, "_binding_module",
+                        SimpleNamespace(adamw_step=lambda *a: events.append(("step", a[-1].cuda_stream)) or 0))
+    one, two = SimpleNamespace(cuda_stream=0x100), SimpleNamespace(cuda_stream=0x200)
+    for s in (one, one, two):
+        fq.fq_adamw_step(plan, lr=1e-3, step=1, stream=s)
+    assert events == [("record", 0x100), ("step", 0x100), ("step", 0x100), ("record", 0x200), ("step", 0x200)]

@@ -931,7 +931,7 @@ class AdamWPlan:
             s.lr_mult, s.weight_decay = t.lr_mult, t.weight_decay
         self.state_type = FQ_STATE_F8 if self.f8 else FQ_STATE_F32
         nbytes = lib().fq_adamw_plan_size(len(array))
-        self.host = torch.empty(nbytes, dtype=torch.uint8)        # 64-byte aligned
+        self.host = torch.empty(nbytes, dtype=torch.uint8, device="cpu")        # 64-byte aligned
         self.address = self.host.data_ptr()
         _check(lib().fq_adamw_plan(array, len(array), self.state_type, self.address, nbytes))
         self.device = self.host.to(self.tensors[0].w.device) if self.tensors else None

@@ -26,3 +26,14 @@ def test_the_table_belongs_to_every_stream_that_reads_it(monkeypatch):
     for s in (one, one, two):
         fq.fq_adamw_step(plan, lr=1e-3, step=1, stream=s)
     assert events == [("record", 0x100), ("step", 0x100), ("step", 0x100), ("record", 0x200), ("step", 0x200)]
+
+
+def test_the_host_copy_is_in_host_memory():
+    """Whatever device torch makes tensors on by default: the library writes the
+    copy with plain stores."""
+    import torch
+    for kind in ("meta", "cpu"):
+        with torch.device(kind):
+            plan = fq.adamw_plan([])
+        assert plan.host.device.type == "cpu"
+        fq.fq_adamw_step(plan, lr=1e-3, step=1, stream=SimpleNamespace(cuda_stream=0))

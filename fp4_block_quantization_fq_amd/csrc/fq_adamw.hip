@@ -350,8 +350,13 @@ __global__ __launch_bounds__(threads_of<F8>()) void k_adamw_plan(
 // us streaming, 90 not, 8-bit ones 45.5 and 54.1; 2^23: 40.5, 45.9 and 26.5, 24.8;
 // 2^22: 21.0, 19.9 and 16.3, 14.7.
 constexpr int64_t kStreamElems = int64_t(1) << 24;
-// A grid holds fewer than 2^32 lanes; the kernels walk over what is left.
+// A grid holds fewer than 2^32 lanes; the kernels walk over what is left, and a
+// tile's number with the grid added stays below 2^32.  A list of kAdamWTensors
+// has few enough tiles by itself.
 constexpr uint32_t kMaxGrid = 1u << 20;
+static_assert(fqimpl::kAdamWMaxTiles + kMaxGrid <= UINT32_MAX, "a walk's tile numbers");
+static_assert(fqimpl::kAdamWTensors * ((uint64_t(1) << 34) / tile_of<true>()) <= fqimpl::kAdamWMaxTiles,
+              "tiles of a list");
 
 bool streams(uint32_t tiles, bool f8)
 {
@@ -362,9 +367,10 @@ bool streams(uint32_t tiles, bool f8)
 
 namespace fqimpl {
 
+uint32_t adamw_tile(bool f8) { return f8 ? tile_of<true>() : tile_of<false>(); }
 uint32_t adamw_tiles(int64_t n, bool f8)
 {
-    const int tile = f8 ? tile_of<true>() : tile_of<false>();
+    const int64_t tile = adamw_tile(f8);
     return (uint32_t)((n + tile - 1) / tile);
 }
 

@@ -1446,7 +1446,7 @@ fq_status fq_adamw_step(const fq_adamw_hyper *hyper, const fq_adamw_tensor *tens
         if (!t.n) continue;
         const uint32_t tiles = fqimpl::adamw_tiles(t.n, f8);
         uint32_t &n = a.step.count;
-        if (n == fqimpl::kAdamWTensors || a.step.tiles + (uint64_t)tiles > 0xFFFFFFFFull) {
+        if (n == fqimpl::kAdamWTensors) {
             FQ_TRY(device_status(fqimpl::launch_adamw(a, f8, (hipStream_t)stream), "AdamW launch"));
             n = a.step.tiles = 0;
         }
@@ -1484,8 +1484,9 @@ fq_status fq_adamw_plan(const fq_adamw_tensor *tensors, int64_t count, int32_t s
         live += tensors[i].n > 0;
         tiles += fqimpl::adamw_tiles(tensors[i].n, f8);
     }
-    if (tiles > 0xFFFFFFFFull)
-        return fail(FQ_ERR_SHAPE, "a plan's tensors must have fewer than 2^42 elements");
+    if (tiles > fqimpl::kAdamWMaxTiles)
+        return fail(FQ_ERR_SHAPE, "a plan's tensors take %llu tiles of %d elements, at most 2^31",
+                    (unsigned long long)tiles, (int)fqimpl::adamw_tile(f8));
     memset(plan, 0, need);
     AdamWPlan *p = (AdamWPlan *)plan;
     p->magic = kPlanMagic;

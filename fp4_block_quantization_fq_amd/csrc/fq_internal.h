@@ -225,7 +225,9 @@ struct AdamWArgs {
     uint32_t index[kAdamWTensors];          // number of each tensor in the whole list
     AdamWTensor t[kAdamWTensors];
 };
+uint32_t adamw_tile(bool f8);               // elements of a workgroup
 uint32_t adamw_tiles(int64_t n, bool f8);   // tiles that n elements take
+constexpr uint64_t kAdamWMaxTiles = uint64_t(1) << 31;      // of one launch
 hipError_t launch_adamw(const AdamWArgs &a, bool f8, hipStream_t stream);
 // The same with the table in device memory.
 hipError_t launch_adamw_plan(const AdamWStep &a, const AdamWTensor *t, const uint32_t *first,

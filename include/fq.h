@@ -576,7 +576,8 @@ fq_status fq_adamw_step(const fq_adamw_hyper *hyper, const fq_adamw_tensor *tens
  * (host memory, 16-byte aligned); the caller keeps them and copies them to
  * device memory once (16-byte aligned).  fq_adamw_step_plan takes both copies;
  * hyper->state_type must be the plan's.  A plan holds the tensors' addresses:
- * their contents may change between steps, where they are may not. */
+ * their contents may change between steps, where they are may not.  A plan has
+ * at most 2^31 tiles (of 4096 elements of a tensor, 2048 with 8-bit moments). */
 size_t fq_adamw_plan_size(int64_t count);
 fq_status fq_adamw_plan(const fq_adamw_tensor *tensors, int64_t count, int32_t state_type,
                         void *plan, size_t plan_bytes);

@@ -29,3 +29,25 @@ def test_rows_of_the_experts_are_narrower_than_2_31(L, cols):
     assert L.fq_moe_combine(p, p, 1, 1, cols, 1, p, p, None) == fq.FQ_ERR_SHAPE
     assert L.fq_moe_combine_bwd(p, p, p, 1, 1, cols, 1, p, p, p, p, None) == fq.FQ_ERR_SHAPE
     assert "cols" in L.fq_last_error().decode()
+
+
+@pytest.mark.parametrize("f8, tile", [(False, 4096), (True, 2048)])
+def test_a_plan_has_fewer_tiles_than_its_grid_can_walk_over(L, f8, tile):
+    """The kernel's walk adds the grid to a 32-bit tile number: the last number has
+    to stay below 2^32 with that added, whatever the tensors' lengths."""
+    each = (1 << 34) // tile                                     # tiles of the longest tensor
+
+    def plan(tiles):
+        lengths = [1 << 34] * (tiles // each) + ([tiles % each * tile] if tiles % each else [])
+        array = (fq.FqAdamWTensor * len(lengths))()
+        for t, n in zip(array, lengths):
+            t.w, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n = 0x1000, 0x2000, 0x3000, 0x4000, 0x5000, 0x6000, n
+        size = L.fq_adamw_plan_size(len(lengths))
+        buf = (ctypes.c_uint8 * (size + 64))()
+        at = ctypes.addressof(buf)
+        return L.fq_adamw_plan(array, len(lengths), int(f8), at + -at % 64, size)
+
+    assert plan((1 << 32) - 2) == fq.FQ_ERR_SHAPE
+    assert "tiles" in L.fq_last_error().decode()
+    assert plan((1 << 31) + 1) == fq.FQ_ERR_SHAPE
+    assert plan(1 << 31) == fq.FQ_OK

@@ -167,7 +167,9 @@ __device__ __forceinline__ uint32_t tensor_of(const uint32_t *__restrict__ first
 // which lifts subnormal v into the range they take (c2 = c * 2^-24); above, and
 // for infinities and NaN, by the correctly rounded operations.  With the latter
 // alone the step with 8-bit moments is bound by arithmetic (229 M elements 705
-// us instead of 657).
+// us instead of 657).  They also take every v (divide_from 0) where a positive
+// eps is outside 2^-100 .. 2^100: alone, as for v = 0, it may have no normal
+// reciprocal, while a positive root is between 2^-75 and 2^67 (c is at most 2^27).
 template <int N>
 __device__ __forceinline__ void update(const fqimpl::AdamWStep &a, const fqimpl::AdamWTensor &t,
                                        const float (&g)[N], float (&w)[N], float (&m)[N],
@@ -183,7 +185,7 @@ __device__ __forceinline__ void update(const fqimpl::AdamWStep &a, const fqimpl:
         v[e] = v[e] * a.beta2 + (gg * a.one_beta2) * gg;
     }
     const float c = a.inv_sqrt_bc2, c2 = c * 0x1p-24f;
-    if (__any(absmax(v) > as_u(0x1p79f))) {
+    if (__any(absmax(v) >= a.divide_from)) {
 #pragma unroll
         for (int e = 0; e < N; ++e)
             w[e] = w[e] * keep - (m[e] / (__builtin_sqrtf(v[e]) * c + a.eps)) * step;

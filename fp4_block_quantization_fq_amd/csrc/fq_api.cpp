@@ -1192,6 +1192,8 @@ fqimpl::AdamWStep adamw_step_of(const fq_adamw_hyper &h)
     a.step = (uint32_t)h.step;
     a.seed_lo = (uint32_t)h.seed;
     a.seed_hi = (uint32_t)(h.seed >> 32);
+    a.divide_from = a.eps == 0 || (a.eps >= 0x1p-100f && a.eps <= 0x1p100f)
+                        ? fqimpl::kAdamWDivideFrom : 0;
     return a;
 }
 

@@ -212,12 +212,14 @@ struct AdamWTensor {
     float lr_mult, weight_decay;
     int g_f32;
 };
+constexpr uint32_t kAdamWDivideFrom = 0x67000001u;      // the next FP32 above 2^79
 struct AdamWStep {           // what all tensors of a launch share
     uint32_t count;          // tensors of this launch, all with n > 0
     uint32_t tiles;          // of all of them
     float lr, beta1, one_beta1, beta2, one_beta2, eps, inv_bc1, inv_sqrt_bc2;
     const float *grad_scale; // device scalar or null
     uint32_t step, seed_lo, seed_hi;
+    uint32_t divide_from;    // bits of the smallest v of a correctly rounded update
 };
 struct AdamWArgs {
     AdamWStep step;

@@ -935,18 +935,17 @@ class AdamWPlan:
         self.address = self.host.data_ptr()
         _check(lib().fq_adamw_plan(array, len(array), self.state_type, self.address, nbytes))
         self.device = self.host.to(self.tensors[0].w.device) if self.tensors else None
-        self._streams = {_raw_stream(None)} if self.tensors else set()
+        self.stream = _raw_stream(None) if self.tensors else 0      # whose memory the table is
+        self._others = set()
 
     def _read_on(self, stream):
         """The table's memory belongs to the stream that it was made on; a step on
         another one makes it that one's too, so that it is not handed out again
         while that step still takes its pointers from it."""
-        if self.device is None:
-            return
         raw = _raw_stream(stream)
-        if raw not in self._streams:
+        if self.device is not None and raw not in self._others:
             self.device.record_stream(_torch().cuda.current_stream() if stream is None else stream)
-            self._streams.add(raw)
+            self._others.add(raw)
 
 
 def adamw_plan(tensors) -> AdamWPlan:
@@ -958,10 +957,9 @@ def fq_adamw_step(plan: AdamWPlan, lr: float, step: int, beta1: float = 0.9, bet
     """One AdamW step (in place) over a plan's tensors.  step counts from 1;
     grad_scale is an FP32 device scalar the gradients are multiplied by; seed
     keys the stochastic rounding of 8-bit moments."""
-    plan._read_on(stream)
     st = (_binding_module or _binding()).adamw_step(
         plan.address, plan.device, plan.state_type, lr, beta1, beta2, eps, step, seed, grad_scale,
-        stream)
+        stream, plan.stream, plan._read_on)
     if st:
         _check(st)
 

@@ -320,10 +320,11 @@ PyObject *moe_combine_bwd(PyObject *, PyObject *const *args, Py_ssize_t nargs)
 }
 
 // (address of the plan in host memory, the plan in device memory or None,
-//  state_type, lr, beta1, beta2, eps, step, seed, grad_scale, stream)
+//  state_type, lr, beta1, beta2, eps, step, seed, grad_scale, stream, handle of
+//  the stream that the device copy belongs to, what to call with another one)
 PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t nargs)
 {
-    Call c(args, nargs, 11);
+    Call c(args, nargs, 13);
     if (!c.ok) return nullptr;
     const void *plan = (const void *)(uintptr_t)c.u64(0);
     const void *plan_device = c.bytes(1, 0, "plan");
@@ -337,6 +338,11 @@ PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t nargs)
     h.seed = c.u64(8);
     h.grad_scale = (const float *)c.typed(9, at::kFloat, 1, "grad_scale");
     void *st = c.stream(10);
+    if (c.u64(11) != (uintptr_t)st && c.ok) {
+        PyObject *r = PyObject_CallOneArg(args[12], args[10]);
+        if (!r) return nullptr;
+        Py_DECREF(r);
+    }
     return launch(c, [&] { return fq_adamw_step_plan(&h, plan, plan_device, st); });
 }
 

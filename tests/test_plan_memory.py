@@ -14,18 +14,21 @@ def built():
         pytest.skip("libfq.so not built")
 
 
-def test_the_table_belongs_to_every_stream_that_reads_it(monkeypatch):
+def test_the_table_belongs_to_every_stream_that_reads_it():
     """A step on another stream than the plan was made on marks the table's memory
     as used there before it launches, once for each stream."""
-    events = []
+    marked, asked = [], []
     plan = fq.adamw_plan([])
-    plan.device = SimpleNamespace(record_stream=lambda s: events.append(("record", s.cuda_stream)))
-    monkeypatch.setattr(fq, "_binding_module",
-                        SimpleNamespace(adamw_step=lambda *a: events.append(("step", a[-1].cuda_stream)) or 0))
     one, two = SimpleNamespace(cuda_stream=0x100), SimpleNamespace(cuda_stream=0x200)
+    plan.device = SimpleNamespace(record_stream=lambda s: marked.append(s.cuda_stream))
     for s in (one, one, two):
+        plan._read_on(s)
+    assert marked == [0x100, 0x200]
+    # an empty plan's step launches nothing, and asks all the same
+    plan.device, plan._read_on = None, lambda s: asked.append(s.cuda_stream)
+    for s in (one, two, SimpleNamespace(cuda_stream=plan.stream)):
         fq.fq_adamw_step(plan, lr=1e-3, step=1, stream=s)
-    assert events == [("record", 0x100), ("step", 0x100), ("step", 0x100), ("record", 0x200), ("step", 0x200)]
+    assert asked == [0x100, 0x200]
 
 
 def test_the_host_copy_is_in_host_memory():

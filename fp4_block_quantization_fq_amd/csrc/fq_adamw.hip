@@ -15,8 +15,8 @@
 // Bound by memory: 28 bytes an element with FP32 moments, BF16 gradients and
 // the BF16 copy, 16.1 with 8-bit ones.  With FP32 moments a lane owns 4
 // consecutive elements, so that each access of a wave is one contiguous kilobyte
-// of an FP32 array, which streaming accesses need (100 M elements: 440 to 470 us,
-// 5.9 to 6.3 TB/s; with 8 elements a lane 515, and 532 streaming).  With 8-bit moments it owns 8, so
+// of an FP32 array, which streaming accesses need (100 M elements: 466 to 476 us,
+// 5.9 to 6.0 TB/s; with 8 elements a lane 515, and 532 streaming).  With 8-bit moments it owns 8, so
 // that a state block is one 16-lane DPP row and the work for its scale is done
 // once for 8 elements; the master weight's two half-used kilobytes go through
 // the caches, the rest streams (134 M elements: 378 us; two times 4 elements a
@@ -350,7 +350,8 @@ __global__ __launch_bounds__(threads_of<F8>()) void k_adamw_plan(
 
 // Streaming accesses from this many elements on.  2^24 elements: FP32 moments 79
 // us streaming, 90 not, 8-bit ones 45.5 and 54.1; 2^23: 40.5, 45.9 and 26.5, 24.8;
-// 2^22: 21.0, 19.9 and 16.3, 14.7.
+// 2^22: 21.0, 19.9 and 16.3, 14.7.  One limit for both kinds: it is the 8-bit
+// moments', FP32 ones cross near 2^22.5 and lose up to 5 us below the limit.
 constexpr int64_t kStreamElems = int64_t(1) << 24;
 // A grid holds fewer than 2^32 lanes; the kernels walk over what is left, and a
 // tile's number with the grid added stays below 2^32.  A list of kAdamWTensors

@@ -201,7 +201,7 @@ hipError_t launch_moe_combine(const MoeRowsArgs &a, hipStream_t stream);
 hipError_t launch_moe_combine_bwd(const MoeRowsArgs &a, hipStream_t stream);
 
 // fq_adamw.hip
-constexpr uint32_t kAdamWTensors = 32;      // of one launch (the table is 2.4 KB of arguments)
+constexpr uint32_t kAdamWTensors = 32;      // of one launch whose table is its arguments
 struct AdamWTensor {
     float *w;
     void *w_bf16;            // or null
@@ -227,6 +227,7 @@ struct AdamWArgs {
     uint32_t index[kAdamWTensors];          // number of each tensor in the whole list
     AdamWTensor t[kAdamWTensors];
 };
+static_assert(sizeof(AdamWTensor) == 80 && sizeof(AdamWArgs) <= 2880, "of 4 KB of arguments");
 uint32_t adamw_tile(bool f8);               // elements of a workgroup
 uint32_t adamw_tiles(int64_t n, bool f8);   // tiles that n elements take
 constexpr uint64_t kAdamWMaxTiles = uint64_t(1) << 31;      // of one launch

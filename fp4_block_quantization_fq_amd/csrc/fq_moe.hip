@@ -34,6 +34,8 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxExperts = fqimpl::kMoeMaxExperts;
 
+static_assert(kSortThreads == kMaxExperts, "one expert a thread");
+
 // ---------------------------------------------------------------------------
 // sort
 // ---------------------------------------------------------------------------
@@ -79,7 +81,7 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_place(fqimpl::MoeSortArgs 
     __shared__ uint32_t wave_sums[kSortWaves];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const int64_t lo = (int64_t)blockIdx.x * a.chunk, hi = min(lo + a.chunk, a.n);
-    const uint32_t e = tid;                // kSortThreads == kMaxExperts: one expert a thread
+    const uint32_t e = tid;                // one expert a thread
     u32w4 *mine_before = (u32w4 *)before[e];
     uint32_t x = expert_of(a.ids, lo + tid, hi, a.E);     // of the first step
     total[e] = next[e] = 0;
@@ -470,8 +472,10 @@ hipError_t by_k(const fqimpl::MoeRowsArgs &a, F launch)
     return launch(std::integral_constant<int, 0>(), a.T);
 }
 
-// Streaming accesses from this many elements of sorted rows on, where they
-// leave the caches.  Of 8192 tokens (94 M elements) and 2048 (24 M): combine
+// Streaming accesses from this many elements of assigned rows (T * k * H) on, where
+// they leave the caches.  Padding, which dispatch and combine's backward write
+// too, does not count: its share is not known without the ids, and a call that is
+// mostly padding streams late.  Of 8192 tokens (94 M elements) and 2048 (24 M): combine
 // 41.6 us streaming, 46.8 not, and 13.1, 12.1; dispatch (its stores) 41.3, 50.6
 // and 15.6, 15.5; combine's backward 76, 90 and 25.5, 29.2, of 1024 tokens (12 M)
 // 16.0, 14.5.

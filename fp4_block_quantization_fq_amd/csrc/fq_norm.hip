@@ -10,19 +10,22 @@
 // Both passes are bound by memory: one read of every input and one write of
 // every output, a row staying in registers between the statistic and its use.
 //  * LANES lanes share a row (8 for a row of 64 elements, up to a workgroup of
-//    1024; powers of two, or 5/8 of one), each holding NCH chunks of 8 consecutive elements (16-byte BF16
-//    accesses); chunk i of lane l is i * LANES + l, so neighbouring lanes read
-//    neighbouring chunks.  One chunk a lane up to 8192 columns: many short
-//    waves keep the loads of some rows in flight while others wait for their
-//    sum (16384x4096 with 8-bit output: 512 lanes 100 us, 256 lanes of two
-//    chunks 107, 64 of eight 113; backward 8192x2880: 37.1, 39.5 and 41.2).
+//    1024; powers of two, or 5/8 of one), each holding NCH chunks of 8
+//    consecutive elements (16-byte BF16 accesses); chunk i of lane l is i * LANES
+//    + l, so neighbouring lanes read neighbouring chunks.  One chunk a lane up to
+//    8192 columns in the backward, and in the forward of few rows or of a large
+//    call with a residual: many short waves keep the loads of some rows in flight
+//    while others wait for their sum (16384x4096 with 8-bit output: 512 lanes 100
+//    us, 256 lanes of two chunks 107, 64 of eight 113; backward 8192x2880: 37.1,
+//    39.5 and 41.2).  Two chunks a lane in the other forwards from 512 rows on
+//    (Fwd::go).
 //  * An MX block of 32 is four neighbouring lanes (two DPP steps).
 //  * dgamma: each group of lanes walks over rows and keeps its column sums in
 //    registers; the groups of a workgroup are added through LDS, the
 //    workgroups' sums go to the workspace, and a second kernel adds those, all
 //    in a fixed order (no atomics, the same bits on every call).
-// Forward 16384x4096 with 8-bit output 98 us (6.2 TB/s), backward 8192x2880 37 us
-// (5.1 TB/s, 4 us of it the second kernel); one row 2.6 us.
+// Forward 16384x4096 with 8-bit output 98 to 101 us (6.0 to 6.2 TB/s), backward
+// 8192x2880 37 us (5.1 TB/s, 4 us of it the second kernel); one row 2.6 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -618,7 +621,9 @@ struct Fwd {
 // 640x1000 7.0 and 6.2, 640x4096 9.6 and 13.1, 768x2880 10.5 and 10.9, 768x1000
 // 8.6 and 6.5, 1024x2880 14.4 and 11.6; 640x6072 11.8 and 13.8, FP32 16.6 and
 // 16.5; rows that start at any element 320x6073 9.6 and 14.2, 640x6073 17.1 and
-// 15.3).
+// 15.3).  The crossing depends on the columns, the limit does not: at 1000 columns
+// one launch still wins at 512 rows (5.4 and 5.9), at 640 it loses 0.8 us, and up
+// to 1.1 in FP32 rows that start at any element (640x2047 13.8 and 12.7).
 constexpr int64_t kFewRows = 640, kFewElems = int64_t(1) << 22, kFewElemsAny = int64_t(1) << 21;
 
 template <int LANES, int NCH>

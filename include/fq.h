@@ -536,7 +536,8 @@ fq_status fq_moe_combine_bwd(const void *dout_bf16, const void *y_bf16, const fl
  * floor(2^16 * fraction of the way to it), with r16 the low (m) or high (v)
  * half of word n mod 4 of Philox4x32-10 with key seed and counter (low and
  * high word of n / 4, number of the tensor in the list, step), n the element.
- * A positive v gets at least code 1; infinities and NaN get code 0x7F, NaN.
+ * A positive v gets at least code 1; infinities and NaN get code 0x7F, NaN (m
+ * with its sign).
  * Rounding to nearest would keep an 8-bit v where it is for ever, because
  * 1 - beta2 is far below half a step of the format.  All-zero codes and scales
  * are the state before the first step.

@@ -166,8 +166,9 @@ __device__ __forceinline__ uint32_t tensor_of(const uint32_t *__restrict__ first
 // root and reciprocal, each within one unit in the last place, of v * 2^48,
 // which lifts subnormal v into the range they take (c2 = c * 2^-24); above, and
 // for infinities and NaN, by the correctly rounded operations.  With the latter
-// alone the step with 8-bit moments is bound by arithmetic (229 M elements 705
-// us instead of 657).  They also take every v (divide_from 0) where a positive
+// alone calls that the caches hold are slower (8-bit moments, 2^22 elements 15.7
+// us instead of 13.8, 2^20 6.1 and 5.5; FP32 2^21 9.1 and 8.6); from 2^25 on
+// memory hides them.  They also take every v (divide_from 0) where a positive
 // eps is outside 2^-100 .. 2^100: alone, as for v = 0, it may have no normal
 // reciprocal, while a positive root is between 2^-75 and 2^67 (c is at most 2^27).
 template <int N>

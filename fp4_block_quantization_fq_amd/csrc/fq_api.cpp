@@ -1132,8 +1132,10 @@ fq_status check_adamw_hyper(const fq_adamw_hyper *hyper)
         return fail(FQ_ERR_DESC, "hyper->state_type=%d is not FQ_STATE_F32/F8", h.state_type);
     if (!(h.beta1 >= 0 && h.beta1 < 1 && h.beta2 >= 0 && h.beta2 < 1))
         return fail(FQ_ERR_DESC, "beta1 and beta2 must be in [0, 1)");
-    if (!(h.eps >= 0) || !std::isfinite(h.lr) || !std::isfinite(h.eps))
-        return fail(FQ_ERR_DESC, "lr must be finite and eps finite and >= 0");
+    // as the kernels use them
+    if (!(h.eps >= 0) || !std::isfinite((float)h.lr) || !std::isfinite((float)h.eps) ||
+        (h.eps > 0 && (float)h.eps == 0))
+        return fail(FQ_ERR_DESC, "lr must be finite, eps 0 or positive and finite, in FP32");
     if (h.step < 1 || h.step > 0xFFFFFFFFll)
         return fail(FQ_ERR_DESC, "step=%lld must be in [1, 2^32)", (long long)h.step);
     FQ_TRY(check_ptr(h.grad_scale, "hyper->grad_scale", false, 4));

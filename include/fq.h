@@ -541,7 +541,9 @@ fq_status fq_moe_combine_bwd(const void *dout_bf16, const void *y_bf16, const fl
  * Rounding to nearest would keep an 8-bit v where it is for ever, because
  * 1 - beta2 is far below half a step of the format.  All-zero codes and scales
  * are the state before the first step.
- * step counts from 1.  grad_scale: device scalar (a clipping factor), NULL for
+ * step counts from 1.  lr and eps are rounded to FP32, where lr is finite and eps 0
+ * or positive and finite (with eps 0 an element whose m and v are 0 becomes NaN,
+ * 0 / 0).  grad_scale: device scalar (a clipping factor), NULL for
  * 1.  lr and step are read by the call: a captured call keeps them.  w, w_bf16,
  * g, m, v 16-byte aligned, scales 4-byte; n <= 2^34, n = 0 is skipped;
  * `tensors` is read during the call only.  No workspace. */

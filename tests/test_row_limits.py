@@ -51,3 +51,18 @@ def test_a_plan_has_fewer_tiles_than_its_grid_can_walk_over(L, f8, tile):
     assert "tiles" in L.fq_last_error().decode()
     assert plan((1 << 31) + 1) == fq.FQ_ERR_SHAPE
     assert plan(1 << 31) == fq.FQ_OK
+
+
+def test_adamw_refuses_what_fp32_does_not_hold(L):
+    """lr and eps are used in FP32: an lr or eps that is infinite there, or a positive
+    eps that is 0 there, would make weights NaN that the formula leaves finite."""
+    t = fq.FqAdamWTensor(w=0x1000, g=0x2000, m=0x3000, v=0x4000, n=0, lr_mult=1.0)
+
+    def step(**fields):
+        h = fq.FqAdamWHyper(**dict(dict(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, step=1), **fields))
+        return L.fq_adamw_step(ctypes.byref(h), ctypes.byref(t), 1, None)
+
+    for bad in (dict(lr=1e39), dict(lr=-1e39), dict(eps=1e39), dict(eps=1e-60), dict(eps=2.0 ** -150)):
+        assert step(**bad) == fq.FQ_ERR_DESC, bad
+    for good in (dict(lr=3.4e38), dict(lr=-1.0), dict(eps=3.4e38), dict(eps=2.0 ** -149), dict(eps=0.0), dict(lr=1e-60)):
+        assert step(**good) == fq.FQ_OK, good

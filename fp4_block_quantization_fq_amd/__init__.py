@@ -303,7 +303,7 @@ def _binding():
     """The compiled argument marshalling of the row operators."""
     global _binding_module
     if _binding_module is None:
-        lib()                              # loaded first: the extension links to it
+        lib(), _torch()                    # loaded first: the extension links to them
         from . import _fq_binding
         _binding_module = _fq_binding
     return _binding_module

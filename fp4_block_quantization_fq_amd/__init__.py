@@ -30,6 +30,7 @@ FQ_OSCI_BIN_CENTRE, FQ_OSCI_GRID_VALUE = 0, 1
 FQ_F8_NONE, FQ_F8_MX, FQ_F8_ROW = 0, 1, 2
 FQ_TYPE_BF16, FQ_TYPE_F32 = 0, 1
 FQ_STATE_F32, FQ_STATE_F8 = 0, 1
+FQ_ACT_NONE, FQ_ACT_RELU, FQ_ACT_SILU, FQ_ACT_GELU = 0, 1, 2, 3
 FQ_MOE_MAX_K, FQ_MOE_MAX_ALIGN = 64, 1024
 STATE_BLOCK = 128                 # elements under one scale of an 8-bit AdamW state
 
@@ -45,7 +46,9 @@ EXPORTED = (
     "fq_qlinear_bwd_retain", "fq_rmsnorm_fwd", "fq_rmsnorm_bwd_workspace_size",
     "fq_rmsnorm_bwd", "fq_moe_rows", "fq_moe_sort_workspace_size", "fq_moe_sort",
     "fq_moe_dispatch", "fq_moe_combine", "fq_moe_combine_bwd", "fq_adamw_step",
-    "fq_adamw_plan_size", "fq_adamw_plan", "fq_adamw_step_plan",
+    "fq_adamw_plan_size", "fq_adamw_plan", "fq_adamw_step_plan", "fq_f8_encode", "fq_f8_decode",
+    "fq_linear_fwd_workspace_size", "fq_linear_fwd", "fq_linear_bwd_workspace_size", "fq_linear_bwd",
+    "fq_glu_fwd_workspace_size", "fq_glu_fwd", "fq_glu_bwd_workspace_size", "fq_glu_bwd",
 )
 
 
@@ -94,6 +97,15 @@ class FqAdamWHyper(ctypes.Structure):
         ("grad_scale", ctypes.c_void_p),
         ("state_type", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
+    ]
+
+
+class FqGate(ctypes.Structure):
+    _fields_ = [
+        ("act", ctypes.c_int32),
+        ("alpha", ctypes.c_float),
+        ("limit", ctypes.c_float),
+        ("shift", ctypes.c_float),
     ]
 
 
@@ -199,6 +211,28 @@ def lib() -> ctypes.CDLL:
         L.fq_adamw_plan.restype = ctypes.c_int
         L.fq_adamw_step_plan.argtypes = [ctypes.POINTER(FqAdamWHyper), vp, vp, vp]
         L.fq_adamw_step_plan.restype = ctypes.c_int
+        L.fq_f8_encode.argtypes = [vp, i32, i64, i64, vp, vp, vp]
+        L.fq_f8_encode.restype = ctypes.c_int
+        L.fq_f8_decode.argtypes = [vp, vp, i32, i64, i64, vp, vp]
+        L.fq_f8_decode.restype = ctypes.c_int
+        gate = ctypes.POINTER(FqGate)
+        for op in ("linear", "glu"):
+            fn = getattr(L, f"fq_{op}_fwd_workspace_size")
+            fn.argtypes, fn.restype = [i64, i64, i64, i64], sz
+            fn = getattr(L, f"fq_{op}_bwd_workspace_size")
+            fn.argtypes, fn.restype = [i64, i64, i64, i64, i32], sz
+        L.fq_linear_fwd.argtypes = [vp, vp, vp, i32, vp, i64, i64, i64, i64, vp, i32, vp, i32, vp, vp,
+                                    i32, vp, sz, vp]
+        L.fq_linear_fwd.restype = ctypes.c_int
+        L.fq_linear_bwd.argtypes = [vp, vp, i32, vp, vp, vp, i32, vp, i64, i64, i64, i64, vp, i32, vp,
+                                    vp, i32, vp, vp, sz, vp]
+        L.fq_linear_bwd.restype = ctypes.c_int
+        L.fq_glu_fwd.argtypes = [gate, vp, vp, vp, i32, i64, i64, i64, i64, vp, vp, i32, vp, vp, vp, sz,
+                                 vp]
+        L.fq_glu_fwd.restype = ctypes.c_int
+        L.fq_glu_bwd.argtypes = [gate, vp, vp, i32, vp, vp, vp, i32, vp, i64, i64, i64, i64, vp, vp, vp,
+                                 i32, vp, vp, vp, sz, vp]
+        L.fq_glu_bwd.restype = ctypes.c_int
         L.fq_status_string.argtypes = [ctypes.c_int]
         L.fq_status_string.restype = ctypes.c_char_p
         L.fq_last_error.argtypes = []
@@ -962,6 +996,175 @@ def fq_adamw_step(plan: AdamWPlan, lr: float, step: int, beta1: float = 0.9, bet
         stream, plan.stream, plan._read_on)
     if st:
         _check(st)
+
+
+# ---------------------------------------------------------------------------
+# the feed-forward products, and checkpoints in 8 bits
+# ---------------------------------------------------------------------------
+
+def _f8_scales(rows: int, cols: int, f8: int, device):
+    torch = _torch()
+    if f8 == FQ_F8_MX:
+        return torch.empty((rows, cols // 32), dtype=torch.uint8, device=device)
+    return torch.empty(rows, dtype=torch.float32, device=device)
+
+
+def fq_f8_encode(x, f8: int, codes=None, scales=None, stream=None):
+    """x BF16 [rows, cols] as 8-bit rows: (codes uint8 [rows, cols], scales)."""
+    if codes is None or scales is None:
+        rows, cols = _matrix(x, "x")
+        with _allocating(stream):
+            if codes is None:
+                codes = _torch().empty((rows, cols), dtype=_torch().uint8, device=x.device)
+            if scales is None:
+                scales = _f8_scales(rows, cols, f8, x.device)
+    st = (_binding_module or _binding()).f8_encode(x, f8, codes, scales, stream)
+    if st:
+        _check(st)
+    return codes, scales
+
+
+def fq_f8_decode(codes, scales, f8: int, y=None, stream=None):
+    """The values that 8-bit rows stand for, in BF16."""
+    if y is None:
+        with _allocating(stream):
+            y = _torch().empty(_matrix(codes, "codes"), dtype=_torch().bfloat16, device=codes.device)
+    st = (_binding_module or _binding()).f8_decode(codes, scales, f8, y, stream)
+    if st:
+        _check(st)
+    return y
+
+
+def _product_workspace(size: int, device):
+    return _torch().empty((size,), dtype=_torch().uint8, device=device)
+
+
+def linear_fwd_workspace(rows: int, k: int, n: int, experts: int, device):
+    return _product_workspace(lib().fq_linear_fwd_workspace_size(rows, k, n, experts), device)
+
+
+def glu_fwd_workspace(rows: int, k: int, n: int, experts: int, device):
+    return _product_workspace(lib().fq_glu_fwd_workspace_size(rows, k, n, experts), device)
+
+
+def linear_bwd_workspace(rows: int, k: int, n: int, experts: int, device, x_f8: int = FQ_F8_NONE):
+    return _product_workspace(lib().fq_linear_bwd_workspace_size(rows, k, n, experts, x_f8), device)
+
+
+def glu_bwd_workspace(rows: int, k: int, n: int, experts: int, device, x_f8: int = FQ_F8_NONE):
+    return _product_workspace(lib().fq_glu_bwd_workspace_size(rows, k, n, experts, x_f8), device)
+
+
+def _weights(w, offsets):
+    """(experts, columns) of a weight; experts is 0 for one product."""
+    if w.dim() != (2 if offsets is None else 3):
+        raise ValueError("w must be [k, columns], or [experts, k, columns] with offsets")
+    return (0 if offsets is None else w.shape[0]), w.shape[-1]
+
+
+def fq_linear_fwd(x, w, bias=None, res=None, act: int = FQ_ACT_NONE, offsets=None, pre=None,
+                  pre_f8: int = FQ_F8_NONE, pre_scales=None, y=None, ws=None, stream=None):
+    """y = act(x @ w + bias) + res.
+
+    x BF16 [rows, k], w BF16 [k, n]; with offsets (int32 [experts + 1], of
+    fq_moe_sort) w [experts, k, n] and every segment of rows meets its own expert.
+    y is BF16 unless it or res says FP32; y may be res.  pre, if given, receives
+    the values before the activation for the backward: BF16 [rows, n], or uint8
+    codes and pre_scales [rows, n / 32] with pre_f8=FQ_F8_MX.  Returns y."""
+    if y is None or ws is None:
+        torch = _torch()
+        rows, k = _matrix(x, "x")
+        experts, n = _weights(w, offsets)
+        with _allocating(stream):
+            if y is None:
+                y = (torch.empty((rows, n), dtype=torch.bfloat16, device=x.device) if res is None
+                     else torch.empty_like(res))
+            if ws is None:
+                ws = linear_fwd_workspace(rows, k, n, experts, x.device)
+    st = (_binding_module or _binding()).linear_fwd(x, w, bias, res, offsets, act, pre, pre_f8,
+                                                    pre_scales, y, ws, stream)
+    if st:
+        _check(st)
+    return y
+
+
+def _bwd_outputs(x, w, offsets, dx, dw, dbias, ws, need, dw_dtype, x_f8, workspace, halves, stream):
+    """The outputs and the workspace of a product's backward that were not given."""
+    need_dx, need_dw, need_dbias = need
+    dx, dw, dbias = (v if n else None for v, n in zip((dx, dw, dbias), need))
+    if (need_dx and dx is None) or (need_dw and dw is None) or (need_dbias and dbias is None) or ws is None:
+        torch = _torch()
+        rows, k = _matrix(x, "x")
+        experts, cols = _weights(w, offsets)
+        with _allocating(stream):
+            if need_dx and dx is None:
+                dx = torch.empty((rows, k), dtype=torch.bfloat16, device=x.device)
+            if need_dw and dw is None:
+                dw = torch.empty(w.shape, dtype=dw_dtype or torch.bfloat16, device=x.device)
+            if need_dbias and dbias is None:
+                dbias = torch.empty((*w.shape[:-2], cols), dtype=torch.float32, device=x.device)
+            if ws is None:
+                ws = workspace(rows, k, cols // halves, experts, x.device, x_f8)
+    return dx, dw, dbias, ws
+
+
+def fq_linear_bwd(dy, x, w, pre=None, act: int = FQ_ACT_NONE, offsets=None, x_f8: int = FQ_F8_NONE,
+                  x_scales=None, pre_f8: int = FQ_F8_NONE, pre_scales=None, dx=None, dw=None,
+                  dbias=None, ws=None, need_dx: bool = True, need_dw: bool = True,
+                  need_dbias: bool = True, dw_dtype=None, stream=None):
+    """(dx, dw, dbias) of fq_linear_fwd for the gradient dy of y (dy is also the
+    gradient of its residual).  x BF16, or the codes of 8-bit rows with x_f8 and
+    x_scales; pre what the forward kept, needed with an activation.  dw is BF16
+    unless it or dw_dtype says FP32; need_...=False leaves an output out (None)."""
+    dx, dw, dbias, ws = _bwd_outputs(x, w, offsets, dx, dw, dbias, ws, (need_dx, need_dw, need_dbias),
+                                     dw_dtype, x_f8, linear_bwd_workspace, 1, stream)
+    st = (_binding_module or _binding()).linear_bwd(dy, x, w, pre, x_f8, x_scales, pre_f8, pre_scales,
+                                                    offsets, dx, dw, dbias, ws, act, stream)
+    if st:
+        _check(st)
+    return dx, dw, dbias
+
+
+def fq_glu_fwd(x, w, bias=None, act: int = FQ_ACT_SILU, alpha: float = 1.0, limit: float = math.inf,
+               shift: float = 0.0, offsets=None, pre=None, pre_f8: int = FQ_F8_NONE, pre_scales=None,
+               h=None, ws=None, stream=None):
+    """h = act(min(g, limit)) * (clamp(u, -limit, limit) + shift) of [g, u] = x @ w + bias.
+
+    x BF16 [rows, k], w BF16 [k, 2 n] (the gate's columns first), or [experts, k,
+    2 n] with offsets; alpha is SiLU's slope.  pre as for fq_linear_fwd, of both
+    projections: [rows, 2 n].  Returns h, BF16 [rows, n]."""
+    if h is None or ws is None:
+        torch = _torch()
+        rows, k = _matrix(x, "x")
+        experts, cols = _weights(w, offsets)
+        with _allocating(stream):
+            if h is None:
+                h = torch.empty((rows, cols // 2), dtype=torch.bfloat16, device=x.device)
+            if ws is None:
+                ws = glu_fwd_workspace(rows, k, cols // 2, experts, x.device)
+    st = (_binding_module or _binding()).glu_fwd(x, w, bias, offsets, act, alpha, limit, shift, pre,
+                                                 pre_f8, pre_scales, h, ws, stream)
+    if st:
+        _check(st)
+    return h
+
+
+def fq_glu_bwd(dh, x, w, pre, act: int = FQ_ACT_SILU, alpha: float = 1.0, limit: float = math.inf,
+               shift: float = 0.0, offsets=None, x_f8: int = FQ_F8_NONE, x_scales=None,
+               pre_f8: int = FQ_F8_NONE, pre_scales=None, dx=None, dw=None, dbias=None, h=None, ws=None,
+               need_dx: bool = True, need_dw: bool = True, need_dbias: bool = True, dw_dtype=None,
+               stream=None):
+    """(dx, dw, dbias) of fq_glu_fwd for the gradient dh of h, from what it kept.
+    h, if given, receives the block's output again, for the next product's
+    backward.  Other arguments as for fq_linear_bwd."""
+    dx, dw, dbias, ws = _bwd_outputs(x, w, offsets, dx, dw, dbias, ws, (need_dx, need_dw, need_dbias),
+                                     dw_dtype, x_f8, glu_bwd_workspace, 2, stream)
+    st = (_binding_module or _binding()).glu_bwd(dh, x, w, pre, x_f8, x_scales, pre_f8, pre_scales,
+                                                 offsets, dx, dw, dbias, ws, act, alpha, limit, shift, h,
+                                                 stream)
+    if st:
+        _check(st)
+    return dx, dw, dbias
 
 
 def version() -> str:

@@ -1,0 +1,160 @@
+// fq_act.hpp -- device code that the feed-forward products and the kernels
+// around them share: activations and their derivatives, the gate, 8-bit blocks,
+// and the experts' segments of rows.
+//
+// Activations are FP32: sigmoid from expf (1 ulp) and the hardware's reciprocal
+// (1 ulp), GELU from erff.  An infinite value before SiLU or GELU may give NaN
+// (infinity times 0), as their formulas have it.
+#pragma once
+
+#include "fq_internal.h"
+#include "fq_rows.hpp"
+
+namespace fqdev {
+
+using fqimpl::Gate;
+
+__device__ __forceinline__ float sigmoid(float v)
+{
+    return __builtin_amdgcn_rcpf(1.0f + expf(-v));
+}
+
+// a(z) and a'(z)
+__device__ __forceinline__ float act1(int act, float alpha, float z)
+{
+    if (act == fqimpl::ACT_SILU) return z * sigmoid(alpha * z);
+    if (act == fqimpl::ACT_GELU) return z * (0.5f + 0.5f * erff(z * 0.70710678118654752f));
+    if (act == fqimpl::ACT_RELU) return z <= 0.0f ? 0.0f : z;
+    return z;
+}
+__device__ __forceinline__ float act1_grad(int act, float alpha, float z, float *value)
+{
+    if (act == fqimpl::ACT_SILU) {
+        const float s = sigmoid(alpha * z);
+        *value = z * s;
+        return s * (1.0f + alpha * z * (1.0f - s));
+    }
+    if (act == fqimpl::ACT_GELU) {
+        const float phi = 0.5f + 0.5f * erff(z * 0.70710678118654752f);
+        *value = z * phi;
+        return phi + z * (0.39894228040143268f * expf(-0.5f * z * z));
+    }
+    if (act == fqimpl::ACT_RELU) {
+        *value = z <= 0.0f ? 0.0f : z;
+        return z <= 0.0f ? 0.0f : 1.0f;
+    }
+    *value = z;
+    return 1.0f;
+}
+__device__ __forceinline__ void act8(int act, float alpha, float (&z)[8])
+{
+    if (act == fqimpl::ACT_NONE) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act1(act, alpha, z[i]);
+}
+
+// g = a(min(g, limit)) (clamp(u, -limit, limit) + shift); NaN stays NaN
+__device__ __forceinline__ void glu8(const Gate &t, float (&g)[8], const float (&u)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float gate = g[i] > t.limit ? t.limit : g[i];
+        const float up = u[i] > t.limit ? t.limit : u[i] < -t.limit ? -t.limit : u[i];
+        g[i] = act1(t.act, t.alpha, gate) * (up + t.shift);
+    }
+}
+// Its backward for the gradient dh: dg and du into g and u, h's value into dh.
+__device__ __forceinline__ void glu8_grad(const Gate &t, float (&g)[8], float (&u)[8], float (&dh)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const bool g_out = g[i] > t.limit, u_out = u[i] > t.limit || u[i] < -t.limit;
+        const float gate = g_out ? t.limit : g[i];
+        const float up = (u[i] > t.limit ? t.limit : u[i] < -t.limit ? -t.limit : u[i]) + t.shift;
+        float a;
+        const float da = act1_grad(t.act, t.alpha, gate, &a);
+        g[i] = g_out ? 0.0f : dh[i] * up * da;
+        u[i] = u_out ? 0.0f : dh[i] * a;
+        dh[i] = a * up;
+    }
+}
+
+// ---- 8-bit blocks ------------------------------------------------------------------
+// Eight of a block's 32 values (four neighbouring lanes hold the block): E4M3
+// codes under the smallest power of two that keeps them below 448; returns its
+// E8M0 code (255 and codes 0x7F where the block has an infinity or NaN).
+__device__ __forceinline__ uint32_t mx8_encode8(const float (&v)[8], u32w2 *codes)
+{
+    const uint32_t top = dpp_max_xor2(dpp_max_xor1(absmax(v)));
+    const uint32_t code = mx8_scale_code(top);
+    const float inv = e8m0_recip(code);
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
+    *codes = e4m3_encode8(q);
+    if (top < 0x7F800000u) return code;
+    *codes = (u32w2){0x7F7F7F7Fu, 0x7F7F7F7Fu};
+    return 255u;
+}
+// the value of an E8M0 code, NaN for 255
+__device__ __forceinline__ float mx8_scale(uint32_t code)
+{
+    return code == 255u ? as_f(0x7FC00000u) : e8m0_value(code);
+}
+
+// ---- the experts' segments of rows ---------------------------------------------------
+// offsets[e] .. offsets[e + 1], brought into 0 .. rows, so that no entry can lead
+// outside the buffers.
+__device__ __forceinline__ void segment_of(const int32_t *offsets, int e, int rows, int *begin, int *end)
+{
+    *begin = min(max(offsets[e], 0), rows);
+    *end = max(*begin, min(offsets[e + 1], rows));
+}
+__device__ __forceinline__ int wave_total(int v)
+{
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    return __builtin_amdgcn_readfirstlane(v);
+}
+// Tiles of `size` rows that experts first .. last take, the same in all lanes.
+__device__ __forceinline__ int segment_tiles(const int32_t *offsets, int experts, int rows, int size, int lane)
+{
+    int n = 0;
+    for (int e = lane; e < experts; e += 64) {
+        int a, b;
+        segment_of(offsets, e, rows, &a, &b);
+        n += (b - a + size - 1) / size;
+    }
+    return wave_total(n);
+}
+// The expert and the rows of tile number `tile`, below segment_tiles.
+__device__ __forceinline__ void find_segment(const int32_t *offsets, int experts, int rows, int size, int tile,
+                                             int lane, int *expert, int *row0, int *row_end)
+{
+    int before = 0;
+    for (int first = 0; first < experts; first += 64) {
+        const int e = first + lane;
+        int a = 0, b = 0;
+        if (e < experts) segment_of(offsets, e, rows, &a, &b);
+        const int n = (b - a + size - 1) / size;
+        int sum = n;                                     // of this lane and those before it
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int s = __shfl_up(sum, d);
+            if (lane >= d) sum += s;
+        }
+        const uint64_t found = __ballot(before + sum > tile);
+        if (found) {
+            const int at = __builtin_ctzll(found);
+            *expert = first + at;
+            *row0 = __builtin_amdgcn_readlane(a, at) +
+                    (tile - before - __builtin_amdgcn_readlane(sum - n, at)) * size;
+            *row_end = __builtin_amdgcn_readlane(b, at);
+            return;
+        }
+        before += __builtin_amdgcn_readlane(sum, 63);
+    }
+    *expert = *row0 = *row_end = 0;                      // not reached
+}
+
+}  // namespace fqdev

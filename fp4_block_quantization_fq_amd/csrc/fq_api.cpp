@@ -1535,6 +1535,394 @@ fq_status fq_adamw_step_plan(const fq_adamw_hyper *hyper, const void *plan,
 
 }  // extern "C"
 
+// ---- the feed-forward products of a training step ----------------------------
+namespace {
+
+constexpr int64_t kTensorMax = kMaxElems;
+
+fq_status check_act(int32_t act)
+{
+    if (act < FQ_ACT_NONE || act > FQ_ACT_GELU)
+        return fail(FQ_ERR_DESC, "act=%d is not FQ_ACT_NONE/RELU/SILU/GELU", act);
+    return FQ_OK;
+}
+
+fq_status check_gate(const fq_gate *gate, fqimpl::Gate *out)
+{
+    if (!gate) return fail(FQ_ERR_NULL, "gate is NULL");
+    FQ_TRY(check_act(gate->act));
+    if (!std::isfinite(gate->alpha) || (gate->act != FQ_ACT_SILU && gate->alpha != 1.0f))
+        return fail(FQ_ERR_DESC, "gate->alpha must be finite, and 1 unless act is FQ_ACT_SILU");
+    if (!(gate->limit > 0.0f)) return fail(FQ_ERR_DESC, "gate->limit must be > 0");
+    if (!std::isfinite(gate->shift)) return fail(FQ_ERR_DESC, "gate->shift must be finite");
+    *out = {gate->act, gate->alpha, gate->limit, gate->shift};
+    return FQ_OK;
+}
+
+// Sizes of a product: rows, k, and `halves` times n columns, per expert.
+struct Product {
+    int64_t rows, k, n, experts, halves;
+    int64_t cols() const { return n * halves; }
+    int64_t groups() const { return experts ? experts : 1; }
+};
+
+fq_status check_product(const Product &d)
+{
+    if (d.rows < 1 || d.rows > kMaxDim)
+        return fail(FQ_ERR_SHAPE, "rows=%lld must be >= 1 and below 2^31", (long long)d.rows);
+    if (d.k < 8 || d.n < 8 || d.k % 8 || d.n % 8 || d.k > fqimpl::kProductMaxDim ||
+        d.n > fqimpl::kProductMaxDim)
+        return fail(FQ_ERR_SHAPE, "k=%lld and n=%lld must be multiples of 8 from 8 to 2^20",
+                    (long long)d.k, (long long)d.n);
+    if (d.experts < 0 || d.experts > fqimpl::kProductMaxExperts)
+        return fail(FQ_ERR_SHAPE, "experts=%lld must be in [0, %lld]", (long long)d.experts,
+                    (long long)fqimpl::kProductMaxExperts);
+    if (d.rows > kTensorMax / d.k || d.rows > kTensorMax / d.cols() ||
+        d.groups() > kTensorMax / d.k / d.cols())
+        return fail(FQ_ERR_SHAPE,
+                    "rows*k, rows*columns and experts*k*columns must be at most 2^34 (rows=%lld k=%lld "
+                    "columns=%lld experts=%lld)", (long long)d.rows, (long long)d.k,
+                    (long long)d.cols(), (long long)d.experts);
+    return FQ_OK;
+}
+
+fq_status check_offsets(const Product &d, const int32_t *offsets)
+{
+    if ((d.experts > 0) != (offsets != nullptr))
+        return fail(FQ_ERR_NULL, offsets ? "offsets are given without experts"
+                                         : "offsets is NULL with experts");
+    return check_ptr(offsets, "offsets", false, 4);
+}
+
+// the values before the activation: *kind is set to a PRE_*
+fq_status check_pre(const Product &d, const void *pre, int32_t f8, const void *scales, bool required,
+                    int *kind)
+{
+    FQ_TRY(check_ptr(pre, "pre", required));
+    if (f8 != FQ_F8_NONE && f8 != FQ_F8_MX)
+        return fail(FQ_ERR_DESC, "pre_f8=%d is not FQ_F8_NONE/MX", f8);
+    *kind = !pre ? fqimpl::PRE_NONE : f8 == FQ_F8_MX ? fqimpl::PRE_MX : fqimpl::PRE_BF16;
+    const bool mx = *kind == fqimpl::PRE_MX;
+    if (scales && !mx) return fail(FQ_ERR_DESC, "pre_scales belong to a pre in FQ_F8_MX");
+    FQ_TRY(check_ptr(scales, "pre_scales", mx));
+    if (mx && d.n % 32 != 0)
+        return fail(FQ_ERR_SHAPE, "n=%lld must be a multiple of 32 for a pre in 8 bits", (long long)d.n);
+    return FQ_OK;
+}
+
+size_t product_fwd_ws(const Product &) { return 0; }
+
+// Workspace of a backward: dz, x decoded, the tiles' column sums.
+struct ProductBwdLayout {
+    size_t x, partials, total;
+};
+ProductBwdLayout product_bwd_layout(const Product &d, int32_t x_f8)
+{
+    ProductBwdLayout l;
+    l.x = round256((size_t)d.rows * d.cols() * 2);
+    l.partials = l.x + (x_f8 != FQ_F8_NONE ? round256((size_t)d.rows * d.k * 2) : 0);
+    l.total = l.partials + (size_t)fqimpl::dz_tiles(d.rows, d.experts) * d.cols() * sizeof(float);
+    return l;
+}
+
+size_t product_bwd_ws(const Product &d, int32_t x_f8)
+{
+    if (check_product(d) != FQ_OK || check_f8(x_f8) != FQ_OK) return 0;
+    return product_bwd_layout(d, x_f8).total;
+}
+
+fq_status check_ws(const void *ws, size_t ws_bytes, size_t need)
+{
+    if (!need) return FQ_OK;
+    FQ_TRY(check_ptr(ws, "ws", true));
+    if (ws_bytes < need)
+        return fail(FQ_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, need);
+    return FQ_OK;
+}
+
+fqimpl::ProductArgs product_args(const Product &d, const int32_t *offsets)
+{
+    fqimpl::ProductArgs p = {};
+    p.rows = (int)d.rows;
+    p.experts = (int)d.experts;
+    p.offsets = offsets;
+    return p;
+}
+
+// The forward's operands that both products share.
+fq_status product_fwd(fqimpl::ProductArgs *p, const Product &d, const void *x, const void *w,
+                      const void *bias, int32_t bias_type, const int32_t *offsets, void *pre,
+                      int32_t pre_f8, void *pre_scales)
+{
+    FQ_TRY(check_type(bias_type, "bias_type"));
+    FQ_TRY(check_product(d));
+    FQ_TRY(check_ptr(x, "x", true));
+    FQ_TRY(check_ptr(w, "w", true));
+    FQ_TRY(check_ptr(bias, "bias", false));
+    FQ_TRY(check_offsets(d, offsets));
+    *p = product_args(d, offsets);
+    FQ_TRY(check_pre(d, pre, pre_f8, pre_scales, false, &p->pre_kind));
+    p->a = (const uint16_t *)x;
+    p->b = (const uint16_t *)w;
+    p->lda = d.k;
+    p->ldb = d.cols();
+    p->b_stride = d.k * d.cols();
+    p->M = (int)d.rows;
+    p->N = (int)d.n;
+    p->K = (int)d.k;
+    p->bias = bias;
+    p->bias_f32 = bias_type == FQ_TYPE_F32;
+    p->pre = pre;
+    p->pre_scales = pre_scales;
+    return FQ_OK;
+}
+
+struct ProductBwd {
+    const void *dy, *x;
+    int32_t x_f8;
+    const void *x_scales, *w, *pre;
+    int32_t pre_f8;
+    const void *pre_scales;
+    const int32_t *offsets;
+    fqimpl::Gate gate;
+    void *dx, *dw;
+    int32_t dw_type;
+    float *dbias;
+    void *h, *ws;
+    size_t ws_bytes;
+    hipStream_t stream;
+};
+
+fq_status product_bwd(const Product &d, const ProductBwd &a)
+{
+    const bool glu = d.halves == 2, plain = !glu && a.gate.act == FQ_ACT_NONE;
+    FQ_TRY(check_f8(a.x_f8));
+    FQ_TRY(check_type(a.dw_type, "dw_type"));
+    FQ_TRY(check_product(d));
+    if (!a.dx && !a.dw && !a.dbias && !a.h) return fail(FQ_ERR_NULL, "no output is given");
+    FQ_TRY(check_ptr(a.dy, glu ? "dh" : "dy", true));
+    FQ_TRY(check_ptr(a.x, "x", a.dw != nullptr));
+    const bool x8 = a.x && a.x_f8 != FQ_F8_NONE;
+    if (a.x_scales && !x8) return fail(FQ_ERR_DESC, "x_scales belong to an x in 8 bits");
+    FQ_TRY(check_ptr(a.x_scales, "x_scales", x8));
+    if (x8 && d.k % 32 != 0)
+        return fail(FQ_ERR_SHAPE, "k=%lld must be a multiple of 32 for an x in 8 bits", (long long)d.k);
+    FQ_TRY(check_ptr(a.w, "w", a.dx != nullptr));
+    FQ_TRY(check_offsets(d, a.offsets));
+    int pre_kind;
+    FQ_TRY(check_pre(d, a.pre, a.pre_f8, a.pre_scales, !plain, &pre_kind));
+    FQ_TRY(check_ptr(a.dx, "dx", false));
+    FQ_TRY(check_ptr(a.dw, "dw", false));
+    FQ_TRY(check_ptr(a.dbias, "dbias", false));
+    FQ_TRY(check_ptr(a.h, "h", false));
+    const ProductBwdLayout l = product_bwd_layout(d, a.x_f8);
+    FQ_TRY(check_ws(a.ws, a.ws_bytes, l.total));
+
+    uint8_t *ws = (uint8_t *)a.ws;
+    const void *dz = plain ? a.dy : a.ws;
+    if (!plain || a.dbias) {
+        fqimpl::DzArgs z = {};
+        z.glu = glu;
+        z.dy = a.dy;
+        z.pre = plain ? nullptr : a.pre;
+        z.pre_scales = a.pre_scales;
+        z.pre_kind = pre_kind;
+        z.gate = a.gate;
+        z.rows = d.rows;
+        z.n = d.n;
+        z.experts = (int)d.experts;
+        z.offsets = a.offsets;
+        z.dz = ws;
+        z.h = a.h;
+        z.partials = a.dbias ? (float *)(ws + l.partials) : nullptr;
+        z.dbias = a.dbias;
+        const hipError_t e = fqimpl::launch_dz(z, a.stream);
+        if (e != hipSuccess) return device_status(e, "gradient before the activation launch");
+    }
+    if (a.dx) {
+        fqimpl::ProductArgs p = product_args(d, a.offsets);
+        p.a = (const uint16_t *)dz;
+        p.b = (const uint16_t *)a.w;
+        p.lda = p.ldb = d.cols();
+        p.b_stride = d.k * d.cols();
+        p.M = (int)d.rows;
+        p.N = (int)d.k;
+        p.K = (int)d.cols();
+        p.y = a.dx;
+        const hipError_t e = fqimpl::launch_product_dx(p, a.stream);
+        if (e != hipSuccess) return device_status(e, "dx product launch");
+    }
+    if (a.dw) {
+        const void *x = a.x;
+        if (x8) {
+            fqimpl::RowArgs8 r = {};
+            r.codes = const_cast<void *>(a.x);
+            r.scales = const_cast<void *>(a.x_scales);
+            r.y = ws + l.x;
+            r.rows = d.rows;
+            r.cols = d.k;
+            const hipError_t e = fqimpl::launch_f8_decode(a.x_f8, r, a.stream);
+            if (e != hipSuccess) return device_status(e, "decode launch");
+            x = r.y;
+        }
+        fqimpl::ProductArgs p = product_args(d, a.offsets);
+        p.a = (const uint16_t *)x;
+        p.b = (const uint16_t *)dz;
+        p.lda = d.k;
+        p.ldb = d.cols();
+        p.M = (int)d.k;
+        p.N = (int)d.cols();
+        p.K = (int)d.rows;
+        p.y = a.dw;
+        p.y_f32 = a.dw_type == FQ_TYPE_F32;
+        const hipError_t e = fqimpl::launch_product_dw(p, a.stream);
+        if (e != hipSuccess) return device_status(e, "dw product launch");
+    }
+    return ok();
+}
+
+fq_status check_f8_rows(int32_t f8, int64_t rows, int64_t cols)
+{
+    FQ_TRY(check_f8(f8));
+    if (f8 == FQ_F8_NONE) return fail(FQ_ERR_DESC, "f8 must be FQ_F8_MX or FQ_F8_ROW");
+    if (rows < 1 || cols < 32 || cols % 32 != 0)
+        return fail(FQ_ERR_SHAPE, "rows=%lld must be >= 1, cols=%lld a positive multiple of 32",
+                    (long long)rows, (long long)cols);
+    if (rows > kMaxDim || cols > kMaxDim || rows > kMaxElems / cols)
+        return fail(FQ_ERR_SHAPE, "rows=%lld cols=%lld: each must be below 2^31 and rows*cols at most 2^34",
+                    (long long)rows, (long long)cols);
+    return FQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fq_status fq_f8_encode(const void *x_bf16, int32_t f8, int64_t rows, int64_t cols, void *codes,
+                       void *scales, void *stream)
+{
+    FQ_TRY(check_f8_rows(f8, rows, cols));
+    if (f8 == FQ_F8_ROW && cols > fqimpl::kF8RowMaxCols)
+        return fail(FQ_ERR_SHAPE, "cols=%lld must be at most %lld for FQ_F8_ROW", (long long)cols,
+                    (long long)fqimpl::kF8RowMaxCols);
+    FQ_TRY(check_ptr(x_bf16, "x", true));
+    FQ_TRY(check_ptr(codes, "codes", true));
+    FQ_TRY(check_ptr(scales, "scales", true));
+    fqimpl::RowArgs8 a = {};
+    a.x = x_bf16;
+    a.codes = codes;
+    a.scales = scales;
+    a.rows = rows;
+    a.cols = cols;
+    return device_status(fqimpl::launch_f8_encode(f8, a, (hipStream_t)stream), "encode launch");
+}
+
+fq_status fq_f8_decode(const void *codes, const void *scales, int32_t f8, int64_t rows,
+                       int64_t cols, void *y_bf16, void *stream)
+{
+    FQ_TRY(check_f8_rows(f8, rows, cols));
+    FQ_TRY(check_ptr(codes, "codes", true));
+    FQ_TRY(check_ptr(scales, "scales", true));
+    FQ_TRY(check_ptr(y_bf16, "y", true));
+    fqimpl::RowArgs8 a = {};
+    a.codes = const_cast<void *>(codes);
+    a.scales = const_cast<void *>(scales);
+    a.y = y_bf16;
+    a.rows = rows;
+    a.cols = cols;
+    return device_status(fqimpl::launch_f8_decode(f8, a, (hipStream_t)stream), "decode launch");
+}
+
+size_t fq_linear_fwd_workspace_size(int64_t rows, int64_t k, int64_t n, int64_t experts)
+{
+    const Product d = {rows, k, n, experts, 1};
+    return check_product(d) == FQ_OK ? product_fwd_ws(d) : 0;
+}
+
+fq_status fq_linear_fwd(const void *x_bf16, const void *w_bf16, const void *bias,
+                        int32_t bias_type, const void *res, int64_t rows, int64_t k, int64_t n,
+                        int64_t experts, const int32_t *offsets, int32_t act, void *pre,
+                        int32_t pre_f8, void *pre_scales, void *y, int32_t y_type, void *ws,
+                        size_t ws_bytes, void *stream)
+{
+    const Product d = {rows, k, n, experts, 1};
+    fqimpl::ProductArgs p;
+    FQ_TRY(check_act(act));
+    FQ_TRY(check_type(y_type, "y_type"));
+    FQ_TRY(product_fwd(&p, d, x_bf16, w_bf16, bias, bias_type, offsets, pre, pre_f8, pre_scales));
+    FQ_TRY(check_ptr(res, "res", false));
+    FQ_TRY(check_ptr(y, "y", true));
+    FQ_TRY(check_ws(ws, ws_bytes, product_fwd_ws(d)));
+    p.act = act;
+    p.res = res;
+    p.y = y;
+    p.y_f32 = y_type == FQ_TYPE_F32;
+    return device_status(fqimpl::launch_product_linear(p, (hipStream_t)stream), "linear launch");
+}
+
+size_t fq_linear_bwd_workspace_size(int64_t rows, int64_t k, int64_t n, int64_t experts,
+                                    int32_t x_f8)
+{
+    return product_bwd_ws({rows, k, n, experts, 1}, x_f8);
+}
+
+fq_status fq_linear_bwd(const void *dy_bf16, const void *x, int32_t x_f8, const void *x_scales,
+                        const void *w_bf16, const void *pre, int32_t pre_f8,
+                        const void *pre_scales, int64_t rows, int64_t k, int64_t n,
+                        int64_t experts, const int32_t *offsets, int32_t act, void *dx_bf16,
+                        void *dw, int32_t dw_type, float *dbias, void *ws, size_t ws_bytes,
+                        void *stream)
+{
+    FQ_TRY(check_act(act));
+    return product_bwd({rows, k, n, experts, 1},
+                       {dy_bf16, x, x_f8, x_scales, w_bf16, pre, pre_f8, pre_scales, offsets,
+                        {act, 1.0f, INFINITY, 0.0f}, dx_bf16, dw, dw_type, dbias, nullptr, ws,
+                        ws_bytes, (hipStream_t)stream});
+}
+
+size_t fq_glu_fwd_workspace_size(int64_t rows, int64_t k, int64_t n, int64_t experts)
+{
+    const Product d = {rows, k, n, experts, 2};
+    return check_product(d) == FQ_OK ? product_fwd_ws(d) : 0;
+}
+
+fq_status fq_glu_fwd(const fq_gate *gate, const void *x_bf16, const void *w_bf16,
+                     const void *bias, int32_t bias_type, int64_t rows, int64_t k, int64_t n,
+                     int64_t experts, const int32_t *offsets, void *pre, int32_t pre_f8,
+                     void *pre_scales, void *h_bf16, void *ws, size_t ws_bytes, void *stream)
+{
+    const Product d = {rows, k, n, experts, 2};
+    fqimpl::ProductArgs p;
+    fqimpl::Gate g;
+    FQ_TRY(check_gate(gate, &g));
+    FQ_TRY(product_fwd(&p, d, x_bf16, w_bf16, bias, bias_type, offsets, pre, pre_f8, pre_scales));
+    FQ_TRY(check_ptr(h_bf16, "h", true));
+    FQ_TRY(check_ws(ws, ws_bytes, product_fwd_ws(d)));
+    p.gate = g;
+    p.y = h_bf16;
+    return device_status(fqimpl::launch_product_glu(p, (hipStream_t)stream), "gated block launch");
+}
+
+size_t fq_glu_bwd_workspace_size(int64_t rows, int64_t k, int64_t n, int64_t experts, int32_t x_f8)
+{
+    return product_bwd_ws({rows, k, n, experts, 2}, x_f8);
+}
+
+fq_status fq_glu_bwd(const fq_gate *gate, const void *dh_bf16, const void *x, int32_t x_f8,
+                     const void *x_scales, const void *w_bf16, const void *pre, int32_t pre_f8,
+                     const void *pre_scales, int64_t rows, int64_t k, int64_t n, int64_t experts,
+                     const int32_t *offsets, void *dx_bf16, void *dw, int32_t dw_type,
+                     float *dbias, void *h_bf16, void *ws, size_t ws_bytes, void *stream)
+{
+    fqimpl::Gate g;
+    FQ_TRY(check_gate(gate, &g));
+    return product_bwd({rows, k, n, experts, 2},
+                       {dh_bf16, x, x_f8, x_scales, w_bf16, pre, pre_f8, pre_scales, offsets, g,
+                        dx_bf16, dw, dw_type, dbias, h_bf16, ws, ws_bytes, (hipStream_t)stream});
+}
+
+}  // extern "C"
+
 extern "C" {
 
 const char *fq_status_string(fq_status s)

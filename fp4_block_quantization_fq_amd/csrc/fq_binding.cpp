@@ -22,6 +22,7 @@ using at::ScalarType;
 PyObject *g_raw_stream = nullptr;     // torch._C._cuda_getCurrentRawStream
 PyObject *g_device = nullptr;         // torch._C._cuda_getDevice
 PyObject *g_cuda_stream = nullptr;    // "cuda_stream"
+PyObject *g_device_index = nullptr;   // "device_index"
 
 const char *type_name(ScalarType t)
 {
@@ -33,6 +34,8 @@ const char *type_name(ScalarType t)
 struct Call {
     PyObject *const *args;
     bool ok = true;
+    int device = -1;          // of the first GPU operand
+    bool several = false;     // a later one is on another
 
     Call(PyObject *const *a, Py_ssize_t n, Py_ssize_t want) : args(a)
     {
@@ -90,9 +93,23 @@ struct Call {
         } else if (t.numel() < n) {
             refuse("%s%s holds %lld elements, %lld are needed", name, "", t.numel(), n);
         } else {
+            if (device < 0) device = t.get_device();
+            else if (device != t.get_device()) several = true;
             return t.data_ptr();
         }
         return nullptr;
+    }
+    // All operands lie on the device whose stream the kernels go to: `i` as for stream().
+    void one_device(int i)
+    {
+        if (!ok) return;
+        PyObject *v = args[i] == Py_None ? PyObject_CallNoArgs(g_device) : PyObject_GetAttr(args[i], g_device_index);
+        const long at = v ? PyLong_AsLong(v) : -1;
+        Py_XDECREF(v);
+        if (PyErr_Occurred()) ok = false;
+        else if (several) refuse("the operands are on several devices%s%s", "");
+        else if (device >= 0 && device != at)
+            refuse("the operands are on device %s%s%lld, the stream is of device %lld", "", "", device, at);
     }
     // Operand of one type, `n` elements at least.
     void *typed(int i, ScalarType type, long long n, const char *name)
@@ -346,6 +363,209 @@ PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t nargs)
     return launch(c, [&] { return fq_adamw_step_plan(&h, plan, plan_device, st); });
 }
 
+// ---- feed-forward products -------------------------------------------------------
+
+// rows and k of x, columns of w [k, columns], or [experts, k, columns] with offsets
+struct Sizes {
+    long long rows = 0, k = 0, cols = 0, experts = 0;
+    const void *w = nullptr;
+    const int32_t *offsets = nullptr;
+    Sizes(Call &c, int x, int w_at, int offsets_at)
+    {
+        if (!c.shape(x, "x", &rows, &k)) return;
+        const at::Tensor *t = c.tensor(w_at, "w"), *o = c.tensor(offsets_at, "offsets");
+        if (!c.ok) return;
+        if (!t || t->dim() != (o ? 3 : 2)) {
+            c.refuse("w must be %s%s", o ? "[experts, k, columns]" : "[k, columns]");
+            return;
+        }
+        cols = t->size(-1);
+        if (t->size(-2) != k) {
+            c.refuse("x has %s%s%lld columns, w %lld rows", "", "", k, t->size(-2));
+            return;
+        }
+        if (o) {
+            experts = t->size(0);
+            if (experts < 1) c.refuse("w must have an expert at least%s%s", "");
+            offsets = (const int32_t *)c.typed(offsets_at, at::kInt, experts + 1, "offsets");
+            if (c.ok && o->numel() != experts + 1)
+                c.refuse("%s%s hold %lld entries, %lld are needed", "offsets", "", o->numel(), experts + 1);
+        }
+        w = c.typed(w_at, at::kBFloat16, (experts ? experts : 1) * k * cols, "w");
+    }
+    long long groups() const { return experts ? experts : 1; }
+};
+
+void *pre_of(Call &c, int i, int f8, long long n)
+{
+    return f8 == FQ_F8_NONE ? c.typed(i, at::kBFloat16, n, "pre") : c.bytes(i, n, "pre");
+}
+
+// a BF16 or FP32 bias or none
+const void *bias_of(Call &c, int i, const Sizes &s, int32_t *type)
+{
+    return c.real(i, s.groups() * s.cols, "bias", type);
+}
+
+// (x, f8, codes, scales, stream)
+PyObject *f8_encode(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    Call c(args, nargs, 5);
+    long long rows = 0, cols = 0;
+    if (!c.ok || !c.shape(0, "x", &rows, &cols)) return nullptr;
+    const int f8 = (int)c.i64(1);
+    const void *x = c.typed(0, at::kBFloat16, rows * cols, "x");
+    void *codes = c.bytes(2, rows * cols, "codes");
+    void *scales = c.scales8(3, f8, rows, cols);
+    c.one_device(4);
+    void *st = c.stream(4);
+    return launch(c, [&] { return fq_f8_encode(x, f8, rows, cols, codes, scales, st); });
+}
+
+// (codes, scales, f8, y, stream)
+PyObject *f8_decode(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    Call c(args, nargs, 5);
+    long long rows = 0, cols = 0;
+    if (!c.ok || !c.shape(0, "codes", &rows, &cols)) return nullptr;
+    const int f8 = (int)c.i64(2);
+    const void *codes = c.bytes(0, rows * cols, "codes");
+    const void *scales = c.scales8(1, f8, rows, cols);
+    void *y = c.typed(3, at::kBFloat16, rows * cols, "y");
+    c.one_device(4);
+    void *st = c.stream(4);
+    return launch(c, [&] { return fq_f8_decode(codes, scales, f8, rows, cols, y, st); });
+}
+
+// (x, w, bias, res, offsets, act, pre, pre_f8, pre_scales, y, ws, stream)
+PyObject *linear_fwd(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    Call c(args, nargs, 12);
+    if (!c.ok) return nullptr;
+    const Sizes s(c, 0, 1, 4);
+    const long long n = s.rows * s.cols;
+    int32_t bias_type = FQ_TYPE_F32, y_type = FQ_TYPE_BF16;
+    const void *x = c.typed(0, at::kBFloat16, s.rows * s.k, "x");
+    const void *bias = bias_of(c, 2, s, &bias_type);
+    void *y = c.real(9, n, "y", &y_type);
+    const void *res = c.typed(3, y_type == FQ_TYPE_F32 ? at::kFloat : at::kBFloat16, n, "res");
+    const int act = (int)c.i64(5), pre_f8 = (int)c.i64(7);
+    void *pre = pre_of(c, 6, pre_f8, n);
+    void *pre_scales = c.bytes(8, n / 32, "pre_scales");
+    size_t ws_bytes = 0;
+    void *ws = c.workspace(10, &ws_bytes);
+    c.one_device(11);
+    void *st = c.stream(11);
+    return launch(c, [&] {
+        return fq_linear_fwd(x, s.w, bias, bias_type, res, s.rows, s.k, s.cols, s.experts,
+                             s.offsets, act, pre, pre_f8, pre_scales, y, y_type, ws, ws_bytes, st);
+    });
+}
+
+// What both backward calls take, from argument 0: dy, x, w, pre, x_f8, x_scales,
+// pre_f8, pre_scales, offsets, dx, dw, dbias, ws
+struct Bwd {
+    const Sizes s;
+    int halves;
+    long long n;
+    const void *dy, *x, *x_scales, *pre, *pre_scales;
+    int x_f8, pre_f8;
+    void *dx, *dw, *ws;
+    float *dbias;
+    int32_t dw_type = FQ_TYPE_BF16;
+    size_t ws_bytes = 0;
+    Bwd(Call &c, int halves, const char *dy_name) : s(c, 1, 2, 8), halves(halves), n(s.cols / halves)
+    {
+        if (c.ok && s.cols % halves)
+            c.refuse("w has %s%s%lld columns, an even number is needed", "", "", s.cols);
+        long long rows = 0, cols = 0;
+        if (c.ok && c.shape(0, dy_name, &rows, &cols) && (rows != s.rows || cols != n))
+            c.refuse("%s must have x's rows and w's columns%s", dy_name);
+        const long long all = s.rows * s.cols;
+        dy = c.typed(0, at::kBFloat16, s.rows * n, dy_name);
+        x_f8 = (int)c.i64(4);
+        x = x_f8 == FQ_F8_NONE ? c.typed(1, at::kBFloat16, s.rows * s.k, "x") : c.bytes(1, s.rows * s.k, "x");
+        x_scales = c.scales8(5, x_f8, s.rows, s.k);
+        pre_f8 = (int)c.i64(6);
+        pre = pre_of(c, 3, pre_f8, all);
+        pre_scales = c.bytes(7, all / 32, "pre_scales");
+        dx = c.typed(9, at::kBFloat16, s.rows * s.k, "dx");
+        dw = c.real(10, s.groups() * s.k * s.cols, "dw", &dw_type);
+        dbias = (float *)c.typed(11, at::kFloat, s.groups() * s.cols, "dbias");
+        ws = c.workspace(12, &ws_bytes);
+    }
+};
+
+// (the above, act, stream)
+PyObject *linear_bwd(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    Call c(args, nargs, 15);
+    if (!c.ok) return nullptr;
+    const Bwd b(c, 1, "dy");
+    const int act = (int)c.i64(13);
+    c.one_device(14);
+    void *st = c.stream(14);
+    return launch(c, [&] {
+        return fq_linear_bwd(b.dy, b.x, b.x_f8, b.x_scales, b.s.w, b.pre, b.pre_f8, b.pre_scales,
+                             b.s.rows, b.s.k, b.n, b.s.experts, b.s.offsets, act, b.dx, b.dw,
+                             b.dw_type, b.dbias, b.ws, b.ws_bytes, st);
+    });
+}
+
+// act, alpha, limit, shift from argument i
+fq_gate gate_of(Call &c, int i)
+{
+    fq_gate g;
+    g.act = (int32_t)c.i64(i);
+    g.alpha = (float)c.f64(i + 1);
+    g.limit = (float)c.f64(i + 2);
+    g.shift = (float)c.f64(i + 3);
+    return g;
+}
+
+// (x, w, bias, offsets, act, alpha, limit, shift, pre, pre_f8, pre_scales, h, ws, stream)
+PyObject *glu_fwd(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    Call c(args, nargs, 14);
+    if (!c.ok) return nullptr;
+    const Sizes s(c, 0, 1, 3);
+    if (c.ok && s.cols % 2) c.refuse("w has %s%s%lld columns, an even number is needed", "", "", s.cols);
+    const long long n = s.cols / 2, all = s.rows * s.cols;
+    int32_t bias_type = FQ_TYPE_F32;
+    const void *x = c.typed(0, at::kBFloat16, s.rows * s.k, "x");
+    const void *bias = bias_of(c, 2, s, &bias_type);
+    const fq_gate gate = gate_of(c, 4);
+    const int pre_f8 = (int)c.i64(9);
+    void *pre = pre_of(c, 8, pre_f8, all);
+    void *pre_scales = c.bytes(10, all / 32, "pre_scales");
+    void *h = c.typed(11, at::kBFloat16, s.rows * n, "h");
+    size_t ws_bytes = 0;
+    void *ws = c.workspace(12, &ws_bytes);
+    c.one_device(13);
+    void *st = c.stream(13);
+    return launch(c, [&] {
+        return fq_glu_fwd(&gate, x, s.w, bias, bias_type, s.rows, s.k, n, s.experts, s.offsets, pre,
+                          pre_f8, pre_scales, h, ws, ws_bytes, st);
+    });
+}
+
+// (as linear_bwd's first 13, act, alpha, limit, shift, h, stream)
+PyObject *glu_bwd(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    Call c(args, nargs, 19);
+    if (!c.ok) return nullptr;
+    const Bwd b(c, 2, "dh");
+    const fq_gate gate = gate_of(c, 13);
+    void *h = c.typed(17, at::kBFloat16, b.s.rows * b.n, "h");
+    c.one_device(18);
+    void *st = c.stream(18);
+    return launch(c, [&] {
+        return fq_glu_bwd(&gate, b.dy, b.x, b.x_f8, b.x_scales, b.s.w, b.pre, b.pre_f8,
+                          b.pre_scales, b.s.rows, b.s.k, b.n, b.s.experts, b.s.offsets, b.dx, b.dw,
+                          b.dw_type, b.dbias, h, b.ws, b.ws_bytes, st);
+    });
+}
+
 // A tensor without storage or strides throws where it is asked for them: that
 // becomes a Python exception, and nothing is launched.
 template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
@@ -365,7 +585,9 @@ PyObject *guarded(PyObject *self, PyObject *const *args, Py_ssize_t nargs)
 PyMethodDef kMethods[] = {
     FQ_METHOD(rmsnorm_fwd),  FQ_METHOD(rmsnorm_bwd),     FQ_METHOD(moe_sort),
     FQ_METHOD(moe_dispatch), FQ_METHOD(moe_combine),     FQ_METHOD(moe_combine_bwd),
-    FQ_METHOD(adamw_step),   {nullptr, nullptr, 0, nullptr},
+    FQ_METHOD(adamw_step),   FQ_METHOD(f8_encode),       FQ_METHOD(f8_decode),
+    FQ_METHOD(linear_fwd),   FQ_METHOD(linear_bwd),      FQ_METHOD(glu_fwd),
+    FQ_METHOD(glu_bwd),      {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fq_binding", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
@@ -379,7 +601,8 @@ PyMODINIT_FUNC PyInit__fq_binding()
     g_raw_stream = PyObject_GetAttrString(torch_c, "_cuda_getCurrentRawStream");
     g_device = PyObject_GetAttrString(torch_c, "_cuda_getDevice");
     g_cuda_stream = PyUnicode_InternFromString("cuda_stream");
+    g_device_index = PyUnicode_InternFromString("device_index");
     Py_DECREF(torch_c);
-    if (!g_raw_stream || !g_device || !g_cuda_stream) return nullptr;
+    if (!g_raw_stream || !g_device || !g_cuda_stream || !g_device_index) return nullptr;
     return PyModule_Create(&kModule);
 }

@@ -1,0 +1,274 @@
+// fq_checkpoint.hip -- activations kept in 8 bits between the forward and the
+// backward, and what the backward of the feed-forward products computes from
+// them element by element: the gradient before the activation, the block's
+// output once more, and the bias gradient's column sums.
+//
+// All of it is bound by memory: 16 bytes of BF16 (8 of codes) a lane and access,
+// one pass over the data.  Column sums are FP32 in a fixed order: rows of a lane,
+// lanes of a workgroup, then the tiles of an expert by a second kernel.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fq_internal.h"
+#include "fq_act.hpp"
+
+namespace {
+
+using namespace fqdev;
+using fqimpl::RowArgs8;
+using fqimpl::DzArgs;
+
+constexpr int kBlock = 256;
+
+// ---- 8-bit rows --------------------------------------------------------------------
+// MX blocks know nothing of rows: chunk after chunk of eight elements.
+__global__ __launch_bounds__(kBlock) void k_encode_mx(RowArgs8 a, int64_t chunks)
+{
+    const int64_t step = (int64_t)gridDim.x * kBlock;
+    for (int64_t c = (int64_t)blockIdx.x * kBlock + threadIdx.x; c < chunks; c += step) {
+        float v[8];
+        load8<false>((const uint16_t *)a.x + c * 8, 8, v);
+        u32w2 codes;
+        const uint32_t scale = mx8_encode8(v, &codes);
+        ((u32w2 *)a.codes)[c] = codes;
+        if ((c & 3) == 0) ((uint8_t *)a.scales)[c >> 2] = (uint8_t)scale;
+    }
+}
+
+// FP32 scale per row: LANES lanes hold a row of at most LANES * NCH chunks.
+template <int LANES, int NCH>
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void k_encode_row(RowArgs8 a)
+{
+    constexpr int THREADS = LANES < 256 ? 256 : LANES, WAVES = LANES / 64;
+    __shared__ uint32_t tops[WAVES > 0 ? WAVES : 1];
+    const int l = threadIdx.x % LANES;
+    const int64_t row = (int64_t)blockIdx.x * (THREADS / LANES) + threadIdx.x / LANES;
+    if (LANES <= 64 && row >= a.rows) return;
+    const uint16_t *x = (const uint16_t *)a.x + row * a.cols;
+    Raw8<uint16_t> raw[NCH];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        raw[i].w = (u32w4){0, 0, 0, 0};
+        const int at = (i * LANES + l) * 8;
+        if (at < a.cols) load_raw8<false>(x + at, 8, raw[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        float v[8];
+        unpack8(raw[i], v);
+        top = max(top, absmax(v));
+    }
+    top = lanes_max<(LANES < 64 ? LANES : 64)>(top);
+    if (WAVES > 1) {
+        if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) top = max(top, tops[i]);
+    }
+    const bool bad = top >= 0x7F800000u;
+    const float s = __builtin_fmaxf(as_f(top) * (1.0f / 448.0f), as_f(0x00800000u));
+    const float inv = 1.0f / s;
+    if (l == 0) ((float *)a.scales)[row] = bad ? as_f(0x7FC00000u) : s;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        const int at = (i * LANES + l) * 8;
+        if (at >= a.cols) continue;
+        float v[8];
+        unpack8(raw[i], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __builtin_fminf(__builtin_fmaxf(v[e] * inv, -448.0f), 448.0f);
+        *(u32w2 *)((uint8_t *)a.codes + row * a.cols + at) = bad ? (u32w2){0x7F7F7F7Fu, 0x7F7F7F7Fu} : e4m3_encode8(v);
+    }
+}
+
+template <bool ROW>
+__global__ __launch_bounds__(kBlock) void k_decode(RowArgs8 a, int64_t chunks)
+{
+    const int64_t step = (int64_t)gridDim.x * kBlock;
+    const uint32_t per_row = (uint32_t)(a.cols / 8);
+    for (int64_t c = (int64_t)blockIdx.x * kBlock + threadIdx.x; c < chunks; c += step) {
+        const u32w2 codes = ((const u32w2 *)a.codes)[c];
+        const float s = ROW ? ((const float *)a.scales)[(uint32_t)c / per_row]      // chunks are below 2^31
+                            : mx8_scale(((const uint8_t *)a.scales)[c >> 2]);
+        float v[8];
+        e4m3_decode8(codes, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= s;
+        store8<false>((uint16_t *)a.y + c * 8, 8, v);
+    }
+}
+
+// ---- gradient before the activation ----------------------------------------------------
+// A workgroup: kDzRows rows of a segment, 256 columns of the output (32 lanes of
+// eight columns, eight rows at a time).
+constexpr int kDzRows = fqimpl::kDzRows;
+
+template <bool MX>
+__device__ __forceinline__ void load_pre(const DzArgs &a, int64_t at, float (&v)[8])
+{
+    if (!MX) {
+        load8<false>((const uint16_t *)a.pre + at, 8, v);
+        return;
+    }
+    const float s = mx8_scale(((const uint8_t *)a.pre_scales)[at >> 5]);
+    e4m3_decode8(*(const u32w2 *)((const uint8_t *)a.pre + at), v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= s;
+}
+
+// GLU: two halves of pre and dz; else pre may be missing (no activation), then
+// only the column sums are made.
+template <bool GLU, bool MX>
+__global__ __launch_bounds__(kBlock) void k_dz(DzArgs a)
+{
+    __shared__ float sums[GLU ? 2 : 1][8][256 + 8];
+    const int lane = threadIdx.x & 63;
+    const int tile = blockIdx.x;
+    int row0 = tile * kDzRows, row_end = (int)a.rows, expert;
+    if (a.offsets) {
+        if (tile >= segment_tiles(a.offsets, a.experts, (int)a.rows, kDzRows, lane)) return;
+        find_segment(a.offsets, a.experts, (int)a.rows, kDzRows, tile, lane, &expert, &row0, &row_end);
+    }
+    row_end = row_end - row0 < kDzRows ? row_end : row0 + kDzRows;
+    const int c = threadIdx.x & 31, r0 = threadIdx.x >> 5;
+    const int64_t col = (int64_t)blockIdx.y * 256 + c * 8;
+    const int64_t cols = GLU ? 2 * a.n : a.n;
+    float s0[8] = {}, s1[8] = {};
+    if (col < a.n) {
+        for (int64_t r = row0 + r0; r < row_end; r += 8) {
+            float d[8], g[8], u[8];
+            load8<false>((const uint16_t *)a.dy + r * a.n + col, 8, d);
+            const int64_t at = r * cols + col;
+            if (GLU) {
+                load_pre<MX>(a, at, g);
+                load_pre<MX>(a, at + a.n, u);
+                glu8_grad(a.gate, g, u, d);
+                store8<false>((uint16_t *)a.dz + at, 8, g);
+                store8<false>((uint16_t *)a.dz + at + a.n, 8, u);
+                if (a.h) store8<false>((uint16_t *)a.h + r * a.n + col, 8, d);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    s0[e] += g[e];
+                    s1[e] += u[e];
+                }
+            } else {
+                if (a.pre) {
+                    load_pre<MX>(a, at, g);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float value;
+                        d[e] *= act1_grad(a.gate.act, 1.0f, g[e], &value);
+                    }
+                    store8<false>((uint16_t *)a.dz + at, 8, d);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s0[e] += d[e];
+            }
+        }
+    }
+    if (!a.partials) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        sums[0][r0][c * 8 + e] = s0[e];
+        if (GLU) sums[GLU ? 1 : 0][r0][c * 8 + e] = s1[e];
+    }
+    __syncthreads();
+    const int64_t to = (int64_t)blockIdx.y * 256 + threadIdx.x;
+    if (to >= a.n) return;
+#pragma unroll
+    for (int half = 0; half < (GLU ? 2 : 1); ++half) {
+        float t = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) t += sums[half][r][threadIdx.x];
+        a.partials[(int64_t)tile * cols + half * a.n + to] = t;
+    }
+}
+
+// dbias of one expert and 64 columns: its tiles' sums, four lanes' quarters of them.
+__global__ __launch_bounds__(kBlock) void k_dbias(DzArgs a, int64_t cols)
+{
+    __shared__ float part[4][64];
+    const int lane = threadIdx.x & 63, quarter = threadIdx.x >> 6, expert = blockIdx.y;
+    int first = 0, count = (int)((a.rows + kDzRows - 1) / kDzRows);
+    if (a.offsets) {
+        int s, e;
+        first = segment_tiles(a.offsets, expert, (int)a.rows, kDzRows, lane);
+        segment_of(a.offsets, expert, (int)a.rows, &s, &e);
+        count = (e - s + kDzRows - 1) / kDzRows;
+    }
+    const int64_t col = (int64_t)blockIdx.x * 64 + lane;
+    const int each = (count + 3) / 4, from = min(quarter * each, count), to = min(from + each, count);
+    float t = 0.0f;
+    if (col < cols)
+        for (int i = from; i < to; ++i) t += a.partials[(int64_t)(first + i) * cols + col];
+    part[quarter][lane] = t;
+    __syncthreads();
+    if (quarter == 0 && col < cols)
+        a.dbias[expert * cols + col] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+}
+
+uint32_t flat_grid(int64_t chunks)
+{
+    const int64_t n = (chunks + kBlock - 1) / kBlock;
+    return (uint32_t)(n < 65536 ? n : 65536);
+}
+
+}  // namespace
+
+namespace fqimpl {
+
+hipError_t launch_f8_encode(int f8, const RowArgs8 &a, hipStream_t stream)
+{
+    const int64_t chunks = a.rows * a.cols / 8;
+    if (f8 == F8_MX) {
+        hipLaunchKernelGGL(k_encode_mx, dim3(flat_grid(chunks)), dim3(kBlock), 0, stream, a, chunks);
+        return hipGetLastError();
+    }
+    const int64_t need = a.cols / 8;         // chunks of a row
+#define FQ_ENCODE_ROW(LANES, NCH)                                                                        \
+    hipLaunchKernelGGL((k_encode_row<LANES, NCH>),                                                       \
+                       dim3((uint32_t)(LANES < 256 ? (a.rows + 256 / LANES - 1) / (256 / LANES) : a.rows)), \
+                       dim3(LANES < 256 ? 256 : LANES), 0, stream, a)
+    if (need <= 16) FQ_ENCODE_ROW(16, 1);
+    else if (need <= 64) FQ_ENCODE_ROW(64, 1);
+    else if (need <= 256) FQ_ENCODE_ROW(256, 1);
+    else if (need <= 512) FQ_ENCODE_ROW(256, 2);
+    else if (need <= 1024) FQ_ENCODE_ROW(512, 2);
+    else FQ_ENCODE_ROW(1024, 4);
+#undef FQ_ENCODE_ROW
+    return hipGetLastError();
+}
+
+hipError_t launch_f8_decode(int f8, const RowArgs8 &a, hipStream_t stream)
+{
+    const int64_t chunks = a.rows * a.cols / 8;
+    if (f8 == F8_MX)
+        hipLaunchKernelGGL((k_decode<false>), dim3(flat_grid(chunks)), dim3(kBlock), 0, stream, a, chunks);
+    else
+        hipLaunchKernelGGL((k_decode<true>), dim3(flat_grid(chunks)), dim3(kBlock), 0, stream, a, chunks);
+    return hipGetLastError();
+}
+
+int64_t dz_tiles(int64_t rows, int64_t experts)
+{
+    if (!experts) return (rows + kDzRows - 1) / kDzRows;
+    return rows / kDzRows + (experts < rows ? experts : rows);
+}
+
+hipError_t launch_dz(const DzArgs &a, hipStream_t stream)
+{
+    const dim3 grid((uint32_t)dz_tiles(a.rows, a.offsets ? a.experts : 0), (uint32_t)((a.n + 255) / 256));
+    const int64_t cols = a.glu ? 2 * a.n : a.n;
+    if (a.glu && a.pre_kind == PRE_MX) hipLaunchKernelGGL((k_dz<true, true>), grid, dim3(kBlock), 0, stream, a);
+    else if (a.glu) hipLaunchKernelGGL((k_dz<true, false>), grid, dim3(kBlock), 0, stream, a);
+    else if (a.pre_kind == PRE_MX) hipLaunchKernelGGL((k_dz<false, true>), grid, dim3(kBlock), 0, stream, a);
+    else hipLaunchKernelGGL((k_dz<false, false>), grid, dim3(kBlock), 0, stream, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.dbias) return e;
+    const dim3 joins((uint32_t)((cols + 63) / 64), (uint32_t)(a.offsets ? a.experts : 1));
+    hipLaunchKernelGGL(k_dbias, joins, dim3(kBlock), 0, stream, a, cols);
+    return hipGetLastError();
+}
+
+}  // namespace fqimpl

@@ -236,4 +236,70 @@ hipError_t launch_adamw(const AdamWArgs &a, bool f8, hipStream_t stream);
 hipError_t launch_adamw_plan(const AdamWStep &a, const AdamWTensor *t, const uint32_t *first,
                              const uint32_t *index, bool f8, hipStream_t stream);
 
+// ---- feed-forward products ----------------------------------------------------
+enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };     // FQ_ACT_* of fq.h
+enum { PRE_NONE = 0, PRE_BF16 = 1, PRE_MX = 2 };
+constexpr int64_t kProductMaxDim = int64_t(1) << 20;                 // of k and n: 32-bit offsets in a tile
+constexpr int64_t kProductMaxExperts = 1024;
+struct Gate {                // h = a(min(g, limit)) (clamp(u, +-limit) + shift)
+    int act;
+    float alpha, limit, shift;
+};
+
+// fq_product.hip: C [M, N] = A B, FP32 sums.  With offsets one product per
+// expert: of C's and A's rows (linear, glu, dx) or of the contraction (dw).
+struct ProductArgs {
+    const uint16_t *a, *b;   // BF16
+    int64_t lda, ldb;        // elements between their rows
+    int64_t b_stride;        // and between two experts' b
+    int M, N, K;
+    int rows;                // that the offsets divide
+    int experts;
+    const int32_t *offsets;  // [experts + 1] or null
+    const void *bias;        // [experts, columns] or null
+    int bias_f32;
+    const void *res;         // of y's type or null (may be y)
+    void *y;
+    int y_f32;
+    void *pre;               // values before the activation, PRE_* kind
+    void *pre_scales;
+    int pre_kind;
+    int act;
+    Gate gate;
+    int group;               // tile rows that share a run of b (set by the launcher)
+};
+hipError_t launch_product_linear(const ProductArgs &p, hipStream_t stream);
+hipError_t launch_product_glu(const ProductArgs &p, hipStream_t stream);      // N of each half
+hipError_t launch_product_dx(const ProductArgs &p, hipStream_t stream);
+hipError_t launch_product_dw(const ProductArgs &p, hipStream_t stream);
+
+// fq_checkpoint.hip
+constexpr int64_t kF8RowMaxCols = 32768;
+struct RowArgs8 {
+    const void *x;           // encode: BF16 [rows, cols]
+    void *codes, *scales;
+    void *y;                 // decode: BF16
+    int64_t rows, cols;
+};
+hipError_t launch_f8_encode(int f8, const RowArgs8 &a, hipStream_t stream);
+hipError_t launch_f8_decode(int f8, const RowArgs8 &a, hipStream_t stream);
+constexpr int kDzRows = 64;
+struct DzArgs {
+    int glu;
+    const void *dy;          // BF16 [rows, n]
+    const void *pre;         // [rows, n or 2n] of kind pre_kind, or null
+    const void *pre_scales;
+    int pre_kind;
+    Gate gate;               // the activation
+    int64_t rows, n;
+    int experts;
+    const int32_t *offsets;
+    void *dz;                // BF16, of pre's shape
+    void *h;                 // BF16 [rows, n] or null
+    float *partials;         // [dz_tiles, n or 2n], or null without dbias
+    float *dbias;            // [experts, n or 2n] or null
+};
+int64_t dz_tiles(int64_t rows, int64_t experts);
+hipError_t launch_dz(const DzArgs &a, hipStream_t stream);
+
 }  // namespace fqimpl

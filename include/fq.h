@@ -587,6 +587,110 @@ fq_status fq_adamw_plan(const fq_adamw_tensor *tensors, int64_t count, int32_t s
 fq_status fq_adamw_step_plan(const fq_adamw_hyper *hyper, const void *plan,
                              const void *plan_device, void *stream);
 
+/* ---- The feed-forward products of a training step ---------------------------------
+ * In BF16 with FP32 sums on the matrix cores: for layers that are not quantized,
+ * and for operands that are fake-quantized already (fq_fake_quant's y and
+ * fq_moe_dispatch's rows are BF16 tensors).
+ *
+ * One product, or one per expert: with offsets (int32 [experts + 1], device, as
+ * fq_moe_sort wrote them) rows offsets[e] .. offsets[e + 1] meet the weight and
+ * bias of expert e, whatever the segments' lengths, none included; rows past the
+ * last segment are neither read nor written.  Entries are brought into 0 .. rows;
+ * where they do not ascend the results of the rows concerned are unspecified.
+ * Without offsets (NULL) experts is 0 and weights and biases have no expert axis.
+ *
+ * Layouts, row-major: activations [rows, ...]; weights BF16 [experts, k, n] (as
+ * fq_qlinear_fwd's); bias BF16 or FP32 [experts, n], may be NULL.
+ * Shapes: 1 <= rows < 2^31; k and n multiples of 8 from 8 to 2^20 (of 32 where an
+ * operand of that width is held in 8 bits); rows * k, rows * columns and experts
+ * * k * columns at most 2^34; experts <= 1024.  Tensors 16-byte aligned, offsets
+ * 4-byte.  Outputs overlap no other operand except where it is said.
+ *
+ * Activations a(z), FP32: FQ_ACT_RELU max(z, 0); FQ_ACT_SILU z / (1 + exp(-z));
+ * FQ_ACT_GELU z (1 + erf(z / sqrt 2)) / 2.  An infinite z may give NaN with the
+ * last two (infinity times zero).  ReLU's derivative is 0 at 0.
+ *
+ * Checkpoints: what a forward keeps for its backward, in BF16 or in 8 bits
+ * (FQ_F8_*, above).  `pre` receives the values before the activation, rounded to
+ * BF16 (FQ_F8_NONE) or as codes and scales (FQ_F8_MX), from FP32 in both; where
+ * an expert's rows end it is left as it was, as y.  A backward takes x in BF16 or as 8-bit rows
+ * (FQ_F8_MX or FQ_F8_ROW, as fq_rmsnorm_fwd or fq_f8_encode wrote them), decoded
+ * and rounded to BF16. */
+enum { FQ_ACT_NONE = 0, FQ_ACT_RELU = 1, FQ_ACT_SILU = 2, FQ_ACT_GELU = 3 };
+
+/* 8-bit rows of x BF16 [rows, cols] and back: codes uint8 [rows, cols], scales as
+ * FQ_F8_MX or FQ_F8_ROW has them (above).  y BF16 [rows, cols] is each code's
+ * value times its scale, rounded to BF16 (exact for FQ_F8_MX unless it falls
+ * below BF16's normal range).  cols a multiple of 32, below 2^31 and for
+ * fq_f8_encode with FQ_F8_ROW at most 32768; rows * cols <= 2^34.  A block or row
+ * with an infinity or NaN stands for NaN.  All pointers 16-byte aligned. */
+fq_status fq_f8_encode(const void *x_bf16, int32_t f8, int64_t rows, int64_t cols, void *codes,
+                       void *scales, void *stream);
+fq_status fq_f8_decode(const void *codes, const void *scales, int32_t f8, int64_t rows,
+                       int64_t cols, void *y_bf16, void *stream);
+
+/* Matrix product with bias, activation and residual:
+ *   z = x w + bias;   y = a(z) + res.
+ * x BF16 [rows, k], w [experts, k, n], y of y_type [rows, n] rounded once, res
+ * (may be NULL, may be y) of y's type.  pre (may be NULL) [rows, n] receives z as
+ * pre_f8 says, pre_scales its scales.  ws: fq_linear_fwd_workspace_size bytes (0:
+ * may be NULL). */
+size_t fq_linear_fwd_workspace_size(int64_t rows, int64_t k, int64_t n, int64_t experts);
+fq_status fq_linear_fwd(const void *x_bf16, const void *w_bf16, const void *bias,
+                        int32_t bias_type, const void *res, int64_t rows, int64_t k, int64_t n,
+                        int64_t experts, const int32_t *offsets, int32_t act, void *pre,
+                        int32_t pre_f8, void *pre_scales, void *y, int32_t y_type, void *ws,
+                        size_t ws_bytes, void *stream);
+
+/* Backward of fq_linear_fwd for the gradient dy BF16 [rows, n] of y (which is also
+ * the gradient of res):
+ *   d = dy a'(z);  dz = BF16_RNE(d);  dx = BF16_RNE(dz w^T);  dw = x^T dz;
+ *   dbias = sum over rows of d,
+ * z read from pre (not read with FQ_ACT_NONE), dw of dw_type [experts, k, n],
+ * dbias FP32 [experts, n], both 0 for an expert without rows.  dx, dw and dbias
+ * may each be NULL, not all; x is read for dw only, w for dx only.  Sums have a
+ * fixed order: equal calls give equal bits. */
+size_t fq_linear_bwd_workspace_size(int64_t rows, int64_t k, int64_t n, int64_t experts,
+                                    int32_t x_f8);
+fq_status fq_linear_bwd(const void *dy_bf16, const void *x, int32_t x_f8, const void *x_scales,
+                        const void *w_bf16, const void *pre, int32_t pre_f8,
+                        const void *pre_scales, int64_t rows, int64_t k, int64_t n,
+                        int64_t experts, const int32_t *offsets, int32_t act, void *dx_bf16,
+                        void *dw, int32_t dw_type, float *dbias, void *ws, size_t ws_bytes,
+                        void *stream);
+
+/* Gated feed-forward block, both projections, the activation and the product in
+ * one kernel:
+ *   [g, u] = x w + bias (the first and the last n columns);
+ *   h = a(min(g, limit)) * (min(max(u, -limit), limit) + shift),
+ * a(v) = v / (1 + exp(-alpha v)) for FQ_ACT_SILU, else as above (alpha 1).
+ * {FQ_ACT_SILU, 1, INFINITY, 0} is the usual block.  limit > 0, may be infinite.
+ * x BF16 [rows, k], w [experts, k, 2 n], bias [experts, 2 n], h BF16 [rows, n], pre
+ * (may be NULL) [rows, 2 n] as for fq_linear_fwd. */
+typedef struct {
+    int32_t act;
+    float alpha, limit, shift;
+} fq_gate;
+size_t fq_glu_fwd_workspace_size(int64_t rows, int64_t k, int64_t n, int64_t experts);
+fq_status fq_glu_fwd(const fq_gate *gate, const void *x_bf16, const void *w_bf16,
+                     const void *bias, int32_t bias_type, int64_t rows, int64_t k, int64_t n,
+                     int64_t experts, const int32_t *offsets, void *pre, int32_t pre_f8,
+                     void *pre_scales, void *h_bf16, void *ws, size_t ws_bytes, void *stream);
+
+/* Its backward for the gradient dh BF16 [rows, n], from pre:
+ *   dg = dh (u' + shift) a'(g') where g <= limit, else 0;
+ *   du = dh a(g') where -limit <= u <= limit, else 0;   d = [dg, du],
+ * and dz, dx, dw [experts, k, 2 n], dbias [experts, 2 n] of d as in fq_linear_bwd.
+ * h, if given, receives the block's output again, from pre: BF16 [rows, n], what
+ * the next product's backward takes as its x. */
+size_t fq_glu_bwd_workspace_size(int64_t rows, int64_t k, int64_t n, int64_t experts,
+                                 int32_t x_f8);
+fq_status fq_glu_bwd(const fq_gate *gate, const void *dh_bf16, const void *x, int32_t x_f8,
+                     const void *x_scales, const void *w_bf16, const void *pre, int32_t pre_f8,
+                     const void *pre_scales, int64_t rows, int64_t k, int64_t n, int64_t experts,
+                     const int32_t *offsets, void *dx_bf16, void *dw, int32_t dw_type,
+                     float *dbias, void *h_bf16, void *ws, size_t ws_bytes, void *stream);
+
 /* Static description of a status code. */
 const char *fq_status_string(fq_status s);
 

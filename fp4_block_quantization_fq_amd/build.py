@@ -24,7 +24,8 @@ LIB = os.path.join(PKG, "libfq.so")
 BINDING = os.path.join(PKG, "_fq_binding.so")
 
 SOURCES = ["fq_api.cpp", "fq_kernels.hip", "fq_gemm.hip", "fq_hadamard.hip", "fq_outcontrol.hip",
-           "fq_norm.hip", "fq_moe.hip", "fq_adamw.hip", "fq_product.hip", "fq_checkpoint.hip"]
+           "fq_norm.hip", "fq_moe.hip", "fq_adamw.hip", "fq_product_fwd.hip",
+           "fq_product_bwd.hip", "fq_checkpoint.hip"]
 ARCH = "gfx950"
 
 COMMON = [

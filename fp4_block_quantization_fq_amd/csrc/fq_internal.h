@@ -246,7 +246,7 @@ struct Gate {                // h = a(min(g, limit)) (clamp(u, +-limit) + shift)
     float alpha, limit, shift;
 };
 
-// fq_product.hip: C [M, N] = A B, FP32 sums.  With offsets one product per
+// fq_product_fwd.hip, fq_product_bwd.hip: C [M, N] = A B, FP32 sums.  With offsets one product per
 // expert: of C's and A's rows (linear, glu, dx) or of the contraction (dw).
 struct ProductArgs {
     const uint16_t *a, *b;   // BF16
@@ -268,10 +268,10 @@ struct ProductArgs {
     Gate gate;
     int group;               // tile rows that share a run of b (set by the launcher)
 };
-hipError_t launch_product_linear(const ProductArgs &p, hipStream_t stream);
-hipError_t launch_product_glu(const ProductArgs &p, hipStream_t stream);      // N of each half
-hipError_t launch_product_dx(const ProductArgs &p, hipStream_t stream);
-hipError_t launch_product_dw(const ProductArgs &p, hipStream_t stream);
+hipError_t launch_product_linear(ProductArgs p, hipStream_t stream);
+hipError_t launch_product_glu(ProductArgs p, hipStream_t stream);      // N of each half
+hipError_t launch_product_dx(ProductArgs p, hipStream_t stream);
+hipError_t launch_product_dw(ProductArgs p, hipStream_t stream);
 
 // fq_checkpoint.hip
 constexpr int64_t kF8RowMaxCols = 32768;

@@ -1,0 +1,541 @@
+// fq_product.hpp -- the tile kernel of the feed-forward products, on BF16 matrix
+// cores: y = a(x w + b) + res, the gated h = a(x wg + bg) (x wu + bu), and the two
+// products of their backward, dx = dz w^T and dw = x^T dz.  One product, or one
+// per expert over the segments of rows that fq_moe_sort made.
+//
+// A product is C[M, N] = sum over k of A(m, k) B(k, n), FP32 sums on
+// v_mfma_f32_32x32x16_bf16.  Weights lie [K, N] and activations [rows, K], so
+// an operand is either contiguous along the contraction (x in the forward, dz
+// and w in dx) or across it (w in the forward, x and dz in dw).  Both go from
+// global memory straight to LDS as they lie, 16 bytes a lane; the second kind
+// is transposed on the way into registers by gfx950's ds_read_b64_tr_b16: in a
+// group of 16 lanes, lane s reads four columns of row s / 4 and receives the
+// four rows of column s.  Those reads run at 128 B a clock and CU, ds_read_b128
+// at 256 (both measured), which is enough for either (below).
+//
+// LDS tiles: contraction-contiguous, a 128-byte row (64 k) per tile row, 16-byte
+// chunks XORed with (row & 7) ^ (row >> 3 & 1); otherwise a row per k of all the
+// tile's columns, its 64-byte units moved by the row's number so that the four
+// rows that a transposing read touches lie in different banks (no conflicts,
+// measured).
+//
+// Schedule: two stages of 64 k.  A substep of 16 k has its fragments in registers
+// when it begins and reads the next one's between its products.  The stage's one
+// barrier lies in front of its last substep, whose fragments are in registers by
+// then: the other stage has landed, this one is free, and the loads that refill it
+// go out between the products of the next two substeps.  What that took:
+//  - The direct loads are written as assembly (they have no result register) and
+//    waited for by hand.  The compiler cannot tell which LDS bytes a load in flight
+//    writes from those that a transposing read asks for: it waited for all loads
+//    behind the barrier, a memory latency a stage (1.77 us a stage of 256 x 256,
+//    with these loads 1.46).
+//  - Order is pinned product by product.  Loads issued together at the barrier keep
+//    the waves from issuing products while the address unit works through them.
+// At 1.46 us a stage the chip runs at 1.8 GHz of its 2.4: power is what is left
+// (products alone, fragments in registers, 1.16 us at 1.8 GHz; with the LDS reads
+// 1.31).
+//
+// Past the end of the contraction both operands are read as zeros (from an
+// array of zeros, chosen by address), so neither infinities nor NaN of other
+// rows reach a sum.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fq_act.hpp"
+#include "fq_internal.h"
+
+namespace {
+
+using namespace fqdev;
+using fqimpl::ProductArgs;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+enum { ALONG = 0, ACROSS = 1 };                  // operand against the contraction
+// what becomes of the sums: stored; bias and residual added; all of the linear's
+// epilogue; the gated block's
+enum { EPI_STORE = 0, EPI_RES = 1, EPI_LINEAR = 2, EPI_GLU = 3 };
+
+constexpr int BK = 64;
+constexpr int kXcds = 8;
+
+__device__ const u32w4 kZeros = {0, 0, 0, 0};
+
+// 16 bytes a lane from base + off (or src) to LDS at `lds` (uniform) + 16 * lane.
+// The instruction takes its LDS address from m0.
+__device__ __forceinline__ void direct_load(const uint8_t *base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 : : "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds)) : "m0");
+}
+__device__ __forceinline__ void direct_load(const uint8_t *src, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 : : "v"(src), "s"(__builtin_amdgcn_readfirstlane(lds)) : "m0");
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p)
+{
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+}
+
+__device__ __forceinline__ int swz(int row, int chunk)
+{
+    return chunk ^ (row & 7) ^ ((row >> 3) & 1);
+}
+
+// ---- operand tiles ---------------------------------------------------------------
+// 64 k of ROWS rows (ALONG) or columns (ACROSS): ROWS * 128 bytes, 1 KB a wave
+// instruction.  Lane offsets are fixed; the base moves on by a step of 64 k.
+template <int L, int ROWS, int WAVES>
+struct Tile {
+    static constexpr int NI = ROWS / 8 / WAVES;            // instructions a wave
+    static constexpr int CHUNKS = ROWS / 8;                // of 16 bytes of a k's row (ACROSS)
+    static constexpr int UNITS = ROWS / 32;                // and of 64 bytes
+    static_assert(NI * WAVES * 8 == ROWS && ROWS % 64 == 0, "whole instructions");
+    const uint8_t *base;
+    uint32_t off[NI];
+    int64_t step;
+
+    // Where unit `unit` of k's row lies.  A row is a multiple of the banks' 256
+    // bytes, or (192 columns) one and a half of it: then rows k and k + 2 would meet.
+    static __device__ __forceinline__ int place(int k, int unit)
+    {
+        if (UNITS % 4 == 0) return unit ^ (k & 3);
+        unit += (k >> 1) & 1;
+        return unit >= UNITS ? unit - UNITS : unit;
+    }
+    static __device__ __forceinline__ int unit_at(int k, int place)
+    {
+        if (UNITS % 4 == 0) return place ^ (k & 3);
+        place -= (k >> 1) & 1;
+        return place < 0 ? place + UNITS : place;
+    }
+
+    // `first` of `count` rows or columns; pitch in elements.  SPLIT: the columns
+    // are 32 of the first half, 32 of the second half (`half` columns on), ...
+    template <bool SPLIT>
+    __device__ __forceinline__ void init(const uint16_t *p, int64_t pitch, int first, int count,
+                                         int half, int wave, int lane)
+    {
+        if (L == ALONG) {
+            base = (const uint8_t *)(p + (int64_t)first * pitch);
+            step = BK * 2;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int r = (wave * NI + i) * 8 + (lane >> 3);
+                const int row = min(r, count - first - 1);          // never stored
+                off[i] = (uint32_t)row * (uint32_t)(pitch * 2) + swz(r, lane & 7) * 16;
+            }
+        } else {
+            base = (const uint8_t *)p;
+            step = BK * 2 * pitch;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int id = (wave * NI + i) * 64 + lane, k = id / CHUNKS, slot = id % CHUNKS;
+                const int t = unit_at(k, slot >> 2) * 32 + (slot & 3) * 8;
+                int col = first + t, more = 0;
+                if (SPLIT) {
+                    col = first + (t >> 6) * 32 + (t & 31);
+                    more = (t & 32) ? half : 0;
+                }
+                if (col >= count) col = first;                      // never stored
+                off[i] = (uint32_t)k * (uint32_t)(pitch * 2) + (uint32_t)(col + more) * 2;
+            }
+        }
+    }
+    // k of instruction i's chunk within the step
+    __device__ __forceinline__ int k_of(int i, int wave, int lane) const
+    {
+        if (L == ALONG) return swz((wave * NI + i) * 8 + (lane >> 3), lane & 7) * 8;
+        return ((wave * NI + i) * 64 + lane) / CHUNKS;
+    }
+    // Instruction i of a step; `left` k of it exist (64 or more: all).
+    __device__ __forceinline__ void issue(uint32_t lds, int i) const
+    {
+        direct_load(base, off[i], lds + i * 1024);
+    }
+    __device__ __forceinline__ void issue(uint32_t lds, int i, int left, int wave, int lane) const
+    {
+        if (left >= BK) return issue(lds, i);
+        direct_load(k_of(i, wave, lane) < left ? base + off[i] : (const uint8_t *)&kZeros, lds + i * 1024);
+    }
+    // eight k of row (column) 32 * t + lane % 32 for substep ks of 16 k
+    static __device__ __forceinline__ bf16x8 read(const uint8_t *lds, int t, int ks, int lane)
+    {
+        if (L == ALONG) {
+            const int r = t * 32 + (lane & 31);
+            return *reinterpret_cast<const bf16x8 *>(lds + r * 128 + swz(r, ks * 2 + (lane >> 5)) * 16);
+        }
+        const int k = ks * 16 + (lane >> 5) * 8 + ((lane & 15) >> 2);
+        const uint8_t *p = lds + k * (ROWS * 2) + place((lane & 15) >> 2, t) * 64 + (lane & 16) * 2 + (lane & 3) * 8;
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * ROWS * 2));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
+// ---- epilogues ---------------------------------------------------------------------
+__device__ __forceinline__ void load_bias(const ProductArgs &p, int64_t at, float (&b)[8])
+{
+    if (!p.bias) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = 0.0f;
+    } else if (p.bias_f32) {
+        load8<false>((const float *)p.bias + at, 8, b);
+    } else {
+        load8<false>((const uint16_t *)p.bias + at, 8, b);
+    }
+}
+
+// Eight values before the activation, kept for the backward: rounded to BF16, or
+// to E4M3 under a power of two per 32 columns, which four neighbouring lanes hold
+// (from FP32: a rounding to BF16 before would move a block's maximum across a
+// border of its scale now and then).
+__device__ __forceinline__ void keep_pre(const ProductArgs &p, int64_t at, const float (&z)[8])
+{
+    if (p.pre_kind == fqimpl::PRE_BF16) {
+        store8<false>((uint16_t *)p.pre + at, 8, z);
+        return;
+    }
+    u32w2 codes;
+    const uint32_t scale = mx8_encode8(z, &codes);
+    *(u32w2 *)((uint8_t *)p.pre + at) = codes;
+    if ((at & 31) == 0) ((uint8_t *)p.pre_scales)[at >> 5] = (uint8_t)scale;
+}
+
+__device__ __forceinline__ void load_res(const ProductArgs &p, int64_t at, float (&r)[8])
+{
+    if (p.y_f32) load8<false>((const float *)p.res + at, 8, r);
+    else load8<false>((const uint16_t *)p.res + at, 8, r);
+}
+__device__ __forceinline__ void store_y(const ProductArgs &p, int64_t at, const float (&v)[8])
+{
+    if (p.y_f32) store8<false>((float *)p.y + at, 8, v);
+    else store8<false>((uint16_t *)p.y + at, 8, v);
+}
+
+// What becomes of eight sums (column `col` of row `row`, of N columns).
+__device__ __forceinline__ void finish_linear(const ProductArgs &p, int64_t row, int col, int N,
+                                              float (&z)[8], const float (&bias)[8])
+{
+    const int64_t at = row * N + col;
+    float r[8] = {};
+    if (p.res) load_res(p, at, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += bias[i];
+    if (p.pre_kind) keep_pre(p, at, z);
+    act8(p.act, 1.0f, z);
+    if (p.res) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] += r[i];
+    }
+    store_y(p, at, z);
+}
+// and of eight pairs of the gated block
+__device__ __forceinline__ void finish_glu(const ProductArgs &p, int64_t row, int col, int n,
+                                           float (&g)[8], float (&u)[8], const float (&bg)[8],
+                                           const float (&bu)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        g[i] += bg[i];
+        u[i] += bu[i];
+    }
+    if (p.pre_kind) {
+        keep_pre(p, row * 2 * n + col, g);
+        keep_pre(p, row * 2 * n + n + col, u);
+    }
+    glu8(p.gate, g, u);
+    store8<false>((uint16_t *)p.y + row * n + col, 8, g);
+}
+
+// ---- the kernel ----------------------------------------------------------------------
+// WM x WN waves of TM x TN accumulator tiles of 32 x 32.  SEGK: the experts'
+// segments are of the contraction (dw), else of C's rows.
+template <int LA, int LB, int TM, int TN, int WM, int WN, int EPI, bool SEGK>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p)
+{
+    constexpr int BM = WM * TM * 32, BN = WN * TN * 32, WAVES = WM * WN;
+    constexpr int BNC = EPI == EPI_GLU ? BN / 2 : BN;      // columns of the output
+    constexpr int A_BYTES = BM * 128, STAGE = A_BYTES + BN * 128;
+    static_assert(EPI != EPI_GLU || TN % 2 == 0, "32 columns of either half next to each other");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds0[STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds1[STAGE];
+
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int wm = wave / WN, wn = wave % WN;
+
+    // this workgroup's tile
+    const int tiles_n = (p.N + BNC - 1) / BNC;
+    int tiles_m = (p.M + BM - 1) / BM;
+    if (p.offsets) tiles_m = SEGK ? tiles_m * p.experts : segment_tiles(p.offsets, p.experts, p.rows, BM, lane);
+    const int total = tiles_m * tiles_n, b = (int)blockIdx.x;
+    if (b >= total) return;
+    // the hardware deals workgroups round-robin to eight XCDs, each with its own
+    // L2: a contiguous run of tiles each
+    const int each = total / kXcds, rest = total % kXcds, xcd = b % kXcds;
+    const int logical = xcd * each + min(xcd, rest) + b / kXcds;
+    const int in_group = p.group * tiles_n, g = logical / in_group, first_m = g * p.group;
+    const int gm = min(tiles_m - first_m, p.group);
+    const int tm = first_m + logical % in_group % gm, tn = logical % in_group / gm;
+
+    int row0, row_end, expert = 0, k_begin = 0, k_end = p.K;
+    if (!p.offsets) {
+        row0 = tm * BM;
+        row_end = p.M;
+    } else if (SEGK) {
+        const int per = (p.M + BM - 1) / BM;
+        expert = tm / per;
+        row0 = tm % per * BM;
+        row_end = p.M;
+        segment_of(p.offsets, expert, p.rows, &k_begin, &k_end);
+        k_begin = __builtin_amdgcn_readfirstlane(k_begin);
+        k_end = __builtin_amdgcn_readfirstlane(k_end);
+    } else {
+        find_segment(p.offsets, p.experts, p.rows, BM, tm, lane, &expert, &row0, &row_end);
+    }
+    const int col0 = tn * BNC;
+
+    Tile<LA, BM, WAVES> ta;
+    Tile<LB, BN, WAVES> tb;
+    const uint16_t *pa = p.a, *pb = p.b + (SEGK ? 0 : expert * p.b_stride);
+    if (SEGK) {
+        pa += (int64_t)k_begin * p.lda;
+        pb += (int64_t)k_begin * p.ldb;
+    }
+    ta.template init<false>(pa, p.lda, row0, row_end, 0, wave, lane);
+    tb.template init<EPI == EPI_GLU>(pb, p.ldb, col0, p.N, p.N, wave, lane);
+
+    floatx16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+    constexpr int NA = decltype(ta)::NI, LOADS = NA + decltype(tb)::NI;
+    constexpr int READS = TM + TN, MFMAS = TM * TN, HALF = LOADS / 2;
+    static_assert(MFMAS >= READS, "a product in front of every read");
+    bf16x8 fa[2][TM], fb[2][TN];
+    const uint32_t to_a[2] = {lds_address(lds0) + wave * NA * 1024, lds_address(lds1) + wave * NA * 1024};
+    const uint32_t to_b[2] = {lds_address(lds0) + A_BYTES + wave * (LOADS - NA) * 1024,
+                              lds_address(lds1) + A_BYTES + wave * (LOADS - NA) * 1024};
+    int left = k_end - k_begin;                // of the contraction
+
+    // fragment n of a substep, in the order of their first use: b0 a0 b1 b2 .. a1 a2 ..
+    auto read = [&](const uint8_t *lds, int ks, int to, int n) {
+        if (n == 0 || (n > 1 && n <= TN)) {
+            const int j = n ? n - 1 : 0;
+            fb[to][j] = tb.read(lds + A_BYTES, wn * TN + j, ks, lane);
+        } else {
+            const int i = n == 1 ? 0 : n - TN;
+            fa[to][i] = ta.read(lds, wm * TM + i, ks, lane);
+        }
+    };
+    // load n of a stage into buffer `buf`; `have` k of it exist (not looked at if FULL)
+    auto load = [&](int buf, int n, int have, bool full) {
+        if (n < NA) {
+            if (full) ta.issue(to_a[buf], n);
+            else if (have > 0) ta.issue(to_a[buf], n, have, wave, lane);
+        } else {
+            if (full) tb.issue(to_b[buf], n - NA);
+            else if (have > 0) tb.issue(to_b[buf], n - NA, have, wave, lane);
+        }
+    };
+    // One substep: its products from fragments `from`; between them the reads of
+    // the next one's from `lds` and `count` loads from number `first` on.
+    auto substep = [&](int from, bool reads, const uint8_t *lds, int ks, int buf, int first, int count,
+                       int have, bool full) {
+#pragma unroll
+        for (int q = 0; q < MFMAS; ++q) {
+            const int i = q / TN, j = q % TN;
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[from][i], fb[from][j], acc[i][j], 0, 0, 0);
+            if (reads && q < READS) read(lds, ks, 1 - from, q);
+#pragma unroll
+            for (int n = 0; n < LOADS; ++n)
+                if (n < count && n * MFMAS / count == q) load(buf, first + n, have, full);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto stage = [&](int cur, bool full) {
+        const uint8_t *here = cur ? lds1 : lds0, *there = cur ? lds0 : lds1;
+        const int next = left - BK, after = left - 2 * BK;        // k of the next two stages
+        substep(0, true, here, 1, 1 - cur, HALF, LOADS - HALF, next, full);
+        substep(1, true, here, 2, 0, 0, 0, 0, true);
+        substep(0, true, here, 3, 0, 0, 0, 0, true);
+        ta.base += ta.step;
+        tb.base += tb.step;
+        if (full || next > 0) {
+            // the next stage has landed, and this wave has read all of this one
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+        }
+        substep(1, full || next > 0, there, 0, cur, 0, HALF, after, full);
+        left -= BK;
+    };
+    if (left > 0) {
+#pragma unroll
+        for (int n = 0; n < LOADS; ++n) load(0, n, left, false);
+        ta.base += ta.step;
+        tb.base += tb.step;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < HALF; ++n) load(1, n, left - BK, false);
+#pragma unroll
+        for (int n = 0; n < READS; ++n) read(lds0, 0, 0, n);
+        while (left >= 4 * BK) {               // all loads of both stages are whole
+            stage(0, true);
+            stage(1, true);
+        }
+        while (left > 0) {
+            stage(0, false);
+            if (left > 0) stage(1, false);
+        }
+        __syncthreads();
+    }
+
+    // Epilogue: 32 rows at a time through this wave's part of the idle stages, so
+    // that a lane gets eight neighbouring columns.  Element v of lane l of an
+    // accumulator is row v / 4 * 8 + l / 32 * 4 + v % 4, column l % 32.
+    constexpr int WCOLS = TN * 32, CHUNKS = EPI == EPI_GLU ? WCOLS / 16 : WCOLS / 8, PASSES = 32 * CHUNKS / 64;
+    constexpr int SLAB = 32 * WCOLS * 4;
+    static_assert(WAVES / 2 * SLAB <= STAGE && WAVES % 2 == 0, "a slab for every wave");
+    float *slab = reinterpret_cast<float *>((wave < WAVES / 2 ? lds0 : lds1) + wave % (WAVES / 2) * SLAB);
+    const int wcol0 = col0 + wn * (EPI == EPI_GLU ? WCOLS / 2 : WCOLS);
+    auto chunk_at = [&](int i, int k, int *r, int *c, int64_t *row, int *col) {
+        const int id = k * 64 + lane;
+        *r = id / CHUNKS;
+        *c = id % CHUNKS * 8;
+        *row = (int64_t)row0 + (wm * TM + i) * 32 + *r;
+        *col = wcol0 + *c;
+        return *row < row_end && *col < p.N;
+    };
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        // residuals first, so that their loads overlap
+        Raw8<uint16_t> res16[EPI == EPI_RES ? PASSES : 1];
+        if (EPI == EPI_RES && p.res && !p.y_f32) {
+#pragma unroll
+            for (int k = 0; k < PASSES; ++k) {
+                int r, c, col;
+                int64_t row;
+                if (chunk_at(i, k, &r, &c, &row, &col))
+                    load_raw8<false>((const uint16_t *)p.res + row * p.N + col, 8, res16[k]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+                slab[((v >> 2) * 8 + (lane >> 5) * 4 + (v & 3)) * WCOLS + j * 32 + (lane & 31)] = acc[i][j][v];
+        // the wave reads what it wrote itself: LDS keeps a wave's order
+        __builtin_amdgcn_wave_barrier();
+        if (EPI == EPI_STORE || EPI == EPI_RES) {
+#pragma unroll
+            for (int k = 0; k < PASSES; ++k) {
+                int r, c, col;
+                int64_t row;
+                const bool in = chunk_at(i, k, &r, &c, &row, &col);
+                float z[8];
+                load8<false>(slab + r * WCOLS + c, 8, z);
+                if (!in) continue;
+                const int64_t at = (SEGK ? (int64_t)expert * p.M * p.N : 0) + row * p.N + col;
+                if (EPI == EPI_RES) {
+                    float bias[8];
+                    load_bias(p, (int64_t)expert * p.N + col, bias);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[e] += bias[e];
+                    if (p.res) {
+                        float v[8];
+                        if (p.y_f32) load_res(p, at, v);
+                        else unpack8(res16[k], v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) z[e] += v[e];
+                    }
+                }
+                store_y(p, at, z);
+            }
+        } else {
+            // not unrolled: the activations' code is long
+#pragma unroll 1
+            for (int k = 0; k < PASSES; ++k) {
+                int r, c, col;
+                int64_t row;
+                const bool in = chunk_at(i, k, &r, &c, &row, &col);
+                float z[8], u[8];
+                if (EPI == EPI_GLU) {
+                    const float *s = slab + r * WCOLS + (c >> 5) * 64 + (c & 31);
+                    load8<false>(s, 8, z);
+                    load8<false>(s + 32, 8, u);
+                } else {
+                    load8<false>(slab + r * WCOLS + c, 8, z);
+                }
+                if (!in) continue;
+                float bias[8], bias_up[8];
+                const int64_t at = (int64_t)expert * (EPI == EPI_GLU ? 2 : 1) * p.N + col;
+                load_bias(p, at, bias);
+                if (EPI == EPI_GLU) {
+                    load_bias(p, at + p.N, bias_up);
+                    finish_glu(p, row, col, p.N, z, u, bias, bias_up);
+                } else {
+                    finish_linear(p, row, col, p.N, z, bias);
+                }
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// ---- launches ------------------------------------------------------------------------
+// Tiles of `bm` rows and `bn` columns (of the output), for the grid at most.
+template <bool SEGK>
+int64_t product_tiles(const ProductArgs &p, int bm, int bn)
+{
+    const int64_t n = ((int64_t)p.N + bn - 1) / bn;
+    int64_t m = ((int64_t)p.M + bm - 1) / bm;
+    if (p.offsets) {
+        const int64_t used = p.experts < p.rows ? p.experts : p.rows;
+        m = SEGK ? m * p.experts : p.rows / bm + used;          // segments end inside tiles
+    }
+    return m * n;
+}
+
+// Time of a call in one shape of tiles, to compare the shapes: rounds of 256 CUs
+// times a round's, of `step` per 64 k and `fixed` around them (us, measured on
+// 8192 x 2880 and 2880 x 5760 outputs).
+template <bool SEGK>
+float product_time(const ProductArgs &p, int bm, int bn, int per_cu, float step, float fixed)
+{
+    const int64_t n = ((int64_t)p.N + bn - 1) / bn;
+    float m = (float)(((int64_t)p.M + bm - 1) / bm), k = (float)p.K;
+    if (p.offsets) {
+        const float used = (float)(p.experts < p.rows ? p.experts : p.rows);
+        if (SEGK) {
+            m *= (float)p.experts;
+            k /= (float)p.experts;
+        } else {
+            m = (float)p.rows / bm + 0.5f * used;              // on average
+        }
+    }
+    const float rounds = ceilf(m * n / (256.0f * per_cu));
+    return rounds * (ceilf(k / 64) * step + fixed);
+}
+
+template <int LA, int LB, int TM, int TN, int WM, int WN, int EPI, bool SEGK>
+hipError_t launch_tiles(const ProductArgs &p, hipStream_t stream)
+{
+    constexpr int BM = WM * TM * 32, BN = WN * TN * 32 / (EPI == EPI_GLU ? 2 : 1);
+    hipLaunchKernelGGL((k_product<LA, LB, TM, TN, WM, WN, EPI, SEGK>),
+                       dim3((uint32_t)product_tiles<SEGK>(p, BM, BN)), dim3(64 * WM * WN), 0, stream, p);
+    return hipGetLastError();
+}
+
+}  // namespace

@@ -73,7 +73,7 @@ def run_linear(rows, k, n, starts=None, act=op.NONE, out=torch.bfloat16, res=Tru
 # one token, ragged rows, odd multiples of eight, contractions that end inside a step; the last ones take the large tiles
 SHAPES = [(1, 8, 8), (1, 72, 264), (1, 2880, 200), (2, 64, 64), (3, 1000, 136), (7, 520, 1032), (16, 128, 72), (17, 136, 128), (31, 64, 8),
           (33, 200, 320), (64, 1032, 96), (65, 264, 392), (127, 8, 128), (128, 192, 256), (129, 64, 264), (257, 776, 136),
-          (300, 40, 1096), (1021, 72, 776), (4200, 72, 4168)]
+          (300, 40, 1096), (1021, 72, 776), (4200, 72, 4168), (4090, 72, 4088), (4090, 392, 4088), (4200, 456, 4168), (4090, 392, 2040)]
 
 
 @pytest.mark.parametrize("rows,k,n", SHAPES)
@@ -202,7 +202,8 @@ def run_bwd(rows, k, n, starts=None, gate=None, act=op.NONE, x_how="bf16", pre_h
 
 
 BWD_SHAPES = [(1, 8, 8), (1, 264, 136), (2, 64, 64), (5, 1000, 72), (63, 72, 264), (64, 128, 128), (65, 136, 264), (100, 520, 776),
-              (129, 256, 136), (333, 1000, 72), (1000, 72, 136), (2200, 4168, 136)]
+              (129, 256, 136), (333, 1000, 72), (1000, 72, 136), (2200, 4168, 136),
+              (4090, 4088, 72), (4200, 4168, 72), (4200, 4168, 456), (100, 4088, 4088), (100, 2872, 2864), (456, 2872, 2864), (392, 4088, 4088)]
 
 
 @pytest.mark.parametrize("rows,k,n", BWD_SHAPES)

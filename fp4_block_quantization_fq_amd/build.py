@@ -25,7 +25,7 @@ BINDING = os.path.join(PKG, "_fq_binding.so")
 
 SOURCES = ["fq_api.cpp", "fq_kernels.hip", "fq_gemm.hip", "fq_hadamard.hip", "fq_outcontrol.hip",
            "fq_norm.hip", "fq_moe.hip", "fq_adamw.hip", "fq_product_fwd.hip",
-           "fq_product_bwd.hip", "fq_checkpoint.hip"]
+           "fq_product_few.hip", "fq_product_bwd.hip", "fq_product_join.hip", "fq_checkpoint.hip"]
 ARCH = "gfx950"
 
 COMMON = [

@@ -2,9 +2,11 @@
 // around them share: activations and their derivatives, the gate, 8-bit blocks,
 // and the experts' segments of rows.
 //
-// Activations are FP32: sigmoid from expf (1 ulp) and the hardware's reciprocal
-// (1 ulp), GELU from erff.  An infinite value before SiLU or GELU may give NaN
-// (infinity times 0), as their formulas have it.
+// Activations are FP32, from the hardware's exp2 and reciprocal (1 ulp each; the
+// exponent's rounding adds |z| / 2 ulp to exp(-z), which the slope of the sigmoid
+// takes back): with expf and erff a tile's epilogue cost EPI_ACT.  An infinite
+// value before SiLU or GELU may give NaN (infinity times 0), as their formulas
+// have it.
 #pragma once
 
 #include "fq_internal.h"
@@ -14,16 +16,38 @@ namespace fqdev {
 
 using fqimpl::Gate;
 
+constexpr float kLog2E = 1.4426950408889634f;
+
 __device__ __forceinline__ float sigmoid(float v)
 {
-    return __builtin_amdgcn_rcpf(1.0f + expf(-v));
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -kLog2E));
+}
+// The normal distribution function and *e = exp(-z^2 / 2).  With x = |z| / sqrt 2 its
+// smaller side is erfc(x) / 2 = e erfcx(x) / 2, and erfcx(x) = t P(t) for
+// t = 1 / (1 + 0.34 x), P of degree 9 fitted to erfcx for the least largest relative
+// error, 3.5e-09, so the far side keeps its relative precision.
+__device__ __forceinline__ float normal_cdf(float z, float *e)
+{
+    constexpr float P[] = {0.191816539f, 0.192037061f, 0.178268477f, 0.174870953f,
+                           0.0593979955f, 0.275508434f, -0.278319448f, 0.401717603f,
+                           -0.246014193f, 0.0507165603f};
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fabsf(z), 0.240416306f, 1.0f));
+    float q = P[9];
+#pragma unroll
+    for (int i = 8; i >= 0; --i) q = __builtin_fmaf(q, t, P[i]);
+    *e = __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2E));
+    q *= 0.5f * t * *e;
+    return z < 0.0f ? q : 1.0f - q;
 }
 
 // a(z) and a'(z)
 __device__ __forceinline__ float act1(int act, float alpha, float z)
 {
     if (act == fqimpl::ACT_SILU) return z * sigmoid(alpha * z);
-    if (act == fqimpl::ACT_GELU) return z * (0.5f + 0.5f * erff(z * 0.70710678118654752f));
+    if (act == fqimpl::ACT_GELU) {
+        float e;
+        return z * normal_cdf(z, &e);
+    }
     if (act == fqimpl::ACT_RELU) return z <= 0.0f ? 0.0f : z;
     return z;
 }
@@ -35,9 +59,10 @@ __device__ __forceinline__ float act1_grad(int act, float alpha, float z, float 
         return s * (1.0f + alpha * z * (1.0f - s));
     }
     if (act == fqimpl::ACT_GELU) {
-        const float phi = 0.5f + 0.5f * erff(z * 0.70710678118654752f);
+        float e;
+        const float phi = normal_cdf(z, &e);
         *value = z * phi;
-        return phi + z * (0.39894228040143268f * expf(-0.5f * z * z));
+        return phi + z * (0.39894228040143268f * e);
     }
     if (act == fqimpl::ACT_RELU) {
         *value = z <= 0.0f ? 0.0f : z;
@@ -53,15 +78,17 @@ __device__ __forceinline__ void act8(int act, float alpha, float (&z)[8])
     for (int i = 0; i < 8; ++i) z[i] = act1(act, alpha, z[i]);
 }
 
-// g = a(min(g, limit)) (clamp(u, -limit, limit) + shift); NaN stays NaN
+// a(min(g, limit)) (clamp(u, -limit, limit) + shift); NaN stays NaN
+__device__ __forceinline__ float glu1(const Gate &t, float g, float u)
+{
+    const float gate = g > t.limit ? t.limit : g;
+    const float up = u > t.limit ? t.limit : u < -t.limit ? -t.limit : u;
+    return act1(t.act, t.alpha, gate) * (up + t.shift);
+}
 __device__ __forceinline__ void glu8(const Gate &t, float (&g)[8], const float (&u)[8])
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float gate = g[i] > t.limit ? t.limit : g[i];
-        const float up = u[i] > t.limit ? t.limit : u[i] < -t.limit ? -t.limit : u[i];
-        g[i] = act1(t.act, t.alpha, gate) * (up + t.shift);
-    }
+    for (int i = 0; i < 8; ++i) g[i] = glu1(t, g[i], u[i]);
 }
 // Its backward for the gradient dh: dg and du into g and u, h's value into dh.
 __device__ __forceinline__ void glu8_grad(const Gate &t, float (&g)[8], float (&u)[8], float (&dh)[8])

@@ -1610,18 +1610,40 @@ fq_status check_pre(const Product &d, const void *pre, int32_t f8, const void *s
     return FQ_OK;
 }
 
-size_t product_fwd_ws(const Product &) { return 0; }
+// Parts of the contraction of one product [M, columns] over K, and their bytes.
+int splits_of(const Product &d, int64_t M, int64_t columns, int64_t K)
+{
+    return d.experts ? 1 : fqimpl::product_splits(M, columns, K);
+}
+size_t split_bytes(const Product &d, int64_t M, int64_t columns, int64_t K)
+{
+    const int n = splits_of(d, M, columns, K);
+    return n > 1 ? (size_t)n * M * columns * sizeof(float) : 0;
+}
 
-// Workspace of a backward: dz, x decoded, the tiles' column sums.
+int fwd_splits(const Product &d)
+{
+    return fqimpl::product_few_rows(d.rows, d.experts) ? 1 : splits_of(d, d.rows, d.cols(), d.k);
+}
+size_t product_fwd_ws(const Product &d)
+{
+    return fwd_splits(d) > 1 ? split_bytes(d, d.rows, d.cols(), d.k) : 0;
+}
+
+// Workspace of a backward: dz, x decoded, the tiles' column sums, the parts of a
+// split dx and then of a split dw.
 struct ProductBwdLayout {
-    size_t x, partials, total;
+    size_t x, partials, parts, total;
 };
 ProductBwdLayout product_bwd_layout(const Product &d, int32_t x_f8)
 {
     ProductBwdLayout l;
     l.x = round256((size_t)d.rows * d.cols() * 2);
     l.partials = l.x + (x_f8 != FQ_F8_NONE ? round256((size_t)d.rows * d.k * 2) : 0);
-    l.total = l.partials + (size_t)fqimpl::dz_tiles(d.rows, d.experts) * d.cols() * sizeof(float);
+    l.parts = l.partials +
+              round256((size_t)fqimpl::dz_tiles(d.rows, d.n, d.experts) * d.cols() * sizeof(float));
+    const size_t dx = split_bytes(d, d.rows, d.k, d.cols()), dw = split_bytes(d, d.k, d.cols(), d.rows);
+    l.total = l.parts + (dx > dw ? dx : dw);
     return l;
 }
 
@@ -1749,6 +1771,8 @@ fq_status product_bwd(const Product &d, const ProductBwd &a)
         p.N = (int)d.k;
         p.K = (int)d.cols();
         p.y = a.dx;
+        p.splits = splits_of(d, d.rows, d.k, d.cols());
+        p.partial = (float *)(ws + l.parts);
         const hipError_t e = fqimpl::launch_product_dx(p, a.stream);
         if (e != hipSuccess) return device_status(e, "dx product launch");
     }
@@ -1774,6 +1798,8 @@ fq_status product_bwd(const Product &d, const ProductBwd &a)
         p.N = (int)d.cols();
         p.K = (int)d.rows;
         p.y = a.dw;
+        p.splits = splits_of(d, d.k, d.cols(), d.rows);
+        p.partial = (float *)(ws + l.parts);
         p.y_f32 = a.dw_type == FQ_TYPE_F32;
         const hipError_t e = fqimpl::launch_product_dw(p, a.stream);
         if (e != hipSuccess) return device_status(e, "dw product launch");
@@ -1856,6 +1882,8 @@ fq_status fq_linear_fwd(const void *x_bf16, const void *w_bf16, const void *bias
     p.act = act;
     p.res = res;
     p.y = y;
+    p.splits = fwd_splits(d);
+    p.partial = (float *)ws;
     p.y_f32 = y_type == FQ_TYPE_F32;
     return device_status(fqimpl::launch_product_linear(p, (hipStream_t)stream), "linear launch");
 }
@@ -1900,6 +1928,8 @@ fq_status fq_glu_fwd(const fq_gate *gate, const void *x_bf16, const void *w_bf16
     FQ_TRY(check_ws(ws, ws_bytes, product_fwd_ws(d)));
     p.gate = g;
     p.y = h_bf16;
+    p.splits = fwd_splits(d);
+    p.partial = (float *)ws;
     return device_status(fqimpl::launch_product_glu(p, (hipStream_t)stream), "gated block launch");
 }
 

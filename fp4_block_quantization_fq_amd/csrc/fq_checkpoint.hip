@@ -100,9 +100,10 @@ __global__ __launch_bounds__(kBlock) void k_decode(RowArgs8 a, int64_t chunks)
 }
 
 // ---- gradient before the activation ----------------------------------------------------
-// A workgroup: kDzRows rows of a segment, 256 columns of the output (32 lanes of
-// eight columns, eight rows at a time).
-constexpr int kDzRows = fqimpl::kDzRows;
+// A workgroup: a tile of a segment's rows, 256 columns of the output (32 lanes of
+// eight columns, eight rows at a time).  Tiles have 64 rows; where that leaves CUs
+// without work (fewer than 512 workgroups), 8: 333 x 776 with GELU takes DZ_FEW us
+// so, 29 in tiles of 64.
 
 template <bool MX>
 __device__ __forceinline__ void load_pre(const DzArgs &a, int64_t at, float (&v)[8])
@@ -125,12 +126,12 @@ __global__ __launch_bounds__(kBlock) void k_dz(DzArgs a)
     __shared__ float sums[GLU ? 2 : 1][8][256 + 8];
     const int lane = threadIdx.x & 63;
     const int tile = blockIdx.x;
-    int row0 = tile * kDzRows, row_end = (int)a.rows, expert;
+    int row0 = tile * a.tile, row_end = (int)a.rows, expert;
     if (a.offsets) {
-        if (tile >= segment_tiles(a.offsets, a.experts, (int)a.rows, kDzRows, lane)) return;
-        find_segment(a.offsets, a.experts, (int)a.rows, kDzRows, tile, lane, &expert, &row0, &row_end);
+        if (tile >= segment_tiles(a.offsets, a.experts, (int)a.rows, a.tile, lane)) return;
+        find_segment(a.offsets, a.experts, (int)a.rows, a.tile, tile, lane, &expert, &row0, &row_end);
     }
-    row_end = row_end - row0 < kDzRows ? row_end : row0 + kDzRows;
+    row_end = row_end - row0 < a.tile ? row_end : row0 + a.tile;
     const int c = threadIdx.x & 31, r0 = threadIdx.x >> 5;
     const int64_t col = (int64_t)blockIdx.y * 256 + c * 8;
     const int64_t cols = GLU ? 2 * a.n : a.n;
@@ -185,27 +186,36 @@ __global__ __launch_bounds__(kBlock) void k_dz(DzArgs a)
     }
 }
 
-// dbias of one expert and 64 columns: its tiles' sums, four lanes' quarters of them.
+// dbias of one expert and COLS columns: its tiles' sums, 256 / COLS lanes a column,
+// joined in the order of the tiles' numbers modulo those.
+template <int COLS>
 __global__ __launch_bounds__(kBlock) void k_dbias(DzArgs a, int64_t cols)
 {
-    __shared__ float part[4][64];
-    const int lane = threadIdx.x & 63, quarter = threadIdx.x >> 6, expert = blockIdx.y;
-    int first = 0, count = (int)((a.rows + kDzRows - 1) / kDzRows);
+    constexpr int SLICES = kBlock / COLS;
+    __shared__ float part[SLICES][COLS + 1];
+    const int lane = threadIdx.x & 63, c = threadIdx.x % COLS, slice = threadIdx.x / COLS, expert = blockIdx.y;
+    int first = 0, count = (int)((a.rows + a.tile - 1) / a.tile);
     if (a.offsets) {
         int s, e;
-        first = segment_tiles(a.offsets, expert, (int)a.rows, kDzRows, lane);
+        first = segment_tiles(a.offsets, expert, (int)a.rows, a.tile, lane);
         segment_of(a.offsets, expert, (int)a.rows, &s, &e);
-        count = (e - s + kDzRows - 1) / kDzRows;
+        count = (e - s + a.tile - 1) / a.tile;
     }
-    const int64_t col = (int64_t)blockIdx.x * 64 + lane;
-    const int each = (count + 3) / 4, from = min(quarter * each, count), to = min(from + each, count);
+    const int64_t col = (int64_t)blockIdx.x * COLS + c;
     float t = 0.0f;
-    if (col < cols)
-        for (int i = from; i < to; ++i) t += a.partials[(int64_t)(first + i) * cols + col];
-    part[quarter][lane] = t;
+    if (col < cols) {
+        const float *p = a.partials + first * cols + col;
+#pragma unroll 4
+        for (int i = slice; i < count; i += SLICES) t += p[i * cols];
+    }
+    part[slice][c] = t;
     __syncthreads();
-    if (quarter == 0 && col < cols)
-        a.dbias[expert * cols + col] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+    if (slice == 0 && col < cols) {
+        t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < SLICES; ++i) t += part[i][c];
+        a.dbias[expert * cols + col] = t;
+    }
 }
 
 uint32_t flat_grid(int64_t chunks)
@@ -250,15 +260,22 @@ hipError_t launch_f8_decode(int f8, const RowArgs8 &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-int64_t dz_tiles(int64_t rows, int64_t experts)
+int dz_tile(int64_t rows, int64_t n)
 {
-    if (!experts) return (rows + kDzRows - 1) / kDzRows;
-    return rows / kDzRows + (experts < rows ? experts : rows);
+    return (rows + 63) / 64 * ((n + 255) / 256) >= 512 ? 64 : 8;
 }
 
-hipError_t launch_dz(const DzArgs &a, hipStream_t stream)
+int64_t dz_tiles(int64_t rows, int64_t n, int64_t experts)
 {
-    const dim3 grid((uint32_t)dz_tiles(a.rows, a.offsets ? a.experts : 0), (uint32_t)((a.n + 255) / 256));
+    const int64_t tile = dz_tile(rows, n);
+    if (!experts) return (rows + tile - 1) / tile;
+    return rows / tile + (experts < rows ? experts : rows);
+}
+
+hipError_t launch_dz(DzArgs a, hipStream_t stream)
+{
+    a.tile = dz_tile(a.rows, a.n);
+    const dim3 grid((uint32_t)dz_tiles(a.rows, a.n, a.offsets ? a.experts : 0), (uint32_t)((a.n + 255) / 256));
     const int64_t cols = a.glu ? 2 * a.n : a.n;
     if (a.glu && a.pre_kind == PRE_MX) hipLaunchKernelGGL((k_dz<true, true>), grid, dim3(kBlock), 0, stream, a);
     else if (a.glu) hipLaunchKernelGGL((k_dz<true, false>), grid, dim3(kBlock), 0, stream, a);
@@ -266,8 +283,12 @@ hipError_t launch_dz(const DzArgs &a, hipStream_t stream)
     else hipLaunchKernelGGL((k_dz<false, false>), grid, dim3(kBlock), 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.dbias) return e;
-    const dim3 joins((uint32_t)((cols + 63) / 64), (uint32_t)(a.offsets ? a.experts : 1));
-    hipLaunchKernelGGL(k_dbias, joins, dim3(kBlock), 0, stream, a, cols);
+    // one long list of tiles, or an expert's short ones
+    if (!a.offsets)
+        hipLaunchKernelGGL((k_dbias<16>), dim3((uint32_t)((cols + 15) / 16)), dim3(kBlock), 0, stream, a, cols);
+    else
+        hipLaunchKernelGGL((k_dbias<64>), dim3((uint32_t)((cols + 63) / 64), (uint32_t)a.experts), dim3(kBlock), 0,
+                           stream, a, cols);
     return hipGetLastError();
 }
 

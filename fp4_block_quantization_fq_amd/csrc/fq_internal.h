@@ -267,9 +267,20 @@ struct ProductArgs {
     int act;
     Gate gate;
     int group;               // tile rows that share a run of b (set by the launcher)
+    int splits;              // parts of the contraction, FP32 in `partial`; 0 or 1: none
+    int split_k;             // k of a part (set by the launcher)
+    float *partial;          // [splits, M, columns of b]
 };
+// fq_product_join.hip: parts worth making of one product, and their sum
+constexpr int kProductMaxSplits = 8;
+int product_splits(int64_t M, int64_t columns, int64_t K);
+hipError_t launch_product_join(ProductArgs p, int epilogue, const float *part, hipStream_t stream);
 hipError_t launch_product_linear(ProductArgs p, hipStream_t stream);
 hipError_t launch_product_glu(ProductArgs p, hipStream_t stream);      // N of each half
+// Rows (of an expert, on average) up to which the weight's bytes bound a forward.
+inline bool product_few_rows(int64_t rows, int64_t experts) { return rows <= 64 * (experts ? experts : 1); }
+hipError_t launch_product_few_linear(const ProductArgs &p, hipStream_t stream);      // fq_product_few.hip
+hipError_t launch_product_few_glu(const ProductArgs &p, hipStream_t stream);
 hipError_t launch_product_dx(ProductArgs p, hipStream_t stream);
 hipError_t launch_product_dw(ProductArgs p, hipStream_t stream);
 
@@ -283,7 +294,6 @@ struct RowArgs8 {
 };
 hipError_t launch_f8_encode(int f8, const RowArgs8 &a, hipStream_t stream);
 hipError_t launch_f8_decode(int f8, const RowArgs8 &a, hipStream_t stream);
-constexpr int kDzRows = 64;
 struct DzArgs {
     int glu;
     const void *dy;          // BF16 [rows, n]
@@ -298,8 +308,9 @@ struct DzArgs {
     void *h;                 // BF16 [rows, n] or null
     float *partials;         // [dz_tiles, n or 2n], or null without dbias
     float *dbias;            // [experts, n or 2n] or null
+    int tile;                // rows of a workgroup (set by the launcher)
 };
-int64_t dz_tiles(int64_t rows, int64_t experts);
-hipError_t launch_dz(const DzArgs &a, hipStream_t stream);
+int64_t dz_tiles(int64_t rows, int64_t n, int64_t experts);
+hipError_t launch_dz(DzArgs a, hipStream_t stream);
 
 }  // namespace fqimpl

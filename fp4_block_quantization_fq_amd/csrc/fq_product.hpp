@@ -219,20 +219,19 @@ __device__ __forceinline__ void store_y(const ProductArgs &p, int64_t at, const 
     else store8<false>((uint16_t *)p.y + at, 8, v);
 }
 
-// What becomes of eight sums (column `col` of row `row`, of N columns).
+// What becomes of eight sums (column `col` of row `row`, of N columns) and the
+// residual's values.
 __device__ __forceinline__ void finish_linear(const ProductArgs &p, int64_t row, int col, int N,
-                                              float (&z)[8], const float (&bias)[8])
+                                              float (&z)[8], const float (&bias)[8], const float (&res)[8])
 {
     const int64_t at = row * N + col;
-    float r[8] = {};
-    if (p.res) load_res(p, at, r);
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] += bias[i];
     if (p.pre_kind) keep_pre(p, at, z);
     act8(p.act, 1.0f, z);
     if (p.res) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] += r[i];
+        for (int i = 0; i < 8; ++i) z[i] += res[i];
     }
     store_y(p, at, z);
 }
@@ -274,7 +273,10 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
     const int tiles_n = (p.N + BNC - 1) / BNC;
     int tiles_m = (p.M + BM - 1) / BM;
     if (p.offsets) tiles_m = SEGK ? tiles_m * p.experts : segment_tiles(p.offsets, p.experts, p.rows, BM, lane);
-    const int total = tiles_m * tiles_n, b = (int)blockIdx.x;
+    const int total = tiles_m * tiles_n;
+    // part of the contraction (of one product, stored as FP32 partial sums)
+    const int split = EPI == EPI_STORE && p.splits > 1 ? (int)blockIdx.x / total : 0;
+    const int b = (int)blockIdx.x - split * total;
     if (b >= total) return;
     // the hardware deals workgroups round-robin to eight XCDs, each with its own
     // L2: a contiguous run of tiles each
@@ -300,13 +302,17 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
         find_segment(p.offsets, p.experts, p.rows, BM, tm, lane, &expert, &row0, &row_end);
     }
     const int col0 = tn * BNC;
+    if (EPI == EPI_STORE && p.splits > 1) {
+        k_begin = split * p.split_k;
+        k_end = min(k_begin + p.split_k, p.K);
+    }
 
     Tile<LA, BM, WAVES> ta;
     Tile<LB, BN, WAVES> tb;
     const uint16_t *pa = p.a, *pb = p.b + (SEGK ? 0 : expert * p.b_stride);
-    if (SEGK) {
-        pa += (int64_t)k_begin * p.lda;
-        pb += (int64_t)k_begin * p.ldb;
+    if (SEGK || EPI == EPI_STORE) {
+        pa += k_begin * (LA == ACROSS ? p.lda : 1);
+        pb += k_begin * (LB == ACROSS ? p.ldb : 1);
     }
     ta.template init<false>(pa, p.lda, row0, row_end, 0, wave, lane);
     tb.template init<EPI == EPI_GLU>(pb, p.ldb, col0, p.N, p.N, wave, lane);
@@ -405,31 +411,34 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
     // Epilogue: 32 rows at a time through this wave's part of the idle stages, so
     // that a lane gets eight neighbouring columns.  Element v of lane l of an
     // accumulator is row v / 4 * 8 + l / 32 * 4 + v % 4, column l % 32.
-    constexpr int WCOLS = TN * 32, CHUNKS = EPI == EPI_GLU ? WCOLS / 16 : WCOLS / 8, PASSES = 32 * CHUNKS / 64;
+    constexpr int WCOLS = TN * 32, CHUNKS = EPI == EPI_GLU ? WCOLS / 16 : WCOLS / 8;
+    constexpr int STEP = 64 / CHUNKS, PASSES = (32 + STEP - 1) / STEP;      // whole rows a pass: a lane keeps its columns
     constexpr int SLAB = 32 * WCOLS * 4;
     static_assert(WAVES / 2 * SLAB <= STAGE && WAVES % 2 == 0, "a slab for every wave");
     float *slab = reinterpret_cast<float *>((wave < WAVES / 2 ? lds0 : lds1) + wave % (WAVES / 2) * SLAB);
-    const int wcol0 = col0 + wn * (EPI == EPI_GLU ? WCOLS / 2 : WCOLS);
-    auto chunk_at = [&](int i, int k, int *r, int *c, int64_t *row, int *col) {
-        const int id = k * 64 + lane;
-        *r = id / CHUNKS;
-        *c = id % CHUNKS * 8;
-        *row = (int64_t)row0 + (wm * TM + i) * 32 + *r;
-        *col = wcol0 + *c;
-        return *row < row_end && *col < p.N;
+    const int c = lane % CHUNKS * 8, r0 = lane / CHUNKS;
+    const int col = col0 + wn * (EPI == EPI_GLU ? WCOLS / 2 : WCOLS) + c;
+    const bool mine = col < p.N && r0 < STEP;
+    auto inside = [&](int i, int k) {
+        const int r = k * STEP + r0;
+        return mine && r < 32 && row0 + (wm * TM + i) * 32 + r < row_end;
     };
+    auto row_of = [&](int i, int k) { return (int64_t)row0 + (wm * TM + i) * 32 + k * STEP + r0; };
+    auto slab_at = [&](int k) { return slab + min(k * STEP + r0, 31) * WCOLS; };
+    float bias[8] = {}, bias_up[8] = {};
+    if (EPI != EPI_STORE && mine) {
+        const int64_t at = (int64_t)expert * (EPI == EPI_GLU ? 2 : 1) * p.N + col;
+        load_bias(p, at, bias);
+        if (EPI == EPI_GLU) load_bias(p, at + p.N, bias_up);
+    }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         // residuals first, so that their loads overlap
         Raw8<uint16_t> res16[EPI == EPI_RES ? PASSES : 1];
         if (EPI == EPI_RES && p.res && !p.y_f32) {
 #pragma unroll
-            for (int k = 0; k < PASSES; ++k) {
-                int r, c, col;
-                int64_t row;
-                if (chunk_at(i, k, &r, &c, &row, &col))
-                    load_raw8<false>((const uint16_t *)p.res + row * p.N + col, 8, res16[k]);
-            }
+            for (int k = 0; k < PASSES; ++k)
+                if (inside(i, k)) load_raw8<false>((const uint16_t *)p.res + row_of(i, k) * p.N + col, 8, res16[k]);
         }
 #pragma unroll
         for (int j = 0; j < TN; ++j)
@@ -441,16 +450,12 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
         if (EPI == EPI_STORE || EPI == EPI_RES) {
 #pragma unroll
             for (int k = 0; k < PASSES; ++k) {
-                int r, c, col;
-                int64_t row;
-                const bool in = chunk_at(i, k, &r, &c, &row, &col);
                 float z[8];
-                load8<false>(slab + r * WCOLS + c, 8, z);
-                if (!in) continue;
-                const int64_t at = (SEGK ? (int64_t)expert * p.M * p.N : 0) + row * p.N + col;
+                load8<false>(slab_at(k) + c, 8, z);
+                if (!inside(i, k)) continue;
+                const int64_t at = (EPI == EPI_STORE ? (int64_t)(expert * SEGK + split) * p.M * p.N : 0) +
+                                   row_of(i, k) * p.N + col;
                 if (EPI == EPI_RES) {
-                    float bias[8];
-                    load_bias(p, (int64_t)expert * p.N + col, bias);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) z[e] += bias[e];
                     if (p.res) {
@@ -464,29 +469,27 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
                 store_y(p, at, z);
             }
         } else {
-            // not unrolled: the activations' code is long
+            // two rows a turn, not unrolled further: the activations' code is long
 #pragma unroll 1
-            for (int k = 0; k < PASSES; ++k) {
-                int r, c, col;
-                int64_t row;
-                const bool in = chunk_at(i, k, &r, &c, &row, &col);
-                float z[8], u[8];
-                if (EPI == EPI_GLU) {
-                    const float *s = slab + r * WCOLS + (c >> 5) * 64 + (c & 31);
-                    load8<false>(s, 8, z);
-                    load8<false>(s + 32, 8, u);
-                } else {
-                    load8<false>(slab + r * WCOLS + c, 8, z);
+            for (int k = 0; k < PASSES; k += 2) {
+                float z[2][8], u[2][8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float *at = slab_at(k + h);
+                    if (EPI == EPI_GLU) {
+                        at += (c >> 5) * 64 + (c & 31);
+                        load8<false>(at, 8, z[h]);
+                        load8<false>(at + 32, 8, u[h]);
+                    } else {
+                        load8<false>(at + c, 8, z[h]);
+                        if (p.res && inside(i, k + h)) load_res(p, row_of(i, k + h) * p.N + col, u[h]);
+                    }
                 }
-                if (!in) continue;
-                float bias[8], bias_up[8];
-                const int64_t at = (int64_t)expert * (EPI == EPI_GLU ? 2 : 1) * p.N + col;
-                load_bias(p, at, bias);
-                if (EPI == EPI_GLU) {
-                    load_bias(p, at + p.N, bias_up);
-                    finish_glu(p, row, col, p.N, z, u, bias, bias_up);
-                } else {
-                    finish_linear(p, row, col, p.N, z, bias);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!inside(i, k + h)) continue;
+                    if (EPI == EPI_GLU) finish_glu(p, row_of(i, k + h), col, p.N, z[h], u[h], bias, bias_up);
+                    else finish_linear(p, row_of(i, k + h), col, p.N, z[h], bias, u[h]);
                 }
             }
         }
@@ -533,9 +536,25 @@ template <int LA, int LB, int TM, int TN, int WM, int WN, int EPI, bool SEGK>
 hipError_t launch_tiles(const ProductArgs &p, hipStream_t stream)
 {
     constexpr int BM = WM * TM * 32, BN = WN * TN * 32 / (EPI == EPI_GLU ? 2 : 1);
-    hipLaunchKernelGGL((k_product<LA, LB, TM, TN, WM, WN, EPI, SEGK>),
-                       dim3((uint32_t)product_tiles<SEGK>(p, BM, BN)), dim3(64 * WM * WN), 0, stream, p);
+    const int64_t n = product_tiles<SEGK>(p, BM, BN) * (p.splits > 1 ? p.splits : 1);
+    hipLaunchKernelGGL((k_product<LA, LB, TM, TN, WM, WN, EPI, SEGK>), dim3((uint32_t)n), dim3(64 * WM * WN), 0,
+                       stream, p);
     return hipGetLastError();
+}
+
+// One product of few tiles: its parts to the workspace (`columns` of B), then joined
+// as `epilogue` says.
+template <int LA, int LB, bool SEGK>
+hipError_t launch_split(const ProductArgs &p, int columns, int epilogue, hipStream_t stream)
+{
+    ProductArgs q = p;
+    q.N = columns;
+    q.res = nullptr;
+    q.y = p.partial;
+    q.y_f32 = 1;
+    q.split_k = ((p.K + 63) / 64 + p.splits - 1) / p.splits * 64;
+    hipError_t e = launch_tiles<LA, LB, 2, 2, 2, 2, EPI_STORE, SEGK>(q, stream);
+    return e != hipSuccess ? e : fqimpl::launch_product_join(p, epilogue, p.partial, stream);
 }
 
 }  // namespace

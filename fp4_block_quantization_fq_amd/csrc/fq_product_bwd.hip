@@ -7,6 +7,7 @@ namespace fqimpl {
 hipError_t launch_product_dx(ProductArgs p, hipStream_t stream)
 {
     p.group = p.offsets ? 2 : 8;
+    if (p.splits > 1) return launch_split<ALONG, ALONG, false>(p, p.N, EPI_STORE, stream);
     const float big = product_time<false>(p, 256, 256, 1, 1.44f, 10.0f);
     const float wide = product_time<false>(p, 256, 192, 1, 1.13f, 10.0f);
     const float small = product_time<false>(p, 128, 128, 2, 0.90f, 7.0f);
@@ -17,6 +18,7 @@ hipError_t launch_product_dx(ProductArgs p, hipStream_t stream)
 hipError_t launch_product_dw(ProductArgs p, hipStream_t stream)
 {
     p.group = 8;
+    if (p.splits > 1) return launch_split<ACROSS, ACROSS, true>(p, p.N, EPI_STORE, stream);
     const float big = product_time<true>(p, 256, 256, 1, 1.44f, 10.0f);
     const float mid = product_time<true>(p, 192, 192, 1, 0.96f, 9.0f);
     const float small = product_time<true>(p, 128, 128, 2, 0.95f, 7.0f);

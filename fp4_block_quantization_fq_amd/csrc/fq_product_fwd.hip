@@ -3,6 +3,10 @@
 
 namespace {
 
+using fqimpl::product_few_rows;
+
+bool few_rows(const ProductArgs &p) { return product_few_rows(p.M, p.offsets ? p.experts : 0); }
+
 template <int EPI>
 hipError_t launch_linear(const ProductArgs &p, hipStream_t stream)
 {
@@ -21,12 +25,16 @@ namespace fqimpl {
 hipError_t launch_product_linear(ProductArgs p, hipStream_t stream)
 {
     p.group = p.offsets ? 2 : 8;
+    if (few_rows(p)) return launch_product_few_linear(p, stream);
+    if (p.splits > 1) return launch_split<ALONG, ACROSS, false>(p, p.N, EPI_LINEAR, stream);
     if (p.act == ACT_NONE && p.pre_kind == PRE_NONE) return launch_linear<EPI_RES>(p, stream);
     return launch_linear<EPI_LINEAR>(p, stream);
 }
 hipError_t launch_product_glu(ProductArgs p, hipStream_t stream)
 {
     p.group = p.offsets ? 2 : 8;
+    if (few_rows(p)) return launch_product_few_glu(p, stream);
+    if (p.splits > 1) return launch_split<ALONG, ACROSS, false>(p, 2 * p.N, EPI_GLU, stream);
     const float big = product_time<false>(p, 256, 128, 1, 1.46f, 15.0f);
     const float small = product_time<false>(p, 128, 64, 2, 0.90f, 10.0f);
     if (small <= big) return launch_tiles<ALONG, ACROSS, 2, 2, 2, 2, EPI_GLU, false>(p, stream);

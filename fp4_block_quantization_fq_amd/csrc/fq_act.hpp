@@ -9,6 +9,8 @@
 // have it.
 #pragma once
 
+#include <type_traits>
+
 #include "fq_internal.h"
 #include "fq_rows.hpp"
 
@@ -41,69 +43,99 @@ __device__ __forceinline__ float normal_cdf(float z, float *e)
 }
 
 // a(z) and a'(z)
-__device__ __forceinline__ float act1(int act, float alpha, float z)
+template <int ACT>
+__device__ __forceinline__ float act_of(float alpha, float z)
 {
-    if (act == fqimpl::ACT_SILU) return z * sigmoid(alpha * z);
-    if (act == fqimpl::ACT_GELU) {
+    if (ACT == fqimpl::ACT_SILU) return z * sigmoid(alpha * z);
+    if (ACT == fqimpl::ACT_GELU) {
         float e;
         return z * normal_cdf(z, &e);
     }
-    if (act == fqimpl::ACT_RELU) return z <= 0.0f ? 0.0f : z;
+    if (ACT == fqimpl::ACT_RELU) return z <= 0.0f ? 0.0f : z;
     return z;
 }
-__device__ __forceinline__ float act1_grad(int act, float alpha, float z, float *value)
+template <int ACT>
+__device__ __forceinline__ float act_grad_of(float alpha, float z, float *value)
 {
-    if (act == fqimpl::ACT_SILU) {
+    if (ACT == fqimpl::ACT_SILU) {
         const float s = sigmoid(alpha * z);
         *value = z * s;
         return s * (1.0f + alpha * z * (1.0f - s));
     }
-    if (act == fqimpl::ACT_GELU) {
+    if (ACT == fqimpl::ACT_GELU) {
         float e;
         const float phi = normal_cdf(z, &e);
         *value = z * phi;
         return phi + z * (0.39894228040143268f * e);
     }
-    if (act == fqimpl::ACT_RELU) {
+    if (ACT == fqimpl::ACT_RELU) {
         *value = z <= 0.0f ? 0.0f : z;
         return z <= 0.0f ? 0.0f : 1.0f;
     }
     *value = z;
     return 1.0f;
 }
-__device__ __forceinline__ void act8(int act, float alpha, float (&z)[8])
+
+// The choice of the activation stands around the eight values, so that their chains
+// of instructions interleave (inside, a branch before each of them cost 7 us in a
+// call of 27).
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F run)
 {
-    if (act == fqimpl::ACT_NONE) return;
+    if (act == fqimpl::ACT_SILU) run(std::integral_constant<int, fqimpl::ACT_SILU>());
+    else if (act == fqimpl::ACT_GELU) run(std::integral_constant<int, fqimpl::ACT_GELU>());
+    else if (act == fqimpl::ACT_RELU) run(std::integral_constant<int, fqimpl::ACT_RELU>());
+    else run(std::integral_constant<int, fqimpl::ACT_NONE>());
+}
+template <int N>
+__device__ __forceinline__ void act_n(int act, float alpha, float (&z)[N])
+{
+    with_act(act, [&](auto kind) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = act1(act, alpha, z[i]);
+        for (int i = 0; i < N; ++i) z[i] = act_of<decltype(kind)::value>(alpha, z[i]);
+    });
+}
+// dy *= a'(z)
+__device__ __forceinline__ void act8_grad(int act, const float (&z)[8], float (&dy)[8])
+{
+    with_act(act, [&](auto kind) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float value;
+            dy[i] *= act_grad_of<decltype(kind)::value>(1.0f, z[i], &value);
+        }
+    });
 }
 
-// a(min(g, limit)) (clamp(u, -limit, limit) + shift); NaN stays NaN
-__device__ __forceinline__ float glu1(const Gate &t, float g, float u)
+// g = a(min(g, limit)) (clamp(u, -limit, limit) + shift); NaN stays NaN
+template <int N>
+__device__ __forceinline__ void glu_n(const Gate &t, float (&g)[N], const float (&u)[N])
 {
-    const float gate = g > t.limit ? t.limit : g;
-    const float up = u > t.limit ? t.limit : u < -t.limit ? -t.limit : u;
-    return act1(t.act, t.alpha, gate) * (up + t.shift);
-}
-__device__ __forceinline__ void glu8(const Gate &t, float (&g)[8], const float (&u)[8])
-{
+    with_act(t.act, [&](auto kind) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = glu1(t, g[i], u[i]);
+        for (int i = 0; i < N; ++i) {
+            const float gate = g[i] > t.limit ? t.limit : g[i];
+            const float up = u[i] > t.limit ? t.limit : u[i] < -t.limit ? -t.limit : u[i];
+            g[i] = act_of<decltype(kind)::value>(t.alpha, gate) * (up + t.shift);
+        }
+    });
 }
 // Its backward for the gradient dh: dg and du into g and u, h's value into dh.
 __device__ __forceinline__ void glu8_grad(const Gate &t, float (&g)[8], float (&u)[8], float (&dh)[8])
 {
+    with_act(t.act, [&](auto kind) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const bool g_out = g[i] > t.limit, u_out = u[i] > t.limit || u[i] < -t.limit;
-        const float gate = g_out ? t.limit : g[i];
-        const float up = (u[i] > t.limit ? t.limit : u[i] < -t.limit ? -t.limit : u[i]) + t.shift;
-        float a;
-        const float da = act1_grad(t.act, t.alpha, gate, &a);
-        g[i] = g_out ? 0.0f : dh[i] * up * da;
-        u[i] = u_out ? 0.0f : dh[i] * a;
-        dh[i] = a * up;
-    }
+        for (int i = 0; i < 8; ++i) {
+            const bool g_out = g[i] > t.limit, u_out = u[i] > t.limit || u[i] < -t.limit;
+            const float gate = g_out ? t.limit : g[i];
+            const float up = (u[i] > t.limit ? t.limit : u[i] < -t.limit ? -t.limit : u[i]) + t.shift;
+            float a;
+            const float da = act_grad_of<decltype(kind)::value>(t.alpha, gate, &a);
+            g[i] = g_out ? 0.0f : dh[i] * up * da;
+            u[i] = u_out ? 0.0f : dh[i] * a;
+            dh[i] = a * up;
+        }
+    });
 }
 
 // ---- 8-bit blocks ------------------------------------------------------------------

@@ -156,11 +156,7 @@ __global__ __launch_bounds__(kBlock) void k_dz(DzArgs a)
             } else {
                 if (a.pre) {
                     load_pre<MX>(a, at, g);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float value;
-                        d[e] *= act1_grad(a.gate.act, 1.0f, g[e], &value);
-                    }
+                    act8_grad(a.gate.act, g, d);
                     store8<false>((uint16_t *)a.dz + at, 8, d);
                 }
 #pragma unroll

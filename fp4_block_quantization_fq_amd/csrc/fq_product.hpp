@@ -228,7 +228,7 @@ __device__ __forceinline__ void finish_linear(const ProductArgs &p, int64_t row,
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] += bias[i];
     if (p.pre_kind) keep_pre(p, at, z);
-    act8(p.act, 1.0f, z);
+    act_n(p.act, 1.0f, z);
     if (p.res) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] += res[i];
@@ -249,7 +249,7 @@ __device__ __forceinline__ void finish_glu(const ProductArgs &p, int64_t row, in
         keep_pre(p, row * 2 * n + col, g);
         keep_pre(p, row * 2 * n + n + col, u);
     }
-    glu8(p.gate, g, u);
+    glu_n(p.gate, g, u);
     store8<false>((uint16_t *)p.y + row * n + col, 8, g);
 }
 

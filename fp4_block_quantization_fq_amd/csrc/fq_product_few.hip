@@ -145,21 +145,22 @@ __global__ __launch_bounds__(64 * WAVES) void k_product_few(const ProductArgs p)
             const int r = e / BNC, c = e % BNC;
             if (i * 16 + r >= rows || col0 + c >= p.N) continue;
             const int64_t at = (int64_t)expert * (EPI == EPI_GLU ? 2 : 1) * p.N + col0 + c;
-            float z = 0.0f, u = 0.0f;
+            float z[1] = {0.0f}, u[1] = {0.0f};
 #pragma unroll
             for (int q = 0; q < WAVES; ++q) {
-                z += join.part[q][r][c];
-                if (EPI == EPI_GLU) u += join.part[q][r][BNC + c];
+                z[0] += join.part[q][r][c];
+                if (EPI == EPI_GLU) u[0] += join.part[q][r][BNC + c];
             }
-            z += bias1(p, at);
-            join.z[r][c] = z;
+            z[0] += bias1(p, at);
+            join.z[r][c] = z[0];
             if (EPI == EPI_GLU) {
-                u += bias1(p, at + p.N);
-                join.z[r][BNC + c] = u;
-                join.y[r][c] = glu1(p.gate, z, u);
+                u[0] += bias1(p, at + p.N);
+                join.z[r][BNC + c] = u[0];
+                glu_n(p.gate, z, u);
             } else {
-                join.y[r][c] = act1(p.act, 1.0f, z);
+                act_n(p.act, 1.0f, z);
             }
+            join.y[r][c] = z[0];
         }
         __syncthreads();
         for (int e = tid; e < 16 * CHUNKS; e += 64 * WAVES) {

@@ -254,17 +254,16 @@ __device__ __forceinline__ void finish_glu(const ProductArgs &p, int64_t row, in
 }
 
 // ---- the kernel ----------------------------------------------------------------------
-// WM x WN waves of TM x TN accumulator tiles of 32 x 32.  SEGK: the experts'
-// segments are of the contraction (dw), else of C's rows.
-template <int LA, int LB, int TM, int TN, int WM, int WN, int EPI, bool SEGK>
+// WM x WN waves of TM x TN accumulator tiles of 32 x 32, STAGES buffers of 64 k.
+// SEGK: the experts' segments are of the contraction (dw), else of C's rows.
+template <int LA, int LB, int TM, int TN, int WM, int WN, int STAGES, int EPI, bool SEGK>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p)
 {
     constexpr int BM = WM * TM * 32, BN = WN * TN * 32, WAVES = WM * WN;
     constexpr int BNC = EPI == EPI_GLU ? BN / 2 : BN;      // columns of the output
     constexpr int A_BYTES = BM * 128, STAGE = A_BYTES + BN * 128;
     static_assert(EPI != EPI_GLU || TN % 2 == 0, "32 columns of either half next to each other");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds0[STAGE];
-    __shared__ __attribute__((aligned(1024))) uint8_t lds1[STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES][STAGE];
 
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int wm = wave / WN, wn = wave % WN;
@@ -329,9 +328,12 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
     constexpr int READS = TM + TN, MFMAS = TM * TN, HALF = LOADS / 2;
     static_assert(MFMAS >= READS, "a product in front of every read");
     bf16x8 fa[2][TM], fb[2][TN];
-    const uint32_t to_a[2] = {lds_address(lds0) + wave * NA * 1024, lds_address(lds1) + wave * NA * 1024};
-    const uint32_t to_b[2] = {lds_address(lds0) + A_BYTES + wave * (LOADS - NA) * 1024,
-                              lds_address(lds1) + A_BYTES + wave * (LOADS - NA) * 1024};
+    const uint32_t to_a = lds_address(lds) + wave * NA * 1024;
+    const uint32_t to_b = lds_address(lds) + A_BYTES + wave * (LOADS - NA) * 1024;
+    // a wave all of whose rows or columns lie behind the end only loads: the other
+    // wave of its SIMD then has the matrix cores for itself
+    const bool idle = row0 + wm * TM * 32 >= row_end ||
+                      col0 + wn * (EPI == EPI_GLU ? TN * 16 : TN * 32) >= p.N;
     int left = k_end - k_begin;                // of the contraction
 
     // fragment n of a substep, in the order of their first use: b0 a0 b1 b2 .. a1 a2 ..
@@ -347,66 +349,98 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
     // load n of a stage into buffer `buf`; `have` k of it exist (not looked at if FULL)
     auto load = [&](int buf, int n, int have, bool full) {
         if (n < NA) {
-            if (full) ta.issue(to_a[buf], n);
-            else if (have > 0) ta.issue(to_a[buf], n, have, wave, lane);
+            if (full) ta.issue(to_a + buf * STAGE, n);
+            else if (have > 0) ta.issue(to_a + buf * STAGE, n, have, wave, lane);
         } else {
-            if (full) tb.issue(to_b[buf], n - NA);
-            else if (have > 0) tb.issue(to_b[buf], n - NA, have, wave, lane);
+            if (full) tb.issue(to_b + buf * STAGE, n - NA);
+            else if (have > 0) tb.issue(to_b + buf * STAGE, n - NA, have, wave, lane);
         }
     };
     // One substep: its products from fragments `from`; between them the reads of
-    // the next one's from `lds` and `count` loads from number `first` on.
-    auto substep = [&](int from, bool reads, const uint8_t *lds, int ks, int buf, int first, int count,
+    // the next one's from `at` and `count` loads from number `first` on.
+    auto substep = [&](int from, bool reads, const uint8_t *at, int ks, int buf, int first, int count,
                        int have, bool full) {
 #pragma unroll
         for (int q = 0; q < MFMAS; ++q) {
             const int i = q / TN, j = q % TN;
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[from][i], fb[from][j], acc[i][j], 0, 0, 0);
-            if (reads && q < READS) read(lds, ks, 1 - from, q);
+            if (reads && q < READS) read(at, ks, 1 - from, q);
 #pragma unroll
             for (int n = 0; n < LOADS; ++n)
                 if (n < count && n * MFMAS / count == q) load(buf, first + n, have, full);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+    // the next stage has landed (of the loads in flight, `behind` are of later ones),
+    // and this wave has read all of this one
+    auto turn = [&](bool behind) {
+        if (behind) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"((STAGES - 2) * LOADS) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    // Stage in buffer `cur`; FULL: STAGES more of 64 k follow it at least.
     auto stage = [&](int cur, bool full) {
-        const uint8_t *here = cur ? lds1 : lds0, *there = cur ? lds0 : lds1;
-        const int next = left - BK, after = left - 2 * BK;        // k of the next two stages
-        substep(0, true, here, 1, 1 - cur, HALF, LOADS - HALF, next, full);
+        const uint8_t *here = lds[cur], *there = lds[(cur + 1) % STAGES];
+        const int next = left - BK;                                // k of the next stage
+        const int rest = left - (STAGES - 1) * BK, after = left - STAGES * BK;
+        substep(0, true, here, 1, (cur + STAGES - 1) % STAGES, HALF, LOADS - HALF, rest, full);
         substep(1, true, here, 2, 0, 0, 0, 0, true);
         substep(0, true, here, 3, 0, 0, 0, 0, true);
         ta.base += ta.step;
         tb.base += tb.step;
-        if (full || next > 0) {
-            // the next stage has landed, and this wave has read all of this one
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-        }
+        if (full || next > 0) turn(full);
         substep(1, full || next > 0, there, 0, cur, 0, HALF, after, full);
         left -= BK;
     };
-    if (left > 0) {
+    auto stage_idle = [&](int cur) {
+        const int rest = left - (STAGES - 1) * BK, after = left - STAGES * BK;
 #pragma unroll
-        for (int n = 0; n < LOADS; ++n) load(0, n, left, false);
+        for (int n = HALF; n < LOADS; ++n) load((cur + STAGES - 1) % STAGES, n, rest, false);
         ta.base += ta.step;
         tb.base += tb.step;
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
+        if (left > BK) turn(false);
 #pragma unroll
-        for (int n = 0; n < HALF; ++n) load(1, n, left - BK, false);
+        for (int n = 0; n < HALF; ++n) load(cur, n, after, false);
+        left -= BK;
+    };
+    if (left > 0) {
+        // the first STAGES - 1 stages and the first half of the next one's loads
 #pragma unroll
-        for (int n = 0; n < READS; ++n) read(lds0, 0, 0, n);
-        while (left >= 4 * BK) {               // all loads of both stages are whole
-            stage(0, true);
-            stage(1, true);
+        for (int s = 0; s < STAGES - 1; ++s) {
+#pragma unroll
+            for (int n = 0; n < LOADS; ++n) load(s, n, left - s * BK, false);
+            ta.base += ta.step;
+            tb.base += tb.step;
         }
-        while (left > 0) {
-            stage(0, false);
-            if (left > 0) stage(1, false);
+        if (left >= (STAGES - 1) * BK) asm volatile("s_waitcnt vmcnt(%0)" : : "n"((STAGES - 2) * LOADS) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int n = 0; n < HALF; ++n) load(STAGES - 1, n, left - (STAGES - 1) * BK, false);
+        if (idle) {
+            while (left > 0) {
+#pragma unroll
+                for (int s = 0; s < STAGES; ++s)
+                    if (left > 0) stage_idle(s);
+            }
+        } else {
+#pragma unroll
+            for (int n = 0; n < READS; ++n) read(lds[0], 0, 0, n);
+            while (left >= 2 * STAGES * BK) {  // all loads of these stages are whole
+#pragma unroll
+                for (int s = 0; s < STAGES; ++s) stage(s, true);
+            }
+            while (left > 0) {
+#pragma unroll
+                for (int s = 0; s < STAGES; ++s)
+                    if (left > 0) stage(s, false);
+            }
         }
         __syncthreads();
     }
+    if (idle) return;                          // no barrier follows
 
     // Epilogue: 32 rows at a time through this wave's part of the idle stages, so
     // that a lane gets eight neighbouring columns.  Element v of lane l of an
@@ -414,8 +448,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
     constexpr int WCOLS = TN * 32, CHUNKS = EPI == EPI_GLU ? WCOLS / 16 : WCOLS / 8;
     constexpr int STEP = 64 / CHUNKS, PASSES = (32 + STEP - 1) / STEP;      // whole rows a pass: a lane keeps its columns
     constexpr int SLAB = 32 * WCOLS * 4;
-    static_assert(WAVES / 2 * SLAB <= STAGE && WAVES % 2 == 0, "a slab for every wave");
-    float *slab = reinterpret_cast<float *>((wave < WAVES / 2 ? lds0 : lds1) + wave % (WAVES / 2) * SLAB);
+    static_assert(WAVES * SLAB <= STAGES * STAGE, "a slab for every wave");
+    float *slab = reinterpret_cast<float *>(&lds[0][0] + wave * SLAB);
     const int c = lane % CHUNKS * 8, r0 = lane / CHUNKS;
     const int col = col0 + wn * (EPI == EPI_GLU ? WCOLS / 2 : WCOLS) + c;
     const bool mine = col < p.N && r0 < STEP;
@@ -532,14 +566,24 @@ float product_time(const ProductArgs &p, int bm, int bn, int per_cu, float step,
     return rounds * (ceilf(k / 64) * step + fixed);
 }
 
-template <int LA, int LB, int TM, int TN, int WM, int WN, int EPI, bool SEGK>
+template <int LA, int LB, int TM, int TN, int WM, int WN, int STAGES, int EPI, bool SEGK>
 hipError_t launch_tiles(const ProductArgs &p, hipStream_t stream)
 {
     constexpr int BM = WM * TM * 32, BN = WN * TN * 32 / (EPI == EPI_GLU ? 2 : 1);
     const int64_t n = product_tiles<SEGK>(p, BM, BN) * (p.splits > 1 ? p.splits : 1);
-    hipLaunchKernelGGL((k_product<LA, LB, TM, TN, WM, WN, EPI, SEGK>), dim3((uint32_t)n), dim3(64 * WM * WN), 0,
+    hipLaunchKernelGGL((k_product<LA, LB, TM, TN, WM, WN, STAGES, EPI, SEGK>), dim3((uint32_t)n), dim3(64 * WM * WN), 0,
                        stream, p);
     return hipGetLastError();
+}
+
+// Tiles of 128 x 128: two workgroups a CU, or one with four stages where there is no
+// second one to fill its waits.
+template <int LA, int LB, int EPI, bool SEGK>
+hipError_t launch_small(const ProductArgs &p, hipStream_t stream)
+{
+    const int64_t n = product_tiles<SEGK>(p, 128, EPI == EPI_GLU ? 64 : 128) * (p.splits > 1 ? p.splits : 1);
+    if (n <= 256) return launch_tiles<LA, LB, 2, 2, 2, 2, 4, EPI, SEGK>(p, stream);
+    return launch_tiles<LA, LB, 2, 2, 2, 2, 2, EPI, SEGK>(p, stream);
 }
 
 // One product of few tiles: its parts to the workspace (`columns` of B), then joined
@@ -553,7 +597,7 @@ hipError_t launch_split(const ProductArgs &p, int columns, int epilogue, hipStre
     q.y = p.partial;
     q.y_f32 = 1;
     q.split_k = ((p.K + 63) / 64 + p.splits - 1) / p.splits * 64;
-    hipError_t e = launch_tiles<LA, LB, 2, 2, 2, 2, EPI_STORE, SEGK>(q, stream);
+    hipError_t e = launch_small<LA, LB, EPI_STORE, SEGK>(q, stream);
     return e != hipSuccess ? e : fqimpl::launch_product_join(p, epilogue, p.partial, stream);
 }
 

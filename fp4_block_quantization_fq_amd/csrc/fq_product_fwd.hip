@@ -13,9 +13,9 @@ hipError_t launch_linear(const ProductArgs &p, hipStream_t stream)
     const float big = product_time<false>(p, 256, 256, 1, 1.46f, 12.0f);
     const float wide = product_time<false>(p, 256, 192, 1, 1.15f, 10.0f);
     const float small = product_time<false>(p, 128, 128, 2, 0.90f, 8.0f);
-    if (small <= big && small <= wide) return launch_tiles<ALONG, ACROSS, 2, 2, 2, 2, EPI, false>(p, stream);
-    if (big <= wide) return launch_tiles<ALONG, ACROSS, 4, 2, 2, 4, EPI, false>(p, stream);
-    return launch_tiles<ALONG, ACROSS, 4, 3, 2, 2, EPI, false>(p, stream);
+    if (small <= big && small <= wide) return launch_small<ALONG, ACROSS, EPI, false>(p, stream);
+    if (big <= wide) return launch_tiles<ALONG, ACROSS, 4, 2, 2, 4, 2, EPI, false>(p, stream);
+    return launch_tiles<ALONG, ACROSS, 4, 3, 2, 2, 2, EPI, false>(p, stream);
 }
 
 }  // namespace
@@ -37,8 +37,8 @@ hipError_t launch_product_glu(ProductArgs p, hipStream_t stream)
     if (p.splits > 1) return launch_split<ALONG, ACROSS, false>(p, 2 * p.N, EPI_GLU, stream);
     const float big = product_time<false>(p, 256, 128, 1, 1.46f, 15.0f);
     const float small = product_time<false>(p, 128, 64, 2, 0.90f, 10.0f);
-    if (small <= big) return launch_tiles<ALONG, ACROSS, 2, 2, 2, 2, EPI_GLU, false>(p, stream);
-    return launch_tiles<ALONG, ACROSS, 4, 2, 2, 4, EPI_GLU, false>(p, stream);
+    if (small <= big) return launch_small<ALONG, ACROSS, EPI_GLU, false>(p, stream);
+    return launch_tiles<ALONG, ACROSS, 4, 2, 2, 4, 2, EPI_GLU, false>(p, stream);
 }
 
 }  // namespace fqimpl

@@ -21,16 +21,19 @@ using fqimpl::DzArgs;
 constexpr int kBlock = 256;
 
 // ---- 8-bit rows --------------------------------------------------------------------
-// MX blocks know nothing of rows: chunk after chunk of eight elements.
+// MX blocks know nothing of rows: chunk after chunk of eight elements.  NT: streaming
+// accesses, where the call's data exceeds the caches.
+template <bool NT>
 __global__ __launch_bounds__(kBlock) void k_encode_mx(RowArgs8 a, int64_t chunks)
 {
     const int64_t step = (int64_t)gridDim.x * kBlock;
     for (int64_t c = (int64_t)blockIdx.x * kBlock + threadIdx.x; c < chunks; c += step) {
         float v[8];
-        load8<false>((const uint16_t *)a.x + c * 8, 8, v);
+        load8<false, NT>((const uint16_t *)a.x + c * 8, 8, v);
         u32w2 codes;
         const uint32_t scale = mx8_encode8(v, &codes);
-        ((u32w2 *)a.codes)[c] = codes;
+        if (NT) __builtin_nontemporal_store(codes, (u32w2 *)a.codes + c);
+        else ((u32w2 *)a.codes)[c] = codes;
         if ((c & 3) == 0) ((uint8_t *)a.scales)[c >> 2] = (uint8_t)scale;
     }
 }
@@ -82,20 +85,20 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void k_encode_row(RowArg
     }
 }
 
-template <bool ROW>
+template <bool ROW, bool NT>
 __global__ __launch_bounds__(kBlock) void k_decode(RowArgs8 a, int64_t chunks)
 {
     const int64_t step = (int64_t)gridDim.x * kBlock;
     const uint32_t per_row = (uint32_t)(a.cols / 8);
     for (int64_t c = (int64_t)blockIdx.x * kBlock + threadIdx.x; c < chunks; c += step) {
-        const u32w2 codes = ((const u32w2 *)a.codes)[c];
+        const u32w2 codes = NT ? __builtin_nontemporal_load((const u32w2 *)a.codes + c) : ((const u32w2 *)a.codes)[c];
         const float s = ROW ? ((const float *)a.scales)[(uint32_t)c / per_row]      // chunks are below 2^31
                             : mx8_scale(((const uint8_t *)a.scales)[c >> 2]);
         float v[8];
         e4m3_decode8(codes, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= s;
-        store8<false>((uint16_t *)a.y + c * 8, 8, v);
+        store8<false, NT>((uint16_t *)a.y + c * 8, 8, v);
     }
 }
 
@@ -214,6 +217,9 @@ __global__ __launch_bounds__(kBlock) void k_dbias(DzArgs a, int64_t cols)
     }
 }
 
+// chunks from which a call streams: 192 MB of values and codes
+constexpr int64_t kStreamChunks = int64_t(1) << 23;
+
 uint32_t flat_grid(int64_t chunks)
 {
     const int64_t n = (chunks + kBlock - 1) / kBlock;
@@ -228,7 +234,8 @@ hipError_t launch_f8_encode(int f8, const RowArgs8 &a, hipStream_t stream)
 {
     const int64_t chunks = a.rows * a.cols / 8;
     if (f8 == F8_MX) {
-        hipLaunchKernelGGL(k_encode_mx, dim3(flat_grid(chunks)), dim3(kBlock), 0, stream, a, chunks);
+        hipLaunchKernelGGL((chunks >= kStreamChunks ? k_encode_mx<true> : k_encode_mx<false>), dim3(flat_grid(chunks)),
+                           dim3(kBlock), 0, stream, a, chunks);
         return hipGetLastError();
     }
     const int64_t need = a.cols / 8;         // chunks of a row
@@ -249,10 +256,10 @@ hipError_t launch_f8_encode(int f8, const RowArgs8 &a, hipStream_t stream)
 hipError_t launch_f8_decode(int f8, const RowArgs8 &a, hipStream_t stream)
 {
     const int64_t chunks = a.rows * a.cols / 8;
-    if (f8 == F8_MX)
-        hipLaunchKernelGGL((k_decode<false>), dim3(flat_grid(chunks)), dim3(kBlock), 0, stream, a, chunks);
-    else
-        hipLaunchKernelGGL((k_decode<true>), dim3(flat_grid(chunks)), dim3(kBlock), 0, stream, a, chunks);
+    const bool nt = chunks >= kStreamChunks;
+    const auto kernel = f8 == F8_MX ? (nt ? k_decode<false, true> : k_decode<false, false>)
+                                    : (nt ? k_decode<true, true> : k_decode<true, false>);
+    hipLaunchKernelGGL(kernel, dim3(flat_grid(chunks)), dim3(kBlock), 0, stream, a, chunks);
     return hipGetLastError();
 }
 

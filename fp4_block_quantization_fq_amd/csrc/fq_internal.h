@@ -267,6 +267,7 @@ struct ProductArgs {
     int act;
     Gate gate;
     int group;               // tile rows that share a run of b (set by the launcher)
+    int stream;              // y exceeds the L2s (set by the launcher)
     int splits;              // parts of the contraction, FP32 in `partial`; 0 or 1: none
     int split_k;             // k of a part (set by the launcher)
     float *partial;          // [splits, M, columns of b]

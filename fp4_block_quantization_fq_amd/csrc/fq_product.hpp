@@ -213,10 +213,14 @@ __device__ __forceinline__ void load_res(const ProductArgs &p, int64_t at, float
     if (p.y_f32) load8<false>((const float *)p.res + at, 8, r);
     else load8<false>((const uint16_t *)p.res + at, 8, r);
 }
+// STREAM: past the L2s where the output would fill them (4 MB each), whose lines the operands' tiles
+// need (8192 x 5760 -> 2880 222 -> 211 us, dw 2880 x 5760 264 -> 247, of 32 experts
+// 402 -> 320; a gated block's h and codes gain nothing).
+template <bool STREAM = false>
 __device__ __forceinline__ void store_y(const ProductArgs &p, int64_t at, const float (&v)[8])
 {
     if (p.y_f32) store8<false>((float *)p.y + at, 8, v);
-    else store8<false>((uint16_t *)p.y + at, 8, v);
+    else store8<false, STREAM>((uint16_t *)p.y + at, 8, v);
 }
 
 // What becomes of eight sums (column `col` of row `row`, of N columns) and the
@@ -482,25 +486,35 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
         // the wave reads what it wrote itself: LDS keeps a wave's order
         __builtin_amdgcn_wave_barrier();
         if (EPI == EPI_STORE || EPI == EPI_RES) {
+            auto store_rows = [&](auto streamed) {
 #pragma unroll
-            for (int k = 0; k < PASSES; ++k) {
-                float z[8];
-                load8<false>(slab_at(k) + c, 8, z);
-                if (!inside(i, k)) continue;
-                const int64_t at = (EPI == EPI_STORE ? (int64_t)(expert * SEGK + split) * p.M * p.N : 0) +
-                                   row_of(i, k) * p.N + col;
-                if (EPI == EPI_RES) {
+                for (int k = 0; k < PASSES; ++k) {
+                    float z[8];
+                    load8<false>(slab_at(k) + c, 8, z);
+                    if (!inside(i, k)) continue;
+                    const int64_t at = (EPI == EPI_STORE ? (int64_t)(expert * SEGK + split) * p.M * p.N : 0) +
+                                       row_of(i, k) * p.N + col;
+                    if (EPI == EPI_RES) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) z[e] += bias[e];
-                    if (p.res) {
-                        float v[8];
-                        if (p.y_f32) load_res(p, at, v);
-                        else unpack8(res16[k], v);
+                        for (int e = 0; e < 8; ++e) z[e] += bias[e];
+                        if (p.res) {
+                            float v[8];
+                            if (p.y_f32) load_res(p, at, v);
+                            else unpack8(res16[k], v);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) z[e] += v[e];
+                            for (int e = 0; e < 8; ++e) z[e] += v[e];
+                        }
                     }
+                    store_y<decltype(streamed)::value>(p, at, z);
                 }
-                store_y(p, at, z);
+            };
+            if (p.stream) {
+                // marked, so that the two branches are not merged, without the hint
+                asm volatile("; streamed rows");
+                store_rows(std::true_type());
+                asm volatile("; end of streamed rows");
+            } else {
+                store_rows(std::false_type());
             }
         } else {
             // two rows a turn, not unrolled further: the activations' code is long
@@ -571,8 +585,10 @@ hipError_t launch_tiles(const ProductArgs &p, hipStream_t stream)
 {
     constexpr int BM = WM * TM * 32, BN = WN * TN * 32 / (EPI == EPI_GLU ? 2 : 1);
     const int64_t n = product_tiles<SEGK>(p, BM, BN) * (p.splits > 1 ? p.splits : 1);
+    ProductArgs q = p;
+    q.stream = (int64_t)p.M * p.N * (SEGK && p.experts ? p.experts : 1) >= int64_t(1) << 22;       // 8 MB of BF16
     hipLaunchKernelGGL((k_product<LA, LB, TM, TN, WM, WN, STAGES, EPI, SEGK>), dim3((uint32_t)n), dim3(64 * WM * WN), 0,
-                       stream, p);
+                       stream, q);
     return hipGetLastError();
 }
 

@@ -4,9 +4,8 @@
 //
 // Activations are FP32, from the hardware's exp2 and reciprocal (1 ulp each; the
 // exponent's rounding adds |z| / 2 ulp to exp(-z), which the slope of the sigmoid
-// takes back): with expf and erff a tile's epilogue cost EPI_ACT.  An infinite
-// value before SiLU or GELU may give NaN (infinity times 0), as their formulas
-// have it.
+// takes back).  An infinite value before SiLU or GELU may give NaN (infinity times
+// 0), as their formulas have it.
 #pragma once
 
 #include <type_traits>
@@ -186,8 +185,9 @@ __device__ __forceinline__ int segment_tiles(const int32_t *offsets, int experts
     }
     return wave_total(n);
 }
-// The expert and the rows of tile number `tile`, below segment_tiles.
-__device__ __forceinline__ void find_segment(const int32_t *offsets, int experts, int rows, int size, int tile,
+// The expert and the rows of tile number `tile`; whether there is one (there is below
+// segment_tiles, unless offsets that do not ascend have made its sum wrap).
+__device__ __forceinline__ bool find_segment(const int32_t *offsets, int experts, int rows, int size, int tile,
                                              int lane, int *expert, int *row0, int *row_end)
 {
     int before = 0;
@@ -209,11 +209,12 @@ __device__ __forceinline__ void find_segment(const int32_t *offsets, int experts
             *row0 = __builtin_amdgcn_readlane(a, at) +
                     (tile - before - __builtin_amdgcn_readlane(sum - n, at)) * size;
             *row_end = __builtin_amdgcn_readlane(b, at);
-            return;
+            return *row0 < *row_end;
         }
         before += __builtin_amdgcn_readlane(sum, 63);
     }
-    *expert = *row0 = *row_end = 0;                      // not reached
+    *expert = *row0 = *row_end = 0;
+    return false;
 }
 
 }  // namespace fqdev

@@ -1568,8 +1568,8 @@ struct Product {
 
 fq_status check_product(const Product &d)
 {
-    if (d.rows < 1 || d.rows > kMaxDim)
-        return fail(FQ_ERR_SHAPE, "rows=%lld must be >= 1 and below 2^31", (long long)d.rows);
+    if (d.rows < 1 || d.rows > fqimpl::kProductMaxRows)
+        return fail(FQ_ERR_SHAPE, "rows=%lld must be in [1, 2^30]", (long long)d.rows);
     if (d.k < 8 || d.n < 8 || d.k % 8 || d.n % 8 || d.k > fqimpl::kProductMaxDim ||
         d.n > fqimpl::kProductMaxDim)
         return fail(FQ_ERR_SHAPE, "k=%lld and n=%lld must be multiples of 8 from 8 to 2^20",

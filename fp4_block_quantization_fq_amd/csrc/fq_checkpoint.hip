@@ -105,7 +105,7 @@ __global__ __launch_bounds__(kBlock) void k_decode(RowArgs8 a, int64_t chunks)
 // ---- gradient before the activation ----------------------------------------------------
 // A workgroup: a tile of a segment's rows, 256 columns of the output (32 lanes of
 // eight columns, eight rows at a time).  Tiles have 64 rows; where that leaves CUs
-// without work (fewer than 512 workgroups), 8: 333 x 776 with GELU takes DZ_FEW us
+// without work (fewer than 512 workgroups), 8: 333 x 776 with GELU takes 4 us
 // so, 29 in tiles of 64.
 
 template <bool MX>
@@ -132,7 +132,7 @@ __global__ __launch_bounds__(kBlock) void k_dz(DzArgs a)
     int row0 = tile * a.tile, row_end = (int)a.rows, expert;
     if (a.offsets) {
         if (tile >= segment_tiles(a.offsets, a.experts, (int)a.rows, a.tile, lane)) return;
-        find_segment(a.offsets, a.experts, (int)a.rows, a.tile, tile, lane, &expert, &row0, &row_end);
+        if (!find_segment(a.offsets, a.experts, (int)a.rows, a.tile, tile, lane, &expert, &row0, &row_end)) return;
     }
     row_end = row_end - row0 < a.tile ? row_end : row0 + a.tile;
     const int c = threadIdx.x & 31, r0 = threadIdx.x >> 5;
@@ -199,6 +199,9 @@ __global__ __launch_bounds__(kBlock) void k_dbias(DzArgs a, int64_t cols)
         first = segment_tiles(a.offsets, expert, (int)a.rows, a.tile, lane);
         segment_of(a.offsets, expert, (int)a.rows, &s, &e);
         count = (e - s + a.tile - 1) / a.tile;
+        // offsets that do not ascend may name more tiles than there are
+        if (first < 0 || first >= a.tiles) count = 0;
+        else count = min(count, a.tiles - first);
     }
     const int64_t col = (int64_t)blockIdx.x * COLS + c;
     float t = 0.0f;
@@ -278,7 +281,8 @@ int64_t dz_tiles(int64_t rows, int64_t n, int64_t experts)
 hipError_t launch_dz(DzArgs a, hipStream_t stream)
 {
     a.tile = dz_tile(a.rows, a.n);
-    const dim3 grid((uint32_t)dz_tiles(a.rows, a.n, a.offsets ? a.experts : 0), (uint32_t)((a.n + 255) / 256));
+    a.tiles = (int)dz_tiles(a.rows, a.n, a.offsets ? a.experts : 0);
+    const dim3 grid((uint32_t)a.tiles, (uint32_t)((a.n + 255) / 256));
     const int64_t cols = a.glu ? 2 * a.n : a.n;
     if (a.glu && a.pre_kind == PRE_MX) hipLaunchKernelGGL((k_dz<true, true>), grid, dim3(kBlock), 0, stream, a);
     else if (a.glu) hipLaunchKernelGGL((k_dz<true, false>), grid, dim3(kBlock), 0, stream, a);

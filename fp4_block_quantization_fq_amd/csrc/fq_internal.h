@@ -240,6 +240,7 @@ hipError_t launch_adamw_plan(const AdamWStep &a, const AdamWTensor *t, const uin
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };     // FQ_ACT_* of fq.h
 enum { PRE_NONE = 0, PRE_BF16 = 1, PRE_MX = 2 };
 constexpr int64_t kProductMaxDim = int64_t(1) << 20;                 // of k and n: 32-bit offsets in a tile
+constexpr int64_t kProductMaxRows = int64_t(1) << 30;                // and tiles of them in an int
 constexpr int64_t kProductMaxExperts = 1024;
 struct Gate {                // h = a(min(g, limit)) (clamp(u, +-limit) + shift)
     int act;
@@ -309,7 +310,7 @@ struct DzArgs {
     void *h;                 // BF16 [rows, n] or null
     float *partials;         // [dz_tiles, n or 2n], or null without dbias
     float *dbias;            // [experts, n or 2n] or null
-    int tile;                // rows of a workgroup (set by the launcher)
+    int tile, tiles;         // rows of a workgroup, workgroups' rows of `partials` (set by the launcher)
 };
 int64_t dz_tiles(int64_t rows, int64_t n, int64_t experts);
 hipError_t launch_dz(DzArgs a, hipStream_t stream);

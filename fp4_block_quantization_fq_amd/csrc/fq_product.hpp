@@ -302,7 +302,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
         k_begin = __builtin_amdgcn_readfirstlane(k_begin);
         k_end = __builtin_amdgcn_readfirstlane(k_end);
     } else {
-        find_segment(p.offsets, p.experts, p.rows, BM, tm, lane, &expert, &row0, &row_end);
+        if (!find_segment(p.offsets, p.experts, p.rows, BM, tm, lane, &expert, &row0, &row_end)) return;
     }
     const int col0 = tn * BNC;
     if (EPI == EPI_STORE && p.splits > 1) {
@@ -612,7 +612,7 @@ hipError_t launch_split(const ProductArgs &p, int columns, int epilogue, hipStre
     q.res = nullptr;
     q.y = p.partial;
     q.y_f32 = 1;
-    q.split_k = ((p.K + 63) / 64 + p.splits - 1) / p.splits * 64;
+    q.split_k = (p.K / 64 + (p.K % 64 ? 1 : 0) + p.splits - 1) / p.splits * 64;
     hipError_t e = launch_small<LA, LB, EPI_STORE, SEGK>(q, stream);
     return e != hipSuccess ? e : fqimpl::launch_product_join(p, epilogue, p.partial, stream);
 }

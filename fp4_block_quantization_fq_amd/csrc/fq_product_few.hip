@@ -53,7 +53,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_product_few(const ProductArgs p)
     const int logical = xcd * each + min(xcd, rest) + b / kXcds;
     const int tm = logical / tiles_n, tn = logical % tiles_n;
     int row0 = tm * ROWS, row_end = p.M, expert = 0;
-    if (p.offsets) find_segment(p.offsets, p.experts, p.rows, ROWS, tm, lane, &expert, &row0, &row_end);
+    if (p.offsets && !find_segment(p.offsets, p.experts, p.rows, ROWS, tm, lane, &expert, &row0, &row_end)) return;
     const int rows = min(row_end - row0, ROWS), col0 = tn * BNC;
 
     // this lane's chunk of the weight's rows: its first k in a step and its columns

@@ -3,8 +3,8 @@
 // their order and go through the epilogue that the tile kernel would have applied.
 //
 // Where a product has fewer tiles than the chip has room for, its time is the
-// latency of its steps: 128 x 2880 -> 2880 took 30 us on 23 workgroups, JOIN_128 us
-// with its contraction in eight parts and this kernel.
+// latency of its steps: 128 x 2880 -> 2880 took 30 us on 23 workgroups, 15 with its
+// contraction in eight parts and this kernel.
 #include "fq_product.hpp"
 
 namespace {

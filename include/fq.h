@@ -601,7 +601,7 @@ fq_status fq_adamw_step_plan(const fq_adamw_hyper *hyper, const void *plan,
  *
  * Layouts, row-major: activations [rows, ...]; weights BF16 [experts, k, n] (as
  * fq_qlinear_fwd's); bias BF16 or FP32 [experts, n], may be NULL.
- * Shapes: 1 <= rows < 2^31; k and n multiples of 8 from 8 to 2^20 (of 32 where an
+ * Shapes: 1 <= rows <= 2^30; k and n multiples of 8 from 8 to 2^20 (of 32 where an
  * operand of that width is held in 8 bits); rows * k, rows * columns and experts
  * * k * columns at most 2^34; experts <= 1024.  Tensors 16-byte aligned, offsets
  * 4-byte.  Outputs overlap no other operand except where it is said.

@@ -73,7 +73,10 @@ def run_linear(rows, k, n, starts=None, act=op.NONE, out=torch.bfloat16, res=Tru
 # one token, ragged rows, odd multiples of eight, contractions that end inside a step; the last ones take the large tiles
 SHAPES = [(1, 8, 8), (1, 72, 264), (1, 2880, 200), (2, 64, 64), (3, 1000, 136), (7, 520, 1032), (16, 128, 72), (17, 136, 128), (31, 64, 8),
           (33, 200, 320), (64, 1032, 96), (65, 264, 392), (127, 8, 128), (128, 192, 256), (129, 64, 264), (257, 776, 136),
-          (300, 40, 1096), (1021, 72, 776), (4200, 72, 4168), (4090, 72, 4088), (4090, 392, 4088), (4200, 456, 4168), (4090, 392, 2040)]
+          (300, 40, 1096), (1021, 72, 776), (4200, 72, 4168), (4090, 72, 4088), (4090, 392, 4088), (4200, 456, 4168), (4090, 392, 2040),
+          # wide weights of few rows, contractions in parts, four stages
+          (1, 72, 8200), (17, 72, 8200), (40, 264, 8200), (64, 136, 8200), (100, 1032, 136), (200, 2880, 264), (130, 4104, 72),
+          (1900, 1032, 1896)]
 
 
 @pytest.mark.parametrize("rows,k,n", SHAPES)
@@ -91,6 +94,21 @@ def test_linear_epilogues(act, out, rows, pre):
 def test_linear_bare():
     run_linear(150, 64, 136, res=False, bias=None)
     run_linear(3, 64, 136, res=False, bias=None)
+
+
+@pytest.mark.parametrize("act", [op.NONE, op.SILU])
+@pytest.mark.parametrize("pre", ["bf16", "mx"])
+def test_epilogues_of_joined_parts(act, pre):
+    run_linear(100, 1032, 160, act=act, pre=pre)
+    run_linear(100, 1032, 160, act=act, out=torch.float32, pre=pre, bias=torch.bfloat16)
+    run_linear(100, 1032, 160, act=act, inplace=True)
+    run_glu(100, 1032, 160, gate="clamped" if act else "gelu", pre=pre)
+
+
+@pytest.mark.parametrize("rows", [1, 17, 40])
+def test_few_rows_of_wide_weights(rows):
+    run_linear(rows, 72, 8224, act=op.GELU, pre="mx", out=torch.float32)
+    run_glu(rows, 72, 8224, gate="clamped", pre="mx")
 
 
 @pytest.mark.parametrize("rows", [1, 40, 200])
@@ -203,7 +221,8 @@ def run_bwd(rows, k, n, starts=None, gate=None, act=op.NONE, x_how="bf16", pre_h
 
 BWD_SHAPES = [(1, 8, 8), (1, 264, 136), (2, 64, 64), (5, 1000, 72), (63, 72, 264), (64, 128, 128), (65, 136, 264), (100, 520, 776),
               (129, 256, 136), (333, 1000, 72), (1000, 72, 136), (2200, 4168, 136),
-              (4090, 4088, 72), (4200, 4168, 72), (4200, 4168, 456), (100, 4088, 4088), (100, 2872, 2864), (456, 2872, 2864), (392, 4088, 4088)]
+              (4090, 4088, 72), (4200, 4168, 72), (4200, 4168, 456), (100, 4088, 4088), (100, 2872, 2864), (456, 2872, 2864), (392, 4088, 4088),
+              (100, 136, 2088), (2056, 136, 200), (1100, 200, 1160), (1900, 1896, 1032)]
 
 
 @pytest.mark.parametrize("rows,k,n", BWD_SHAPES)
@@ -316,6 +335,23 @@ def test_offsets_that_do_not_ascend_stay_inside():
         fq.fq_linear_bwd(dy, x, w, offsets=offsets_of(starts), dx=dx, dw=dw, dbias=db)
         torch.cuda.synchronize()
         g.check()
+
+
+@pytest.mark.parametrize("rows,experts", [(100, 600), (1000, 1024), (65, 1)])
+def test_many_segments_that_overlap_stay_inside(rows, experts):
+    """More tiles in the offsets than any that ascend have: no index leaves the
+    outputs or the workspace, which ends where it has to."""
+    starts = [0 if e % 2 == 0 else rows for e in range(experts + 1)]
+    g = Guarded()
+    x, w, dy = g.input(normal(0, rows, 64)), g.input(normal(1, experts, 64, 128)), g.input(normal(2, rows, 64))
+    pre = g.input(normal(3, rows, 128))
+    h, dx = g.output((rows, 64), torch.bfloat16), g.output((rows, 64), torch.bfloat16)
+    dw, db = g.output((experts, 64, 128), torch.bfloat16), g.output((experts, 128), torch.float32)
+    size = fq.glu_bwd_workspace(rows, 64, 64, experts, "cpu").numel()
+    fq.fq_glu_fwd(x, w, offsets=offsets_of(starts), h=h)
+    fq.fq_glu_bwd(dy, x, w, pre, offsets=offsets_of(starts), dx=dx, dw=dw, dbias=db, ws=g.output((size,), torch.uint8))
+    torch.cuda.synchronize()
+    g.check()
 
 
 def test_equal_calls_give_equal_bits():

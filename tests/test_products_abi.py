@@ -46,7 +46,7 @@ def glu_bwd(L, gate=fq.FqGate(fq.FQ_ACT_SILU, 1.0, math.inf, 0.0), dy=fake(), x=
 
 @pytest.mark.parametrize("call", [linear, glu, linear_bwd, glu_bwd])
 def test_shapes(L, call):
-    for bad in (dict(rows=0), dict(rows=-1), dict(rows=BIG), dict(k=0), dict(k=4), dict(k=60), dict(n=0), dict(n=12), dict(k=-64),
+    for bad in (dict(rows=0), dict(rows=-1), dict(rows=BIG), dict(rows=(1 << 30) + 1, k=8, n=8), dict(k=0), dict(k=4), dict(k=60), dict(n=0), dict(n=12), dict(k=-64),
                 dict(k=(1 << 20) + 8), dict(n=(1 << 20) + 8), dict(rows=1 << 30, k=64), dict(rows=1 << 30, n=64),
                 dict(k=1 << 20, n=1 << 20), dict(experts=1025, offsets=fake()), dict(experts=-1, offsets=fake()),
                 dict(experts=1024, offsets=fake(), k=1 << 16, n=1 << 16), dict(rows=BIG - 1, k=1 << 20)):

@@ -1631,19 +1631,19 @@ size_t product_fwd_ws(const Product &d)
 }
 
 // Workspace of a backward: dz, x decoded, the tiles' column sums, the parts of a
-// split dx and then of a split dw.
+// split dx and of a split dw.
 struct ProductBwdLayout {
-    size_t x, partials, parts, total;
+    size_t x, partials, dx_parts, dw_parts, total;
 };
 ProductBwdLayout product_bwd_layout(const Product &d, int32_t x_f8)
 {
     ProductBwdLayout l;
     l.x = round256((size_t)d.rows * d.cols() * 2);
     l.partials = l.x + (x_f8 != FQ_F8_NONE ? round256((size_t)d.rows * d.k * 2) : 0);
-    l.parts = l.partials +
-              round256((size_t)fqimpl::dz_tiles(d.rows, d.n, d.experts) * d.cols() * sizeof(float));
-    const size_t dx = split_bytes(d, d.rows, d.k, d.cols()), dw = split_bytes(d, d.k, d.cols(), d.rows);
-    l.total = l.parts + (dx > dw ? dx : dw);
+    l.dx_parts = l.partials +
+                 round256((size_t)fqimpl::dz_tiles(d.rows, d.n, d.experts) * d.cols() * sizeof(float));
+    l.dw_parts = l.dx_parts + round256(split_bytes(d, d.rows, d.k, d.cols()));
+    l.total = l.dw_parts + split_bytes(d, d.k, d.cols(), d.rows);
     return l;
 }
 
@@ -1761,20 +1761,18 @@ fq_status product_bwd(const Product &d, const ProductBwd &a)
         const hipError_t e = fqimpl::launch_dz(z, a.stream);
         if (e != hipSuccess) return device_status(e, "gradient before the activation launch");
     }
+    fqimpl::ProductArgs dx = product_args(d, a.offsets), dw = dx;
     if (a.dx) {
-        fqimpl::ProductArgs p = product_args(d, a.offsets);
-        p.a = (const uint16_t *)dz;
-        p.b = (const uint16_t *)a.w;
-        p.lda = p.ldb = d.cols();
-        p.b_stride = d.k * d.cols();
-        p.M = (int)d.rows;
-        p.N = (int)d.k;
-        p.K = (int)d.cols();
-        p.y = a.dx;
-        p.splits = splits_of(d, d.rows, d.k, d.cols());
-        p.partial = (float *)(ws + l.parts);
-        const hipError_t e = fqimpl::launch_product_dx(p, a.stream);
-        if (e != hipSuccess) return device_status(e, "dx product launch");
+        dx.a = (const uint16_t *)dz;
+        dx.b = (const uint16_t *)a.w;
+        dx.lda = dx.ldb = d.cols();
+        dx.b_stride = d.k * d.cols();
+        dx.M = (int)d.rows;
+        dx.N = (int)d.k;
+        dx.K = (int)d.cols();
+        dx.y = a.dx;
+        dx.splits = splits_of(d, d.rows, d.k, d.cols());
+        dx.partial = (float *)(ws + l.dx_parts);
     }
     if (a.dw) {
         const void *x = a.x;
@@ -1789,20 +1787,21 @@ fq_status product_bwd(const Product &d, const ProductBwd &a)
             if (e != hipSuccess) return device_status(e, "decode launch");
             x = r.y;
         }
-        fqimpl::ProductArgs p = product_args(d, a.offsets);
-        p.a = (const uint16_t *)x;
-        p.b = (const uint16_t *)dz;
-        p.lda = d.k;
-        p.ldb = d.cols();
-        p.M = (int)d.k;
-        p.N = (int)d.cols();
-        p.K = (int)d.rows;
-        p.y = a.dw;
-        p.splits = splits_of(d, d.k, d.cols(), d.rows);
-        p.partial = (float *)(ws + l.parts);
-        p.y_f32 = a.dw_type == FQ_TYPE_F32;
-        const hipError_t e = fqimpl::launch_product_dw(p, a.stream);
-        if (e != hipSuccess) return device_status(e, "dw product launch");
+        dw.a = (const uint16_t *)x;
+        dw.b = (const uint16_t *)dz;
+        dw.lda = d.k;
+        dw.ldb = d.cols();
+        dw.M = (int)d.k;
+        dw.N = (int)d.cols();
+        dw.K = (int)d.rows;
+        dw.y = a.dw;
+        dw.y_f32 = a.dw_type == FQ_TYPE_F32;
+        dw.splits = splits_of(d, d.k, d.cols(), d.rows);
+        dw.partial = (float *)(ws + l.dw_parts);
+    }
+    if (a.dx || a.dw) {
+        const hipError_t e = fqimpl::launch_product_bwd(a.dx ? &dx : nullptr, a.dw ? &dw : nullptr, a.stream);
+        if (e != hipSuccess) return device_status(e, "dx and dw launch");
     }
     return ok();
 }

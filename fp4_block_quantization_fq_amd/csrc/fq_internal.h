@@ -283,8 +283,7 @@ hipError_t launch_product_glu(ProductArgs p, hipStream_t stream);      // N of e
 inline bool product_few_rows(int64_t rows, int64_t experts) { return rows <= 64 * (experts ? experts : 1); }
 hipError_t launch_product_few_linear(const ProductArgs &p, hipStream_t stream);      // fq_product_few.hip
 hipError_t launch_product_few_glu(const ProductArgs &p, hipStream_t stream);
-hipError_t launch_product_dx(ProductArgs p, hipStream_t stream);
-hipError_t launch_product_dw(ProductArgs p, hipStream_t stream);
+hipError_t launch_product_bwd(const ProductArgs *dx, const ProductArgs *dw, hipStream_t stream);      // one may be null
 
 // fq_checkpoint.hip
 constexpr int64_t kF8RowMaxCols = 32768;

@@ -261,13 +261,12 @@ __device__ __forceinline__ void finish_glu(const ProductArgs &p, int64_t row, in
 // WM x WN waves of TM x TN accumulator tiles of 32 x 32, STAGES buffers of 64 k.
 // SEGK: the experts' segments are of the contraction (dw), else of C's rows.
 template <int LA, int LB, int TM, int TN, int WM, int WN, int STAGES, int EPI, bool SEGK>
-__global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p)
+__device__ __forceinline__ void product_tile(const ProductArgs &p, uint8_t *lds, const int block)
 {
     constexpr int BM = WM * TM * 32, BN = WN * TN * 32, WAVES = WM * WN;
     constexpr int BNC = EPI == EPI_GLU ? BN / 2 : BN;      // columns of the output
     constexpr int A_BYTES = BM * 128, STAGE = A_BYTES + BN * 128;
     static_assert(EPI != EPI_GLU || TN % 2 == 0, "32 columns of either half next to each other");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES][STAGE];
 
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int wm = wave / WN, wn = wave % WN;
@@ -278,9 +277,9 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
     if (p.offsets) tiles_m = SEGK ? tiles_m * p.experts : segment_tiles(p.offsets, p.experts, p.rows, BM, lane);
     const int total = tiles_m * tiles_n;
     // part of the contraction (of one product, stored as FP32 partial sums)
-    const int split = EPI == EPI_STORE && p.splits > 1 ? (int)blockIdx.x / total : 0;
-    const int b = (int)blockIdx.x - split * total;
-    if (b >= total) return;
+    const int split = EPI == EPI_STORE && p.splits > 1 && total ? block / total : 0;
+    const int b = block - split * total;
+    if (b >= total || split >= max(p.splits, 1)) return;
     // the hardware deals workgroups round-robin to eight XCDs, each with its own
     // L2: a contiguous run of tiles each
     const int each = total / kXcds, rest = total % kXcds, xcd = b % kXcds;
@@ -341,13 +340,13 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
     int left = k_end - k_begin;                // of the contraction
 
     // fragment n of a substep, in the order of their first use: b0 a0 b1 b2 .. a1 a2 ..
-    auto read = [&](const uint8_t *lds, int ks, int to, int n) {
+    auto read = [&](const uint8_t *from, int ks, int to, int n) {
         if (n == 0 || (n > 1 && n <= TN)) {
             const int j = n ? n - 1 : 0;
-            fb[to][j] = tb.read(lds + A_BYTES, wn * TN + j, ks, lane);
+            fb[to][j] = tb.read(from + A_BYTES, wn * TN + j, ks, lane);
         } else {
             const int i = n == 1 ? 0 : n - TN;
-            fa[to][i] = ta.read(lds, wm * TM + i, ks, lane);
+            fa[to][i] = ta.read(from, wm * TM + i, ks, lane);
         }
     };
     // load n of a stage into buffer `buf`; `have` k of it exist (not looked at if FULL)
@@ -385,7 +384,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
     };
     // Stage in buffer `cur`; FULL: STAGES more of 64 k follow it at least.
     auto stage = [&](int cur, bool full) {
-        const uint8_t *here = lds[cur], *there = lds[(cur + 1) % STAGES];
+        const uint8_t *here = lds + cur * STAGE, *there = lds + (cur + 1) % STAGES * STAGE;
         const int next = left - BK;                                // k of the next stage
         const int rest = left - (STAGES - 1) * BK, after = left - STAGES * BK;
         substep(0, true, here, 1, (cur + STAGES - 1) % STAGES, HALF, LOADS - HALF, rest, full);
@@ -431,7 +430,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
             }
         } else {
 #pragma unroll
-            for (int n = 0; n < READS; ++n) read(lds[0], 0, 0, n);
+            for (int n = 0; n < READS; ++n) read(lds, 0, 0, n);
             while (left >= 2 * STAGES * BK) {  // all loads of these stages are whole
 #pragma unroll
                 for (int s = 0; s < STAGES; ++s) stage(s, true);
@@ -453,7 +452,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
     constexpr int STEP = 64 / CHUNKS, PASSES = (32 + STEP - 1) / STEP;      // whole rows a pass: a lane keeps its columns
     constexpr int SLAB = 32 * WCOLS * 4;
     static_assert(WAVES * SLAB <= STAGES * STAGE, "a slab for every wave");
-    float *slab = reinterpret_cast<float *>(&lds[0][0] + wave * SLAB);
+    float *slab = reinterpret_cast<float *>(lds + wave * SLAB);
     const int c = lane % CHUNKS * 8, r0 = lane / CHUNKS;
     const int col = col0 + wn * (EPI == EPI_GLU ? WCOLS / 2 : WCOLS) + c;
     const bool mine = col < p.N && r0 < STEP;
@@ -545,6 +544,34 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_product(const ProductArgs p
     }
 }
 
+template <int LA_, int LB_, int TM, int TN, int WM, int WN, int STAGES, int EPI, bool SEGK>
+struct Shape {
+    static constexpr int kThreads = 64 * WM * WN, kRows = WM * TM * 32, kCols = WN * TN * 32;
+    static constexpr int kOutCols = EPI == EPI_GLU ? kCols / 2 : kCols, kLds = STAGES * (kRows + kCols) * 128;
+    static constexpr bool kSegK = SEGK;
+    static __device__ __forceinline__ void run(const ProductArgs &p, uint8_t *lds, int block)
+    {
+        product_tile<LA_, LB_, TM, TN, WM, WN, STAGES, EPI, SEGK>(p, lds, block);
+    }
+};
+
+template <typename S>
+__global__ __launch_bounds__(S::kThreads, 1) void k_product(const ProductArgs p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
+    S::run(p, lds, (int)blockIdx.x);
+}
+// Two products in one launch: the second one's tiles fill the CUs that the first one's
+// last ones leave.
+template <typename S0, typename S1>
+__global__ __launch_bounds__(S0::kThreads, 1) void k_product_pair(const ProductArgs p0, const ProductArgs p1, int n0)
+{
+    static_assert(S0::kThreads == S1::kThreads, "one size of workgroups");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S0::kLds > S1::kLds ? S0::kLds : S1::kLds];
+    if ((int)blockIdx.x < n0) S0::run(p0, lds, (int)blockIdx.x);
+    else S1::run(p1, lds, (int)blockIdx.x - n0);
+}
+
 // ---- launches ------------------------------------------------------------------------
 // Tiles of `bm` rows and `bn` columns (of the output), for the grid at most.
 template <bool SEGK>
@@ -580,16 +607,37 @@ float product_time(const ProductArgs &p, int bm, int bn, int per_cu, float step,
     return rounds * (ceilf(k / 64) * step + fixed);
 }
 
+// Workgroups of a product in tiles of shape S, and its arguments for them.
+template <typename S>
+int64_t shape_grid(const ProductArgs &p)
+{
+    return product_tiles<S::kSegK>(p, S::kRows, S::kOutCols) * (p.splits > 1 ? p.splits : 1);
+}
+template <typename S>
+ProductArgs shape_args(ProductArgs p)
+{
+    const int64_t n = (int64_t)p.M * p.N * (S::kSegK && p.experts ? p.experts : 1);
+    p.stream = n >= int64_t(1) << 22;                              // 8 MB of BF16
+    return p;
+}
+template <typename S>
+hipError_t launch_shape(const ProductArgs &p, hipStream_t stream)
+{
+    hipLaunchKernelGGL((k_product<S>), dim3((uint32_t)shape_grid<S>(p)), dim3(S::kThreads), 0, stream, shape_args<S>(p));
+    return hipGetLastError();
+}
+template <typename S0, typename S1>
+hipError_t launch_pair(const ProductArgs &p0, const ProductArgs &p1, hipStream_t stream)
+{
+    const int64_t n0 = (shape_grid<S0>(p0) + kXcds - 1) / kXcds * kXcds;       // the second one's XCDs stay in step
+    hipLaunchKernelGGL((k_product_pair<S0, S1>), dim3((uint32_t)(n0 + shape_grid<S1>(p1))), dim3(S0::kThreads), 0,
+                       stream, shape_args<S0>(p0), shape_args<S1>(p1), (int)n0);
+    return hipGetLastError();
+}
 template <int LA, int LB, int TM, int TN, int WM, int WN, int STAGES, int EPI, bool SEGK>
 hipError_t launch_tiles(const ProductArgs &p, hipStream_t stream)
 {
-    constexpr int BM = WM * TM * 32, BN = WN * TN * 32 / (EPI == EPI_GLU ? 2 : 1);
-    const int64_t n = product_tiles<SEGK>(p, BM, BN) * (p.splits > 1 ? p.splits : 1);
-    ProductArgs q = p;
-    q.stream = (int64_t)p.M * p.N * (SEGK && p.experts ? p.experts : 1) >= int64_t(1) << 22;       // 8 MB of BF16
-    hipLaunchKernelGGL((k_product<LA, LB, TM, TN, WM, WN, STAGES, EPI, SEGK>), dim3((uint32_t)n), dim3(64 * WM * WN), 0,
-                       stream, q);
-    return hipGetLastError();
+    return launch_shape<Shape<LA, LB, TM, TN, WM, WN, STAGES, EPI, SEGK>>(p, stream);
 }
 
 // Tiles of 128 x 128: two workgroups a CU, or one with four stages where there is no
@@ -602,18 +650,21 @@ hipError_t launch_small(const ProductArgs &p, hipStream_t stream)
     return launch_tiles<LA, LB, 2, 2, 2, 2, 2, EPI, SEGK>(p, stream);
 }
 
-// One product of few tiles: its parts to the workspace (`columns` of B), then joined
-// as `epilogue` says.
+// The arguments of a product whose parts go to the workspace (`columns` of B).
+inline ProductArgs split_args(ProductArgs p, int columns)
+{
+    p.N = columns;
+    p.res = nullptr;
+    p.y = p.partial;
+    p.y_f32 = 1;
+    p.split_k = (p.K / 64 + (p.K % 64 ? 1 : 0) + p.splits - 1) / p.splits * 64;
+    return p;
+}
+// One product of few tiles: its parts to the workspace, then joined as `epilogue` says.
 template <int LA, int LB, bool SEGK>
 hipError_t launch_split(const ProductArgs &p, int columns, int epilogue, hipStream_t stream)
 {
-    ProductArgs q = p;
-    q.N = columns;
-    q.res = nullptr;
-    q.y = p.partial;
-    q.y_f32 = 1;
-    q.split_k = (p.K / 64 + (p.K % 64 ? 1 : 0) + p.splits - 1) / p.splits * 64;
-    hipError_t e = launch_small<LA, LB, EPI_STORE, SEGK>(q, stream);
+    const hipError_t e = launch_small<LA, LB, EPI_STORE, SEGK>(split_args(p, columns), stream);
     return e != hipSuccess ? e : fqimpl::launch_product_join(p, epilogue, p.partial, stream);
 }
 

@@ -1,8 +1,8 @@
 """Blockwise FP4 (MXFP4 / NVFP4) fake quantization on AMD MI355X (gfx950).
 
 Thin binding over libfq.so (C ABI in include/fq.h): ctypes, and for the row
-operators, whose calls can be shorter than that takes, a small extension
-(csrc/fq_binding.cpp).  Every function here only marshals arguments: shapes, device pointers and the current HIP
+operators and the feed-forward products, whose calls can be shorter than that
+takes, a small extension (csrc/fq_binding.cpp).  Every function here only marshals arguments: shapes, device pointers and the current HIP
 stream go to the library, and all arithmetic runs in its HIP kernels.  PyTorch
 supplies device memory and streams.  There is no fallback: if libfq.so is
 missing or a call fails, an exception is raised.

@@ -1,5 +1,6 @@
 // fq_binding.cpp -- the argument marshalling of the row operators (norm,
-// expert sorting, optimizer) as a CPython extension over the C ABI.
+// expert sorting, optimizer) and of the feed-forward products and checkpoints
+// as a CPython extension over the C ABI.
 //
 // Such a call's kernels take 2 to 5 us on a small batch; checking seven
 // tensors and calling through ctypes took 8 us of host time before the launch,

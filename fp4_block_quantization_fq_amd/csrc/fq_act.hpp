@@ -59,7 +59,7 @@ __device__ __forceinline__ float act_grad_of(float alpha, float z, float *value)
     if (ACT == fqimpl::ACT_SILU) {
         const float s = sigmoid(alpha * z);
         *value = z * s;
-        return s * (1.0f + alpha * z * (1.0f - s));
+        return __builtin_fmaf(alpha, *value * (1.0f - s), s);          // in this order no finite z overflows
     }
     if (ACT == fqimpl::ACT_GELU) {
         float e;
@@ -159,6 +159,18 @@ __device__ __forceinline__ float mx8_scale(uint32_t code)
 {
     return code == 255u ? as_f(0x7FC00000u) : e8m0_value(code);
 }
+
+// ---- grids -----------------------------------------------------------------------------
+// `n` workgroups and one's number.  The threads along an axis of a grid have to stay
+// below 2^32, which the largest calls' workgroups are not; the last row of such a grid
+// has numbers from n on.
+inline dim3 grid_of(int64_t n, int threads)
+{
+    const int64_t row = (int64_t(1) << 30) / threads;          // a multiple of the XCDs
+    if (n <= row) return dim3((uint32_t)n);
+    return dim3((uint32_t)row, (uint32_t)((n + row - 1) / row));
+}
+__device__ __forceinline__ int workgroup() { return (int)(blockIdx.y * gridDim.x + blockIdx.x); }
 
 // ---- the experts' segments of rows ---------------------------------------------------
 // offsets[e] .. offsets[e + 1], brought into 0 .. rows, so that no entry can lead

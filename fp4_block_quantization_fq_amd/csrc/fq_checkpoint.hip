@@ -45,8 +45,8 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void k_encode_row(RowArg
     constexpr int THREADS = LANES < 256 ? 256 : LANES, WAVES = LANES / 64;
     __shared__ uint32_t tops[WAVES > 0 ? WAVES : 1];
     const int l = threadIdx.x % LANES;
-    const int64_t row = (int64_t)blockIdx.x * (THREADS / LANES) + threadIdx.x / LANES;
-    if (LANES <= 64 && row >= a.rows) return;
+    const int64_t row = (int64_t)workgroup() * (THREADS / LANES) + threadIdx.x / LANES;
+    if (row >= a.rows) return;                   // of whole waves or workgroups, where those share rows
     const uint16_t *x = (const uint16_t *)a.x + row * a.cols;
     Raw8<uint16_t> raw[NCH];
     uint32_t top = 0;
@@ -106,7 +106,7 @@ __global__ __launch_bounds__(kBlock) void k_decode(RowArgs8 a, int64_t chunks)
 // A workgroup: a tile of a segment's rows, 256 columns of the output (32 lanes of
 // eight columns, eight rows at a time).  Tiles have 64 rows; where that leaves CUs
 // without work (fewer than 512 workgroups), 8: 333 x 776 with GELU takes 4 us
-// so, 29 in tiles of 64.
+// so, 29 in tiles of 64.  More than 2^28 rows have tiles of 512, for the grid's sake.
 
 template <bool MX>
 __device__ __forceinline__ void load_pre(const DzArgs &a, int64_t at, float (&v)[8])
@@ -244,7 +244,8 @@ hipError_t launch_f8_encode(int f8, const RowArgs8 &a, hipStream_t stream)
     const int64_t need = a.cols / 8;         // chunks of a row
 #define FQ_ENCODE_ROW(LANES, NCH)                                                                        \
     hipLaunchKernelGGL((k_encode_row<LANES, NCH>),                                                       \
-                       dim3((uint32_t)(LANES < 256 ? (a.rows + 256 / LANES - 1) / (256 / LANES) : a.rows)), \
+                       grid_of(LANES < 256 ? (a.rows + 256 / LANES - 1) / (256 / LANES) : a.rows,      \
+                               LANES < 256 ? 256 : LANES),                                              \
                        dim3(LANES < 256 ? 256 : LANES), 0, stream, a)
     if (need <= 16) FQ_ENCODE_ROW(16, 1);
     else if (need <= 64) FQ_ENCODE_ROW(64, 1);
@@ -268,6 +269,7 @@ hipError_t launch_f8_decode(int f8, const RowArgs8 &a, hipStream_t stream)
 
 int dz_tile(int64_t rows, int64_t n)
 {
+    if (rows > int64_t(1) << 28) return 512;
     return (rows + 63) / 64 * ((n + 255) / 256) >= 512 ? 64 : 8;
 }
 

@@ -10,8 +10,8 @@
 // global memory straight to LDS as they lie, 16 bytes a lane; the second kind
 // is transposed on the way into registers by gfx950's ds_read_b64_tr_b16: in a
 // group of 16 lanes, lane s reads four columns of row s / 4 and receives the
-// four rows of column s.  Those reads run at 128 B a clock and CU, ds_read_b128
-// at 256 (both measured), which is enough for either (below).
+// four rows of column s.  Those reads run at 124 B a clock and CU, ds_read_b128
+// at 240 (measured), which is enough for either (below).
 //
 // LDS tiles: contraction-contiguous, a 128-byte row (64 k) per tile row, 16-byte
 // chunks XORed with (row & 7) ^ (row >> 3 & 1); otherwise a row per k of all the
@@ -19,7 +19,7 @@
 // rows that a transposing read touches lie in different banks (no conflicts,
 // measured).
 //
-// Schedule: two stages of 64 k.  A substep of 16 k has its fragments in registers
+// Schedule: two stages of 64 k (more where a workgroup is alone on its CU).  A substep of 16 k has its fragments in registers
 // when it begins and reads the next one's between its products.  The stage's one
 // barrier lies in front of its last substep, whose fragments are in registers by
 // then: the other stage has landed, this one is free, and the loads that refill it
@@ -213,9 +213,9 @@ __device__ __forceinline__ void load_res(const ProductArgs &p, int64_t at, float
     if (p.y_f32) load8<false>((const float *)p.res + at, 8, r);
     else load8<false>((const uint16_t *)p.res + at, 8, r);
 }
-// STREAM: past the L2s where the output would fill them (4 MB each), whose lines the operands' tiles
-// need (8192 x 5760 -> 2880 222 -> 211 us, dw 2880 x 5760 264 -> 247, of 32 experts
-// 402 -> 320; a gated block's h and codes gain nothing).
+// STREAM: past the L2s where the output would fill them (4 MB each), whose lines the
+// operands' tiles need (8192 x 5760 -> 2880 222 -> 211 us, dw 2880 x 5760 264 -> 247, of
+// 32 experts 402 -> 325; a gated block's h and codes gain nothing).
 template <bool STREAM = false>
 __device__ __forceinline__ void store_y(const ProductArgs &p, int64_t at, const float (&v)[8])
 {
@@ -559,7 +559,7 @@ template <typename S>
 __global__ __launch_bounds__(S::kThreads, 1) void k_product(const ProductArgs p)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
-    S::run(p, lds, (int)blockIdx.x);
+    S::run(p, lds, workgroup());
 }
 // Two products in one launch: the second one's tiles fill the CUs that the first one's
 // last ones leave.
@@ -568,8 +568,9 @@ __global__ __launch_bounds__(S0::kThreads, 1) void k_product_pair(const ProductA
 {
     static_assert(S0::kThreads == S1::kThreads, "one size of workgroups");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S0::kLds > S1::kLds ? S0::kLds : S1::kLds];
-    if ((int)blockIdx.x < n0) S0::run(p0, lds, (int)blockIdx.x);
-    else S1::run(p1, lds, (int)blockIdx.x - n0);
+    const int block = workgroup();
+    if (block < n0) S0::run(p0, lds, block);
+    else S1::run(p1, lds, block - n0);
 }
 
 // ---- launches ------------------------------------------------------------------------
@@ -623,14 +624,14 @@ ProductArgs shape_args(ProductArgs p)
 template <typename S>
 hipError_t launch_shape(const ProductArgs &p, hipStream_t stream)
 {
-    hipLaunchKernelGGL((k_product<S>), dim3((uint32_t)shape_grid<S>(p)), dim3(S::kThreads), 0, stream, shape_args<S>(p));
+    hipLaunchKernelGGL((k_product<S>), grid_of(shape_grid<S>(p), S::kThreads), dim3(S::kThreads), 0, stream, shape_args<S>(p));
     return hipGetLastError();
 }
 template <typename S0, typename S1>
 hipError_t launch_pair(const ProductArgs &p0, const ProductArgs &p1, hipStream_t stream)
 {
     const int64_t n0 = (shape_grid<S0>(p0) + kXcds - 1) / kXcds * kXcds;       // the second one's XCDs stay in step
-    hipLaunchKernelGGL((k_product_pair<S0, S1>), dim3((uint32_t)(n0 + shape_grid<S1>(p1))), dim3(S0::kThreads), 0,
+    hipLaunchKernelGGL((k_product_pair<S0, S1>), grid_of(n0 + shape_grid<S1>(p1), S0::kThreads), dim3(S0::kThreads), 0,
                        stream, shape_args<S0>(p0), shape_args<S1>(p1), (int)n0);
     return hipGetLastError();
 }

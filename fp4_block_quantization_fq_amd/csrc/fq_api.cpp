@@ -1630,15 +1630,17 @@ size_t product_fwd_ws(const Product &d)
     return fwd_splits(d) > 1 ? split_bytes(d, d.rows, d.cols(), d.k) : 0;
 }
 
-// Workspace of a backward: dz, x decoded, the tiles' column sums, the parts of a
-// split dx and of a split dw.
+// Workspace of a backward: dz, dz with the row scales' mantissas, x decoded, the tiles'
+// column sums, the parts of a split dx and of a split dw.
 struct ProductBwdLayout {
-    size_t x, partials, dx_parts, dw_parts, total;
+    size_t scaled, x, partials, dx_parts, dw_parts, total;
 };
 ProductBwdLayout product_bwd_layout(const Product &d, int32_t x_f8)
 {
     ProductBwdLayout l;
-    l.x = round256((size_t)d.rows * d.cols() * 2);
+    const size_t dz = round256((size_t)d.rows * d.cols() * 2);
+    l.scaled = dz;
+    l.x = l.scaled + (x_f8 == FQ_F8_ROW ? dz : 0);
     l.partials = l.x + (x_f8 != FQ_F8_NONE ? round256((size_t)d.rows * d.k * 2) : 0);
     l.dx_parts = l.partials +
                  round256((size_t)fqimpl::dz_tiles(d.rows, d.n, d.experts) * d.cols() * sizeof(float));
@@ -1742,6 +1744,8 @@ fq_status product_bwd(const Product &d, const ProductBwd &a)
 
     uint8_t *ws = (uint8_t *)a.ws;
     const void *dz = plain ? a.dy : a.ws;
+    // x's row scales go into dz where that is rounded anyway
+    const bool scaled = x8 && a.dw && !plain && a.x_f8 == FQ_F8_ROW;
     if (!plain || a.dbias) {
         fqimpl::DzArgs z = {};
         z.glu = glu;
@@ -1754,7 +1758,9 @@ fq_status product_bwd(const Product &d, const ProductBwd &a)
         z.n = d.n;
         z.experts = (int)d.experts;
         z.offsets = a.offsets;
-        z.dz = ws;
+        z.dz = a.dx || (a.dw && !scaled) ? ws : nullptr;
+        z.dz_scaled = scaled ? ws + l.scaled : nullptr;
+        z.row_scales = (const float *)a.x_scales;
         z.h = a.h;
         z.partials = a.dbias ? (float *)(ws + l.partials) : nullptr;
         z.dbias = a.dbias;
@@ -1783,12 +1789,13 @@ fq_status product_bwd(const Product &d, const ProductBwd &a)
             r.y = ws + l.x;
             r.rows = d.rows;
             r.cols = d.k;
+            r.power = scaled;
             const hipError_t e = fqimpl::launch_f8_decode(a.x_f8, r, a.stream);
             if (e != hipSuccess) return device_status(e, "decode launch");
             x = r.y;
         }
         dw.a = (const uint16_t *)x;
-        dw.b = (const uint16_t *)dz;
+        dw.b = scaled ? (const uint16_t *)(ws + l.scaled) : (const uint16_t *)dz;
         dw.lda = d.k;
         dw.ldb = d.cols();
         dw.M = (int)d.k;

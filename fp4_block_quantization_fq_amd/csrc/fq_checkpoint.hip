@@ -92,8 +92,9 @@ __global__ __launch_bounds__(kBlock) void k_decode(RowArgs8 a, int64_t chunks)
     const uint32_t per_row = (uint32_t)(a.cols / 8);
     for (int64_t c = (int64_t)blockIdx.x * kBlock + threadIdx.x; c < chunks; c += step) {
         const u32w2 codes = NT ? __builtin_nontemporal_load((const u32w2 *)a.codes + c) : ((const u32w2 *)a.codes)[c];
-        const float s = ROW ? ((const float *)a.scales)[(uint32_t)c / per_row]      // chunks are below 2^31
-                            : mx8_scale(((const uint8_t *)a.scales)[c >> 2]);
+        float s = ROW ? ((const float *)a.scales)[(uint32_t)c / per_row]            // chunks are below 2^31
+                      : mx8_scale(((const uint8_t *)a.scales)[c >> 2]);
+        if (ROW && a.power) s = as_f(as_u(s) & 0xFF800000u);                        // scales are normal or NaN
         float v[8];
         e4m3_decode8(codes, v);
 #pragma unroll
@@ -121,6 +122,19 @@ __device__ __forceinline__ void load_pre(const DzArgs &a, int64_t at, float (&v)
     for (int e = 0; e < 8; ++e) v[e] *= s;
 }
 
+// Eight values of dz.  Where x comes with a scale per row, dw = x^T dz takes the codes
+// times the scale's power of two, which BF16 holds exactly, and the scale's mantissa
+// here: one rounding to BF16 (0.0017 of dw in the mean) instead of x's and dz's (0.0024).
+__device__ __forceinline__ void store_dz(const DzArgs &a, int64_t at, float mantissa, const float (&v)[8])
+{
+    if (a.dz) store8<false>((uint16_t *)a.dz + at, 8, v);
+    if (!a.dz_scaled) return;
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = v[e] * mantissa;
+    store8<false>((uint16_t *)a.dz_scaled + at, 8, t);
+}
+
 // GLU: two halves of pre and dz; else pre may be missing (no activation), then
 // only the column sums are made.
 template <bool GLU, bool MX>
@@ -144,12 +158,13 @@ __global__ __launch_bounds__(kBlock) void k_dz(DzArgs a)
             float d[8], g[8], u[8];
             load8<false>((const uint16_t *)a.dy + r * a.n + col, 8, d);
             const int64_t at = r * cols + col;
+            const float mantissa = a.dz_scaled ? as_f((as_u(a.row_scales[r]) & 0x7FFFFFu) | 0x3F800000u) : 1.0f;
             if (GLU) {
                 load_pre<MX>(a, at, g);
                 load_pre<MX>(a, at + a.n, u);
                 glu8_grad(a.gate, g, u, d);
-                store8<false>((uint16_t *)a.dz + at, 8, g);
-                store8<false>((uint16_t *)a.dz + at + a.n, 8, u);
+                store_dz(a, at, mantissa, g);
+                store_dz(a, at + a.n, mantissa, u);
                 if (a.h) store8<false>((uint16_t *)a.h + r * a.n + col, 8, d);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -160,7 +175,7 @@ __global__ __launch_bounds__(kBlock) void k_dz(DzArgs a)
                 if (a.pre) {
                     load_pre<MX>(a, at, g);
                     act8_grad(a.gate.act, g, d);
-                    store8<false>((uint16_t *)a.dz + at, 8, d);
+                    store_dz(a, at, mantissa, d);
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s0[e] += d[e];

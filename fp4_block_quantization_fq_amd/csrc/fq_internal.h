@@ -292,6 +292,7 @@ struct RowArgs8 {
     void *codes, *scales;
     void *y;                 // decode: BF16
     int64_t rows, cols;
+    int power;               // decode: under the scales' powers of two alone (F8_ROW)
 };
 hipError_t launch_f8_encode(int f8, const RowArgs8 &a, hipStream_t stream);
 hipError_t launch_f8_decode(int f8, const RowArgs8 &a, hipStream_t stream);
@@ -305,7 +306,9 @@ struct DzArgs {
     int64_t rows, n;
     int experts;
     const int32_t *offsets;
-    void *dz;                // BF16, of pre's shape
+    void *dz;                // BF16, of pre's shape, or null
+    void *dz_scaled;         // the same times the mantissas of row_scales, or null
+    const float *row_scales;
     void *h;                 // BF16 [rows, n] or null
     float *partials;         // [dz_tiles, n or 2n], or null without dbias
     float *dbias;            // [experts, n or 2n] or null

@@ -161,16 +161,23 @@ __device__ __forceinline__ float mx8_scale(uint32_t code)
 }
 
 // ---- grids -----------------------------------------------------------------------------
-// `n` workgroups and one's number.  The threads along an axis of a grid have to stay
-// below 2^32, which the largest calls' workgroups are not; the last row of such a grid
-// has numbers from n on.
-inline dim3 grid_of(int64_t n, int threads)
+// `n` workgroups of THREADS and one's number.  The threads along an axis of a grid have
+// to stay below 2^32, which the largest calls' workgroups are not; the last row of such a
+// grid has numbers from n on.  A row is a constant: gridDim would have to be loaded (0.2
+// of 7 us in a call of one row).
+constexpr int grid_row(int threads) { return (1 << 30) / threads; }       // a multiple of the XCDs
+template <int THREADS>
+dim3 grid_of(int64_t n)
 {
-    const int64_t row = (int64_t(1) << 30) / threads;          // a multiple of the XCDs
+    constexpr int row = grid_row(THREADS);
     if (n <= row) return dim3((uint32_t)n);
     return dim3((uint32_t)row, (uint32_t)((n + row - 1) / row));
 }
-__device__ __forceinline__ int workgroup() { return (int)(blockIdx.y * gridDim.x + blockIdx.x); }
+template <int THREADS>
+__device__ __forceinline__ int workgroup()
+{
+    return (int)(blockIdx.y * grid_row(THREADS) + blockIdx.x);
+}
 
 // ---- the experts' segments of rows ---------------------------------------------------
 // offsets[e] .. offsets[e + 1], brought into 0 .. rows, so that no entry can lead

@@ -45,7 +45,7 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void k_encode_row(RowArg
     constexpr int THREADS = LANES < 256 ? 256 : LANES, WAVES = LANES / 64;
     __shared__ uint32_t tops[WAVES > 0 ? WAVES : 1];
     const int l = threadIdx.x % LANES;
-    const int64_t row = (int64_t)workgroup() * (THREADS / LANES) + threadIdx.x / LANES;
+    const int64_t row = (int64_t)workgroup<THREADS>() * (THREADS / LANES) + threadIdx.x / LANES;
     if (row >= a.rows) return;                   // of whole waves or workgroups, where those share rows
     const uint16_t *x = (const uint16_t *)a.x + row * a.cols;
     Raw8<uint16_t> raw[NCH];
@@ -259,8 +259,8 @@ hipError_t launch_f8_encode(int f8, const RowArgs8 &a, hipStream_t stream)
     const int64_t need = a.cols / 8;         // chunks of a row
 #define FQ_ENCODE_ROW(LANES, NCH)                                                                        \
     hipLaunchKernelGGL((k_encode_row<LANES, NCH>),                                                       \
-                       grid_of(LANES < 256 ? (a.rows + 256 / LANES - 1) / (256 / LANES) : a.rows,      \
-                               LANES < 256 ? 256 : LANES),                                              \
+                       grid_of<(LANES < 256 ? 256 : LANES)>(                                            \
+                           LANES < 256 ? (a.rows + 256 / LANES - 1) / (256 / LANES) : a.rows),          \
                        dim3(LANES < 256 ? 256 : LANES), 0, stream, a)
     if (need <= 16) FQ_ENCODE_ROW(16, 1);
     else if (need <= 64) FQ_ENCODE_ROW(64, 1);

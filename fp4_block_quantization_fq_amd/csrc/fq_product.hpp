@@ -559,7 +559,7 @@ template <typename S>
 __global__ __launch_bounds__(S::kThreads, 1) void k_product(const ProductArgs p)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
-    S::run(p, lds, workgroup());
+    S::run(p, lds, workgroup<S::kThreads>());
 }
 // Two products in one launch: the second one's tiles fill the CUs that the first one's
 // last ones leave.
@@ -568,7 +568,7 @@ __global__ __launch_bounds__(S0::kThreads, 1) void k_product_pair(const ProductA
 {
     static_assert(S0::kThreads == S1::kThreads, "one size of workgroups");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S0::kLds > S1::kLds ? S0::kLds : S1::kLds];
-    const int block = workgroup();
+    const int block = workgroup<S0::kThreads>();
     if (block < n0) S0::run(p0, lds, block);
     else S1::run(p1, lds, block - n0);
 }
@@ -624,14 +624,14 @@ ProductArgs shape_args(ProductArgs p)
 template <typename S>
 hipError_t launch_shape(const ProductArgs &p, hipStream_t stream)
 {
-    hipLaunchKernelGGL((k_product<S>), grid_of(shape_grid<S>(p), S::kThreads), dim3(S::kThreads), 0, stream, shape_args<S>(p));
+    hipLaunchKernelGGL((k_product<S>), grid_of<S::kThreads>(shape_grid<S>(p)), dim3(S::kThreads), 0, stream, shape_args<S>(p));
     return hipGetLastError();
 }
 template <typename S0, typename S1>
 hipError_t launch_pair(const ProductArgs &p0, const ProductArgs &p1, hipStream_t stream)
 {
     const int64_t n0 = (shape_grid<S0>(p0) + kXcds - 1) / kXcds * kXcds;       // the second one's XCDs stay in step
-    hipLaunchKernelGGL((k_product_pair<S0, S1>), grid_of(n0 + shape_grid<S1>(p1), S0::kThreads), dim3(S0::kThreads), 0,
+    hipLaunchKernelGGL((k_product_pair<S0, S1>), grid_of<S0::kThreads>(n0 + shape_grid<S1>(p1)), dim3(S0::kThreads), 0,
                        stream, shape_args<S0>(p0), shape_args<S1>(p1), (int)n0);
     return hipGetLastError();
 }

@@ -46,7 +46,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_product_few(const ProductArgs p)
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int tiles_n = (p.N + BNC - 1) / BNC;
     const int tiles_m = p.offsets ? segment_tiles(p.offsets, p.experts, p.rows, ROWS, lane) : (p.M + ROWS - 1) / ROWS;
-    const int total = tiles_m * tiles_n, b = workgroup();
+    const int total = tiles_m * tiles_n, b = workgroup<64 * WAVES>();
     if (b >= total) return;
     // neighbours in one XCD share lines of the weight's rows
     const int each = total / kXcds, rest = total % kXcds, xcd = b % kXcds;
@@ -193,7 +193,7 @@ template <int COLS, int RT, int WAVES, int DEPTH, int EPI>
 hipError_t launch_few(const ProductArgs &p, hipStream_t stream)
 {
     const int64_t tiles = product_tiles<false>(p, 16 * RT, COLS / (EPI == EPI_GLU ? 2 : 1));
-    hipLaunchKernelGGL((k_product_few<COLS, RT, WAVES, DEPTH, EPI>), grid_of(tiles, 64 * WAVES), dim3(64 * WAVES), 0, stream, p);
+    hipLaunchKernelGGL((k_product_few<COLS, RT, WAVES, DEPTH, EPI>), grid_of<64 * WAVES>(tiles), dim3(64 * WAVES), 0, stream, p);
     return hipGetLastError();
 }
 

@@ -159,6 +159,19 @@ __device__ __forceinline__ float mx8_scale(uint32_t code)
 {
     return code == 255u ? as_f(0x7FC00000u) : e8m0_value(code);
 }
+// An FP32 scale of a row (normal, or NaN) as a power of two and a mantissa.  Mantissas
+// are from 1/2 to 1, so that a finite gradient times one is finite in BF16.  From 2^100
+// on they are from 1 to 2: there twice the power could take a code's value out of range.
+__device__ __forceinline__ bool row_scale_large(float s) { return !(s < 0x1p100f); }
+__device__ __forceinline__ float row_scale_power(float s)
+{
+    const float p = as_f(as_u(s) & 0xFF800000u);
+    return row_scale_large(s) ? p : 2.0f * p;
+}
+__device__ __forceinline__ float row_scale_mantissa(float s)
+{
+    return as_f((as_u(s) & 0x7FFFFFu) | (row_scale_large(s) ? 0x3F800000u : 0x3F000000u));
+}
 
 // ---- grids -----------------------------------------------------------------------------
 // `n` workgroups of THREADS and one's number.  The threads along an axis of a grid have

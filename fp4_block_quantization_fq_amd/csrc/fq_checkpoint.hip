@@ -94,7 +94,7 @@ __global__ __launch_bounds__(kBlock) void k_decode(RowArgs8 a, int64_t chunks)
         const u32w2 codes = NT ? __builtin_nontemporal_load((const u32w2 *)a.codes + c) : ((const u32w2 *)a.codes)[c];
         float s = ROW ? ((const float *)a.scales)[(uint32_t)c / per_row]            // chunks are below 2^31
                       : mx8_scale(((const uint8_t *)a.scales)[c >> 2]);
-        if (ROW && a.power) s = as_f(as_u(s) & 0xFF800000u);                        // scales are normal or NaN
+        if (ROW && a.power) s = row_scale_power(s);
         float v[8];
         e4m3_decode8(codes, v);
 #pragma unroll
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(kBlock) void k_dz(DzArgs a)
             float d[8], g[8], u[8];
             load8<false>((const uint16_t *)a.dy + r * a.n + col, 8, d);
             const int64_t at = r * cols + col;
-            const float mantissa = a.dz_scaled ? as_f((as_u(a.row_scales[r]) & 0x7FFFFFu) | 0x3F800000u) : 1.0f;
+            const float mantissa = a.dz_scaled ? row_scale_mantissa(a.row_scales[r]) : 1.0f;
             if (GLU) {
                 load_pre<MX>(a, at, g);
                 load_pre<MX>(a, at + a.n, u);

@@ -617,8 +617,8 @@ fq_status fq_adamw_step_plan(const fq_adamw_hyper *hyper, const void *plan,
  * 8-bit rows (FQ_F8_MX or FQ_F8_ROW, as fq_rmsnorm_fwd or fq_f8_encode wrote them):
  * the values that codes and scales stand for.  FQ_F8_MX's are exact in BF16 (but below
  * its normal range).  FQ_F8_ROW's are rounded to it where dz is dy; else dw is made of
- * the codes times their scale's power of two and of d times its mantissa, that product
- * rounded to BF16. */
+ * the codes times a power of two of their scale and of d times its mantissa (at most 1
+ * for scales below 2^100), that product rounded to BF16. */
 enum { FQ_ACT_NONE = 0, FQ_ACT_RELU = 1, FQ_ACT_SILU = 2, FQ_ACT_GELU = 3 };
 
 /* 8-bit rows of x BF16 [rows, cols] and back: codes uint8 [rows, cols], scales as

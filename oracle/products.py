@@ -37,6 +37,43 @@ def act(z, kind, alpha=1.0):
     return z, torch.ones_like(z)
 
 
+def act_close(z, kind, alpha=1.0):
+    """(a(z), a'(z)) of SiLU or GELU and how far an FP32 evaluation of their formulas
+    may be from either, relative to what they are: the side that falls to 0 keeps its
+    precision.  In units of 2^-24, with exp2 and reciprocal to two of them:
+      * exp(-v): v, its product with log2 e and that constant are rounded, 2.23 |v|,
+        and 2; s = 1 / (1 + exp(-v)) takes the share 1 - s of that, and 3 more;
+      * a = z s one more; a' = s + v s (1 - s), where 1 - s has the absolute error of s
+        and a rounding, one product and one sum;
+      * the normal distribution's smaller side q = exp(-z^2 / 2) t P(t) / 2: 1.12 z^2 + 2
+        for the exponent; 3.8 for the polynomial's sums, 3 for t, which its slope makes at
+        most 10, 0.4 for the fit; 2 products.  The other side is 1 - q;
+      * a' = phi + z exp(-z^2 / 2) / sqrt(2 pi) from the same exponential.
+    Where a reciprocal or exp2 that a result depends on is below the normal range, it may
+    be lost whole (its border is moved by a factor of 2 for its own error); products below
+    that range are rounded to 2^-150."""
+    z = z.double()
+    if kind == SILU:
+        v = alpha * z
+        s, c = torch.sigmoid(v), torch.sigmoid(-v)
+        es = c * (2.3 * v.abs() + 2.1) + 3.1
+        value, slope = z * s, s + v * s * c
+        tv = (es + 1.1) * value.abs()
+        td = es * s + v.abs() * s * (c * (es + 3.1) + s * es) + slope.abs()
+        lost = torch.where(s < 2.0 ** -125, s, 0.0) * (1 + v.abs()) * (1 + z.abs())
+    else:
+        phi, q = (torch.special.erfc(side * z / math.sqrt(2)) / 2 for side in (-1, 1))
+        pdf = torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+        eq = 1.15 * z * z + 19.0
+        ephi = torch.where(z < 0, phi * eq, q * eq + 1.1)
+        value, slope = z * phi, phi + z * pdf
+        tv = z.abs() * ephi + 1.1 * value.abs()
+        td = ephi + z.abs() * pdf * (1.15 * z * z + 7.0) + slope.abs()
+        lost = torch.where(torch.exp(-0.5 * z * z) < 2.0 ** -125, q + z.abs() * pdf, 0.0) * (1 + z.abs())
+    lost = lost + 2.0 ** -148 * (1 + z.abs())
+    return value, slope, EPS32 * tv + lost, EPS32 * td + lost
+
+
 def gate(z, g):
     """(a(g'), a'(g') or 0, u' + shift, 1 or 0) of z = [g, u]; g = (act, alpha, limit, shift)."""
     kind, alpha, limit, shift = g

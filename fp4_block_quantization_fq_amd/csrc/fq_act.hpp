@@ -130,7 +130,10 @@ __device__ __forceinline__ void glu8_grad(const Gate &t, float (&g)[8], float (&
             const float up = (u[i] > t.limit ? t.limit : u[i] < -t.limit ? -t.limit : u[i]) + t.shift;
             float a;
             const float da = act_grad_of<decltype(kind)::value>(t.alpha, gate, &a);
-            g[i] = g_out ? 0.0f : dh[i] * up * da;
+            // dh up first, whose underflow is the result's; where it overflows, dh da first
+            float dg = dh[i] * up;
+            dg = __builtin_fabsf(dg) == __builtin_inff() ? dh[i] * da * up : dg * da;
+            g[i] = g_out ? 0.0f : dg;
             u[i] = u_out ? 0.0f : dh[i] * a;
             dh[i] = a * up;
         }

@@ -68,3 +68,19 @@ def test_rows_that_stand_for_nan():
     dx, dw, _ = fq.fq_linear_bwd(normal(1, rows, n), codes, normal(2, k, n), pre=normal(3, rows, n), act=op.SILU,
                                  x_f8=fq.FQ_F8_ROW, x_scales=scales)
     assert bool(dw.isnan().all()) and bool(dx.isfinite().all())
+
+
+@pytest.mark.parametrize("dh,u,g", [(2.5e38, 4.0, -9.0), (-2.5e38, 100.0, -12.0), (1e3, 1e36, -200.0), (3e-3, 3.3e38, 2.4), (2e-38, 1e6, -9.0)])
+@pytest.mark.parametrize("kind", [op.SILU, op.GELU])
+def test_gate_of_large_values(dh, u, g, kind):
+    """dh (u + shift) a'(g) is finite, dh (u + shift) may not be: dg from the bias gradient
+    of one row, to 2^-24 of three products and the slope's own bound."""
+    n = 32
+    h = torch.full((1, n), dh, dtype=torch.bfloat16, device=DEV)
+    pre = torch.cat([torch.full((1, n), v, dtype=torch.bfloat16, device=DEV) for v in (g, u)], 1)
+    x, w = torch.zeros((1, 8), dtype=torch.bfloat16, device=DEV), torch.zeros((8, 2 * n), dtype=torch.bfloat16, device=DEV)
+    _, _, dbias = fq.fq_glu_bwd(h, x, w, pre, act=kind, need_dx=False, need_dw=False)
+    value, slope, tv, td = op.act_close(pre[0, :n], kind)
+    up, d = pre[0, n:].double(), h[0].double()
+    for got, want, bound in ((dbias[:n], d * slope * up, td * (d * up).abs()), (dbias[n:], d * value, tv * d.abs())):
+        within(got, want, bound + 3 * op.EPS32 * want.abs() + 2.0 ** -140, "dbias")

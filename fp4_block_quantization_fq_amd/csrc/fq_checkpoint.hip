@@ -122,7 +122,11 @@ __device__ __forceinline__ void load_pre(const DzArgs &a, int64_t at, float (&v)
     for (int e = 0; e < 8; ++e) v[e] *= s;
 }
 
-// Eight values of dz.  Where x comes with a scale per row, dw = x^T dz takes the codes
+// Eight values of dz, rounded to BF16, which is what the matrix cores take: the products
+// of this backward are then off by 0.0023 of their norm with outputs in BF16, whose own
+// rounding is 0.0017 of it.  Two BF16 parts would hold 16 bits of dz and cost both products
+// again (450 of 530 us at 8192 x 2880 -> 2 x 2880).  Column sums take the FP32 values.
+// Where x comes with a scale per row, dw = x^T dz takes the codes
 // times the scale's power of two, which BF16 holds exactly, and the scale's mantissa
 // here: one rounding to BF16 (0.0017 of dw in the mean) instead of x's and dz's (0.0024).
 __device__ __forceinline__ void store_dz(const DzArgs &a, int64_t at, float mantissa, const float (&v)[8])
@@ -235,7 +239,13 @@ __global__ __launch_bounds__(kBlock) void k_dbias(DzArgs a, int64_t cols)
     }
 }
 
-// chunks from which a call streams: 192 MB of values and codes
+// Chunks from which a call streams: 192 MB of values and codes, of the 256 MB that the
+// memory-side cache holds.  What is better below depends on who uses the data next (widths
+// of 4096, plain / streamed, us).  Encoding and decoding again: 4096 rows 22 / 21, 8192 40 /
+// 38, 16384 75 / 70, 32768 142 / 134.  Encoding what was just made: 20 / 17, 42 / 36, 78 /
+// 70, 160 / 136.  Decoding for a pass over the values: 21 / 23, 39 / 42, 77 / 82, 157 / 157,
+// and in a product's backward 8192 x 2880 247 / 266, 16384 468 / 497, 32768 1021 / 1014.  So
+// smaller calls leave their values where a backward finds them.
 constexpr int64_t kStreamChunks = int64_t(1) << 23;
 
 uint32_t flat_grid(int64_t chunks)

@@ -279,7 +279,12 @@ int product_splits(int64_t M, int64_t columns, int64_t K);
 hipError_t launch_product_join(ProductArgs p, int epilogue, const float *part, hipStream_t stream);
 hipError_t launch_product_linear(ProductArgs p, hipStream_t stream);
 hipError_t launch_product_glu(ProductArgs p, hipStream_t stream);      // N of each half
-// Rows (of an expert, on average) up to which the weight's bytes bound a forward.
+// Rows (of an expert, on average) up to which a forward takes the few-rows kernel.  Without
+// experts (us, few rows / tiles): 2880 -> 2880 16 rows 6.0 / 12.3, 64 10.3 / 14.7, 96 13.3 /
+// 14.4; gated 11.4 / 15.1, 48 rows 15.8 / 16.0, 64 17.6 / 16.6, 96 32.7 / 16.0.  With experts
+// the tiles fill the chip, and it pays for small weights only: 4 experts of 2880 -> 2880, 16
+// rows each 19 / 32, 64 28 / 33; 8 experts 30 / 35 and 63 / 37; 32 experts 157 / 114 and 265
+// / 126, gated 390 / 188 and 665 / 244.
 inline bool product_few_rows(int64_t rows, int64_t experts) { return rows <= 64 * (experts ? experts : 1); }
 hipError_t launch_product_few_linear(const ProductArgs &p, hipStream_t stream);      // fq_product_few.hip
 hipError_t launch_product_few_glu(const ProductArgs &p, hipStream_t stream);

@@ -215,7 +215,10 @@ __device__ __forceinline__ void load_res(const ProductArgs &p, int64_t at, float
 }
 // STREAM: past the L2s where the output would fill them (4 MB each), whose lines the
 // operands' tiles need (8192 x 5760 -> 2880 222 -> 211 us, dw 2880 x 5760 264 -> 247, of
-// 32 experts 402 -> 325; a gated block's h and codes gain nothing).
+// 32 experts 402 -> 325; a gated block's h and codes gain nothing).  Smaller ones gain little
+// (1024 x 2880 -> 1440 18.0 and 17.7) and are left to the next kernel.  FP32 outputs are not
+// streamed: 8192 x 2880 -> 2880 with its residual 174 plain, 181 streamed, 4096 rows 93 and
+// 90, dw of 2880 x 2880 152 and 151, of 32 experts 270 and 269.
 template <bool STREAM = false>
 __device__ __forceinline__ void store_y(const ProductArgs &p, int64_t at, const float (&v)[8])
 {
@@ -589,7 +592,13 @@ int64_t product_tiles(const ProductArgs &p, int bm, int bn)
 
 // Time of a call in one shape of tiles, to compare the shapes: rounds of 256 CUs
 // times a round's, of `step` per 64 k and `fixed` around them (us, measured on
-// 8192 x 2880 and 2880 x 5760 outputs).
+// 8192 x 2880 and 2880 x 5760 outputs).  Segments are taken to end in the middle of a tile;
+// where they are shorter than a tile that counts too few.  32 even experts, 2880 -> 2880, us
+// in tiles of 128 x 128, 256 x 192, 256 x 256, the one taken last: dx of 512 rows 112, 126,
+// 138 (128 x 128), 1024 114, 128, 139 (256 x 256), 2048 118, 129, 140 (128 x 128), 4099 137,
+// 135, 142 (256 x 192), 8192 193, 163, 164 (256 x 192), 16384 334, 268, 256 (256 x 256);
+// forward of 4099 138, 139, 146 (256 x 192), 8192 194, 165, 166 (256 x 192), 16384 336, 280,
+// 258 (256 x 192).
 template <bool SEGK>
 float product_time(const ProductArgs &p, int bm, int bn, int per_cu, float step, float fixed)
 {

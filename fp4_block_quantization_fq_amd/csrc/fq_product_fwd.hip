@@ -36,8 +36,11 @@ hipError_t launch_product_glu(ProductArgs p, hipStream_t stream)
     if (few_rows(p)) return launch_product_few_glu(p, stream);
     if (p.splits > 1) return launch_split<ALONG, ACROSS, false>(p, 2 * p.N, EPI_GLU, stream);
     // Experts of few rows each are bound by their weights, which more and smaller
-    // workgroups read faster (4099 rows of 32 experts, 2880 -> 2 x 2880: 295 us
-    // against 340; 16384 rows: 795 against 704).
+    // workgroups read faster.  32 experts, 2880 -> 2 x 2880, us in tiles of 128 x 64 / 256 x
+    // 128, segments of even and of uneven lengths: 65 rows each 206 / 236 and 220 / 237, 96
+    // 221 / 241 and 266 / 255, 128 235 / 250 and 307 / 263, 160 330 / 276 and 336 / 320, 192
+    // 339 / 286 and 365 / 333, 256 382 / 305 and 455 / 404, 512 679 / 519 and 733 / 641.  The
+    // border is late for these: they cross between 96 and 160 rows.
     const bool short_segments = p.offsets && p.M < 192 * (int64_t)p.experts;
     const float big = product_time<false>(p, 256, 128, 1, 1.46f, 15.0f);
     const float small = product_time<false>(p, 128, 64, 2, p.offsets ? 1.13f : 0.90f, 10.0f);

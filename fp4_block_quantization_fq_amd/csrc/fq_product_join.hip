@@ -4,7 +4,7 @@
 //
 // Where a product has fewer tiles than the chip has room for, its time is the
 // latency of its steps: 128 x 2880 -> 2880 took 30 us on 23 workgroups, 15 with its
-// contraction in eight parts and this kernel.
+// contraction in four parts and this kernel.
 #include "fq_product.hpp"
 
 namespace {

@@ -125,7 +125,7 @@ __device__ __forceinline__ void load_pre(const DzArgs &a, int64_t at, float (&v)
 // Eight values of dz, rounded to BF16, which is what the matrix cores take: the products
 // of this backward are then off by 0.0023 of their norm with outputs in BF16, whose own
 // rounding is 0.0017 of it.  Two BF16 parts would hold 16 bits of dz and cost both products
-// again (450 of 530 us at 8192 x 2880 -> 2 x 2880).  Column sums take the FP32 values.
+// again (460 to 500 of 530 us at 8192 x 2880 -> 2 x 2880).  Column sums take the FP32 values.
 // Where x comes with a scale per row, dw = x^T dz takes the codes
 // times the scale's power of two, which BF16 holds exactly, and the scale's mantissa
 // here: one rounding to BF16 (0.0017 of dw in the mean) instead of x's and dz's (0.0024).
